@@ -39,6 +39,9 @@ EXPORTS = (
     "moe_event_destroy", "moe_event_record", "moe_event_elapsed_ms", "moe_stream_wait_event",
     "moe_last_error", "moe_version", "moe_vmm_granularity", "moe_vmm_create", "moe_vmm_map",
     "moe_vmm_unmap", "moe_vmm_release",
+    "moe_layer_norm", "moe_layer_norm_backward_workspace_size", "moe_layer_norm_backward",
+    "moe_combine_backward", "moe_permute_backward", "moe_route_backward",
+    "moe_grouped_swiglu_backward_workspace_size", "moe_grouped_swiglu_backward",
 )
 
 
@@ -64,6 +67,7 @@ def _load() -> ctypes.CDLL:
         raise ImportError(f"{LIB_PATH} is not built; run `python -m grouped_gemm_weights_amd.build`")
     lib = ctypes.CDLL(LIB_PATH)
     P, I, I64, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+    F = ctypes.c_float
     PSZ = ctypes.POINTER(ctypes.c_size_t)
     sig = {
         "moe_route": [P, I, I, I, P, P, P, P],
@@ -93,6 +97,15 @@ def _load() -> ctypes.CDLL:
         "moe_vmm_map": [I, ctypes.POINTER(ctypes.c_void_p), PSZ, I, ctypes.POINTER(ctypes.c_void_p)],
         "moe_vmm_unmap": [P, PSZ, I],
         "moe_vmm_release": [P],
+        "moe_layer_norm": [P, P, P, I, I, F, I, P, P, P, P],
+        "moe_layer_norm_backward_workspace_size": [I, I, PSZ],
+        "moe_layer_norm_backward": [P, P, P, P, P, I, I, I, P, P, P, P, SZ, P],
+        "moe_combine_backward": [P, I, P, P, P, I, I, I, I, P, P, P],
+        "moe_permute_backward": [P, P, I, I, I, I, P, P],
+        "moe_route_backward": [P, P, P, I, I, I, P, P, P],
+        "moe_grouped_swiglu_backward_workspace_size": [I, I, I, I, I, PSZ],
+        "moe_grouped_swiglu_backward": [P, P, P, I, I, I, I, I, ctypes.POINTER(MoeWbuf), P, SZ, P, P,
+                                        P, P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -241,6 +254,60 @@ def moe_grouped_swiglu_combine(x, src_of, topk_w, T, k, offsets, E, H, I, dtype,
 def moe_combine(y_perm, row_of, topk_w, T, k, H, y, stream=None):
     _check("moe_combine", lib.moe_combine(ptr(y_perm), ptr(row_of), ptr(topk_w), T, k, H, ptr(y),
                                           stream_handle(stream)))
+
+
+def moe_layer_norm(x, gamma, beta, T, H, eps, dtype, y, mean=None, rstd=None, stream=None):
+    _check("moe_layer_norm", lib.moe_layer_norm(ptr(x), ptr(gamma), ptr(beta), T, H, eps, dtype, ptr(y),
+                                                ptr(mean), ptr(rstd), stream_handle(stream)))
+
+
+def moe_layer_norm_backward_workspace_size(T, H) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_layer_norm_backward_workspace_size",
+           lib.moe_layer_norm_backward_workspace_size(T, H, ctypes.byref(n)))
+    return n.value
+
+
+def moe_layer_norm_backward(dy, x, gamma, mean, rstd, T, H, dtype, dx, dgamma, dbeta, ws, ws_bytes,
+                            stream=None):
+    _check("moe_layer_norm_backward",
+           lib.moe_layer_norm_backward(ptr(dy), ptr(x), ptr(gamma), ptr(mean), ptr(rstd), T, H, dtype,
+                                       ptr(dx), ptr(dgamma), ptr(dbeta), ptr(ws), ws_bytes,
+                                       stream_handle(stream)))
+
+
+def moe_combine_backward(dy, dy_dtype, y_perm, row_of, topk_w, T, k, H, dtype, dy_perm, dtopk_w=None,
+                         stream=None):
+    _check("moe_combine_backward",
+           lib.moe_combine_backward(ptr(dy), dy_dtype, ptr(y_perm), ptr(row_of), ptr(topk_w), T, k, H,
+                                    dtype, ptr(dy_perm), ptr(dtopk_w), stream_handle(stream)))
+
+
+def moe_permute_backward(dx_perm, row_of, T, k, H, dtype, dx, stream=None):
+    _check("moe_permute_backward",
+           lib.moe_permute_backward(ptr(dx_perm), ptr(row_of), T, k, H, dtype, ptr(dx),
+                                    stream_handle(stream)))
+
+
+def moe_route_backward(topk_idx, topk_w, dtopk_w, T, E, k, dlogits, status=None, stream=None):
+    _check("moe_route_backward",
+           lib.moe_route_backward(ptr(topk_idx), ptr(topk_w), ptr(dtopk_w), T, E, k, ptr(dlogits),
+                                  ptr(status), stream_handle(stream)))
+
+
+def moe_grouped_swiglu_backward_workspace_size(R, E, H, I, dtype) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_grouped_swiglu_backward_workspace_size",
+           lib.moe_grouped_swiglu_backward_workspace_size(R, E, H, I, dtype, ctypes.byref(n)))
+    return n.value
+
+
+def moe_grouped_swiglu_backward(x_perm, dy_perm, offsets, R, E, H, I, dtype, w: MoeWbuf, ws, ws_bytes,
+                                dx_perm, dw, status=None, stream=None):
+    _check("moe_grouped_swiglu_backward",
+           lib.moe_grouped_swiglu_backward(ptr(x_perm), ptr(dy_perm), ptr(offsets), R, E, H, I, dtype,
+                                           ctypes.byref(w), ptr(ws), ws_bytes, ptr(dx_perm), ptr(dw),
+                                           ptr(status), stream_handle(stream)))
 
 
 def moe_dense_gemm(x, w, M, N, K, out, stream=None):

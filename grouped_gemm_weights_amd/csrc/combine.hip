@@ -1,12 +1,12 @@
-// moe_combine: weighted un-permute of the expert outputs, and the residual
-// add used between pipeline layers.
+// moe_combine: weighted un-permute of the expert outputs, its gradient
+// (moe_combine_backward), and the residual add used between pipeline layers.
 //
 // One 256-thread block per token: the k routing weights and row indices are
 // read once, then each thread sweeps float4 columns of the k expert rows
 // (k independent 16-byte loads in flight per step) and accumulates in j order
 // with fused multiply-adds.  Every y_perm row is read exactly once, so its loads
 // are non-temporal (9 % faster on prefill-sized layers than cached loads).
-#include "common.h"
+#include "rows.h"
 
 namespace moe {
 namespace {
@@ -62,6 +62,74 @@ __global__ __launch_bounds__(256) void residual_kernel(const uint16_t* x, const 
     out[i] = f32_to_bf16(bf16_to_f32(x[i]) + y[i]);
 }
 
+// Gradient of y[t] = sum_j w[t][j] y_perm[row_of[t k + j]]:
+//   dy_perm[row] = w[t][j] dy[t],   dw[t][j] = <dy[t], y_perm[row]>.
+// Bound by HBM: y_perm is read once (4 R H bytes) and dy_perm written once, so both bypass the
+// caches; dy[t] stays in registers for the token's k rows.  One block per token; a wave's share
+// of a dot product goes to its own LDS slot, so the k sums cost one barrier, and the slots are
+// added in wave order (the same bits every run).
+constexpr int kCbVecs = 4;  // vectors of 8 columns a thread holds: 8192 columns per sweep
+
+template <typename D, typename O>
+__global__ __launch_bounds__(256) void combine_backward_kernel(
+    const D* __restrict__ dy, const float* __restrict__ y_perm, const int32_t* __restrict__ row_of,
+    const float* __restrict__ topk_w, int T, int k, int H, O* __restrict__ dy_perm,
+    float* __restrict__ dtopk_w) {
+  __shared__ float dot[MOE_MAX_K][4];
+  const int t = blockIdx.x;
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  const int64_t R = static_cast<int64_t>(T) * k;
+  const D* dr = dy + static_cast<int64_t>(t) * H;
+  for (int c0 = 0; c0 == 0 || c0 * kVec < H; c0 += kCbVecs * 256) {
+    float d[kCbVecs][kVec];
+#pragma unroll
+    for (int i = 0; i < kCbVecs; ++i) load8<true>(dr, c0 + threadIdx.x + i * 256, H, d[i]);
+    for (int j = 0; j < k; ++j) {
+      const int r = row_of[static_cast<int64_t>(t) * k + j];
+      // an unwritten row index (after an out-of-range expert id) must not fault
+      const bool ok = r >= 0 && r < R;
+      const float w = topk_w[static_cast<int64_t>(t) * k + j];
+      float s = 0.f;
+      if (ok) {
+        O* out = dy_perm + static_cast<int64_t>(r) * H;
+        const float* yr = y_perm + static_cast<int64_t>(r) * H;
+#pragma unroll
+        for (int i = 0; i < kCbVecs; ++i) {
+          const int at = c0 + threadIdx.x + i * 256;
+          float v[kVec];
+          if (dtopk_w) {
+            load8<true>(yr, at, H, v);
+#pragma unroll
+            for (int q = 0; q < kVec; ++q) s = fmaf(d[i][q], v[q], s);
+          }
+#pragma unroll
+          for (int q = 0; q < kVec; ++q) v[q] = w * d[i][q];
+          store8<true>(out, at, H, v);
+        }
+      }
+      if (dtopk_w) {
+        s = wave_sum(s);
+        if (lane == 0) dot[j][wave] = c0 ? dot[j][wave] + s : s;
+      }
+    }
+  }
+  if (dtopk_w) {
+    __syncthreads();
+    const int j = threadIdx.x;
+    if (j < k)
+      dtopk_w[static_cast<int64_t>(t) * k + j] = (dot[j][0] + dot[j][1]) + (dot[j][2] + dot[j][3]);
+  }
+}
+
+template <typename D, typename O>
+void launch_combine_backward(const void* dy, const float* y_perm, const int32_t* row_of,
+                             const float* topk_w, int T, int k, int H, void* dy_perm, float* dtopk_w,
+                             hipStream_t s) {
+  hipLaunchKernelGGL((combine_backward_kernel<D, O>), dim3(T), dim3(256), 0, s,
+                     static_cast<const D*>(dy), y_perm, row_of, topk_w, T, k, H,
+                     static_cast<O*>(dy_perm), dtopk_w);
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -80,6 +148,34 @@ extern "C" int moe_combine(const float* y_perm, const int32_t* row_of, const flo
     hipLaunchKernelGGL(combine_kernel<false>, dim3(T), dim3(256), 0, s, y_perm, row_of, topk_w, T, k, H, y);
   MOE_LAUNCH_CHECK("moe_combine: launch");
   return debug_check(MOE_OK, "moe_combine", s, nullptr);
+}
+
+extern "C" int moe_combine_backward(const void* dy, moe_dtype dy_dtype, const float* y_perm,
+                                    const int32_t* row_of, const float* topk_w, int T, int k, int H,
+                                    moe_dtype dtype, void* dy_perm, float* dtopk_w,
+                                    moe_stream_t stream) {
+  using namespace moe;
+  if (T < 0 || k < 1 || H < 1 || (dy_dtype != MOE_F32 && dy_dtype != MOE_BF16) ||
+      (dtype != MOE_F32 && dtype != MOE_BF16))
+    return fail(MOE_ERR_ARG, "moe_combine_backward: bad sizes T=%d k=%d H=%d or dtype", T, k, H);
+  if (k > MOE_MAX_K)
+    return fail(MOE_ERR_UNSUPPORTED, "moe_combine_backward: k=%d above %d", k, MOE_MAX_K);
+  if (static_cast<int64_t>(T) * k > INT32_MAX || H > kMaxRow)
+    return fail(MOE_ERR_UNSUPPORTED, "moe_combine_backward: T*k or H=%d too large", H);
+  if (T == 0) return MOE_OK;
+  if (!dy || !row_of || !topk_w || !dy_perm || (dtopk_w && !y_perm))
+    return fail(MOE_ERR_ARG, "moe_combine_backward: null pointer");
+  hipStream_t s = as_stream(stream);
+  if (dy_dtype == MOE_F32 && dtype == MOE_F32)
+    launch_combine_backward<float, float>(dy, y_perm, row_of, topk_w, T, k, H, dy_perm, dtopk_w, s);
+  else if (dy_dtype == MOE_F32)
+    launch_combine_backward<float, uint16_t>(dy, y_perm, row_of, topk_w, T, k, H, dy_perm, dtopk_w, s);
+  else if (dtype == MOE_F32)
+    launch_combine_backward<uint16_t, float>(dy, y_perm, row_of, topk_w, T, k, H, dy_perm, dtopk_w, s);
+  else
+    launch_combine_backward<uint16_t, uint16_t>(dy, y_perm, row_of, topk_w, T, k, H, dy_perm, dtopk_w, s);
+  MOE_LAUNCH_CHECK("moe_combine_backward: launch");
+  return debug_check(MOE_OK, "moe_combine_backward", s, nullptr);
 }
 
 extern "C" int moe_residual_add(const void* x, const float* y, int64_t n, void* out,

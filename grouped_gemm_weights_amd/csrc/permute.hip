@@ -14,9 +14,11 @@
 //              the running position across batches.  No atomics decide an
 //              order, so the permutation is the stable counting sort.
 //  4. gather:  x_perm[r] = x[src_of[r] / k] with 16-byte vector copies.
+//
+// moe_permute_backward: the gradient of the gather, a sum over each token's k rows.
 #include <mutex>
 
-#include "common.h"
+#include "rows.h"
 
 namespace moe {
 namespace {
@@ -221,6 +223,45 @@ __global__ __launch_bounds__(256) void gather_kernel(const char* __restrict__ x,
   }
 }
 
+// Gradient of x_perm[row_of[t k + j]] = x[t]:  dx[t] = sum_j dx_perm[row_of[t k + j]], summed in
+// j order in fp32 and rounded once.  Bound by HBM: R H elements are read once (non-temporal) and
+// T H written.  One wave per 512 columns of a token, up to 8 rows' loads in flight per lane.
+constexpr int kPbRows = 8;
+
+template <typename E>
+__global__ __launch_bounds__(256) void permute_backward_kernel(const E* __restrict__ dx_perm,
+                                                               const int32_t* __restrict__ row_of,
+                                                               int T, int k, int H, int chunks,
+                                                               E* __restrict__ dx) {
+  const int64_t job = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / kWave;
+  const int t = static_cast<int>(job / chunks);
+  if (t >= T) return;
+  const int at = static_cast<int>(job % chunks) * kWave + (threadIdx.x & (kWave - 1));
+  const int64_t R = static_cast<int64_t>(T) * k;
+  float acc[kVec];
+#pragma unroll
+  for (int q = 0; q < kVec; ++q) acc[q] = 0.f;
+  for (int j0 = 0; j0 < k; j0 += kPbRows) {
+    float v[kPbRows][kVec];
+#pragma unroll
+    for (int j = 0; j < kPbRows; ++j) {
+      const int r = j0 + j < k ? row_of[static_cast<int64_t>(t) * k + j0 + j] : -1;
+      // an unwritten row index (after an out-of-range expert id) must not fault: it adds nothing
+      if (r >= 0 && r < R) {
+        load8<true>(dx_perm + static_cast<int64_t>(r) * H, at, H, v[j]);
+      } else {
+#pragma unroll
+        for (int q = 0; q < kVec; ++q) v[j][q] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kPbRows; ++j)
+#pragma unroll
+      for (int q = 0; q < kVec; ++q) acc[q] += v[j][q];
+  }
+  store8<true>(dx + static_cast<int64_t>(t) * H, at, H, acc);
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -343,4 +384,29 @@ extern "C" int moe_permute_noalloc(const int32_t* topk_idx, int T, int E, int k,
                                offsets, row_of, src_of, x_perm, scratch, kPermuteScratchBytes,
                                status, stream);
   return debug_check(rc2, "moe_permute_noalloc", as_stream(stream), status);
+}
+
+extern "C" int moe_permute_backward(const void* dx_perm, const int32_t* row_of, int T, int k, int H,
+                                    moe_dtype dtype, void* dx, moe_stream_t stream) {
+  using namespace moe;
+  if (T < 0 || k < 1 || H < 1 || (dtype != MOE_F32 && dtype != MOE_BF16))
+    return fail(MOE_ERR_ARG, "moe_permute_backward: bad sizes T=%d k=%d H=%d or dtype", T, k, H);
+  const int chunks = ceil_div(H, kWave * kVec);
+  const int64_t blocks = ceil_div64(static_cast<int64_t>(T) * chunks, 4);
+  if (static_cast<int64_t>(T) * k > INT32_MAX || H > kMaxRow || blocks > INT32_MAX)
+    return fail(MOE_ERR_UNSUPPORTED, "moe_permute_backward: T=%d k=%d H=%d too large", T, k, H);
+  if (T == 0) return MOE_OK;
+  if (!dx_perm || !row_of || !dx) return fail(MOE_ERR_ARG, "moe_permute_backward: null pointer");
+  hipStream_t s = as_stream(stream);
+  const dim3 grid(static_cast<unsigned>(blocks));
+  if (dtype == MOE_F32)
+    hipLaunchKernelGGL(permute_backward_kernel<float>, grid, dim3(256), 0, s,
+                       static_cast<const float*>(dx_perm), row_of, T, k, H, chunks,
+                       static_cast<float*>(dx));
+  else
+    hipLaunchKernelGGL(permute_backward_kernel<uint16_t>, grid, dim3(256), 0, s,
+                       static_cast<const uint16_t*>(dx_perm), row_of, T, k, H, chunks,
+                       static_cast<uint16_t*>(dx));
+  MOE_LAUNCH_CHECK("moe_permute_backward: launch");
+  return debug_check(MOE_OK, "moe_permute_backward", s, nullptr);
 }

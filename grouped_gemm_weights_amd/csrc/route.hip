@@ -6,6 +6,8 @@
 // (logit descending, expert id ascending); comparisons are exact fp32, so the
 // selection is deterministic and +0 / -0 tie.  Lane j keeps the j-th choice and
 // the weights exp(l_j - l_0) / sum_i exp(l_i - l_0) are formed in fp32.
+//
+// moe_route_backward: the gradient of those weights with respect to the logits.
 #include "common.h"
 
 namespace moe {
@@ -92,6 +94,54 @@ void launch_route(const float* logits, int T, int E, int k, int32_t* idx, float*
                      T, E, k, idx, w, status);
 }
 
+// Gradient of w = softmax over the chosen k logits:  dl_j = w_j (dw_j - sum_i w_i dw_i) at the
+// chosen ids, zero at the other E - k.  Bound by writing the dense row (4 E bytes a token).  One
+// wave per token: lane j holds slot j, the row is built in the wave's own LDS and leaves in wide
+// stores.  An id that a token lists twice gets the sum of its slots, added in slot order.
+__global__ __launch_bounds__(kRouteWaves * kWave) void route_backward_kernel(
+    const int32_t* __restrict__ topk_idx, const float* __restrict__ topk_w,
+    const float* __restrict__ dtopk_w, int T, int E, int k, float* __restrict__ dlogits,
+    int32_t* status) {
+  extern __shared__ float rows[];
+  const int lane = threadIdx.x & (kWave - 1);
+  const int t = blockIdx.x * kRouteWaves + (threadIdx.x / kWave);
+  if (t >= T) return;
+  float* row = rows + (threadIdx.x / kWave) * static_cast<int64_t>(E);
+  int id = -1;
+  float w = 0.f, dw = 0.f;
+  if (lane < k) {
+    const int64_t a = static_cast<int64_t>(t) * k + lane;
+    id = topk_idx[a];
+    w = topk_w[a];
+    dw = dtopk_w[a];
+    if (id < 0 || id >= E) {
+      status_or(status, MOE_STATUS_BAD_EXPERT_ID);
+      id = -1;
+    }
+  }
+  float s = w * dw;
+#pragma unroll
+  for (int off = kWave / 2; off >= 1; off >>= 1) s += __shfl_xor(s, off);
+  const float mine = w * (dw - s);
+  // the first slot of an id adds up the slots that share it
+  float g = 0.f;
+  bool first = id >= 0;
+  for (int j = 0; j < k; ++j) {
+    const int oid = __shfl(id, j);
+    const float og = __shfl(mine, j);
+    if (oid == id) {
+      g += og;
+      if (j < lane) first = false;
+    }
+  }
+  for (int e = lane; e < E; e += kWave) row[e] = 0.f;
+  __builtin_amdgcn_wave_barrier();
+  if (first) row[id] = g;
+  __builtin_amdgcn_wave_barrier();
+  float* out = dlogits + static_cast<int64_t>(t) * E;
+  for (int e = lane; e < E; e += kWave) out[e] = row[e];
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -112,4 +162,23 @@ extern "C" int moe_route(const float* logits, int T, int E, int k, int32_t* topk
   else launch_route<16>(logits, T, E, k, topk_idx, topk_w, status, s);
   MOE_LAUNCH_CHECK("moe_route: launch");
   return debug_check(MOE_OK, "moe_route", s, status);
+}
+
+extern "C" int moe_route_backward(const int32_t* topk_idx, const float* topk_w, const float* dtopk_w,
+                                  int T, int E, int k, float* dlogits, int32_t* status,
+                                  moe_stream_t stream) {
+  using namespace moe;
+  if (T < 0 || E < 1 || k < 1 || k > E)
+    return fail(MOE_ERR_ARG, "moe_route_backward: bad sizes T=%d E=%d k=%d", T, E, k);
+  if (E > MOE_MAX_E || k > MOE_MAX_K)
+    return fail(MOE_ERR_UNSUPPORTED, "moe_route_backward: E=%d or k=%d above the limits", E, k);
+  if (T == 0) return MOE_OK;
+  if (!topk_idx || !topk_w || !dtopk_w || !dlogits)
+    return fail(MOE_ERR_ARG, "moe_route_backward: null pointer");
+  hipStream_t s = as_stream(stream);
+  hipLaunchKernelGGL(route_backward_kernel, dim3(ceil_div(T, kRouteWaves)), dim3(kRouteWaves * kWave),
+                     kRouteWaves * E * sizeof(float), s, topk_idx, topk_w, dtopk_w, T, E, k, dlogits,
+                     status);
+  MOE_LAUNCH_CHECK("moe_route_backward: launch");
+  return debug_check(MOE_OK, "moe_route_backward", s, status);
 }

@@ -1,4 +1,5 @@
-"""Host orchestration of the MoE layer forward on one GPU, through the C ABI.
+"""Host orchestration of the MoE layer on one GPU, through the C ABI: the forward step and, for a
+layer built with ``training=True``, its backward pass.
 
 ``MoELayer`` owns the device buffers of one layer (PyTorch is used only to
 allocate device memory and to provide streams) and issues the library calls
@@ -13,6 +14,14 @@ of one forward step:
 This is the layer step of the DWDP explainer's prefetch-schedule panel with
 the merged buffer of its contiguous-buffer panel; the peers' share of the
 experts is a separate device pool (or pinned host memory) on this GPU.
+
+``pre_norm=True`` puts a layer norm in front of the router and the experts.
+The backward pass runs on the compute stream, on the buffers of the step it
+follows:
+
+    moe_combine_backward -> moe_route_backward -> moe_grouped_swiglu_backward
+    -> moe_permute_backward (-> moe_layer_norm_backward)
+
 Every step of the arithmetic runs in the library's HIP kernels.
 """
 from __future__ import annotations
@@ -46,13 +55,20 @@ class MoELayer:
                  n_halves: int = 2, compute_stream=None, copy_stream=None,
                  copy_mode: int = B.MOE_COPY_KERNEL, stitched: bool = False,
                  allocate_halves: bool = True, fused_gather: bool = False,
-                 combine_in_epilogue: bool = False):
+                 combine_in_epilogue: bool = False, pre_norm: bool = False, eps: float = 1e-5,
+                 training: bool = False):
         """stitched: each half is one virtual range over [the local-expert block | the half's own
         block], so merging the local experts copies nothing (page stitching, moe_vmm_*).
         allocate_halves=False leaves the halves to the caller (the pipeline builds per-layer ranges).
         fused_gather: the grouped GEMM reads its rows from x through src_of, and x_perm is not built.
         combine_in_epilogue: the down GEMM adds its w-scaled rows straight into y
-        (moe_grouped_swiglu_combine; implies fused_gather), and y_perm is not written."""
+        (moe_grouped_swiglu_combine; implies fused_gather), and y_perm is not written.
+        pre_norm: the rows the experts see are the layer norm of x (``gamma``, ``beta``, ``eps``).
+        training: allocate what ``backward`` writes; it needs x_perm and y_perm, so neither
+        fused_gather nor combine_in_epilogue."""
+        if training and (fused_gather or combine_in_epilogue):
+            raise ValueError("the backward pass reads x_perm and y_perm: a training layer gathers "
+                             "and combines in calls of their own")
         self.cfg = cfg
         self.stitched = stitched
         self.combine_in_epilogue = combine_in_epilogue
@@ -70,6 +86,13 @@ class MoELayer:
         i32 = dict(dtype=torch.int32, device=d)
         self.logits = torch.empty((T, E), dtype=torch.float32, device=d)
         self.x = torch.empty((T, H), dtype=tdt, device=d)
+        f32 = dict(dtype=torch.float32, device=d)
+        self.pre_norm, self.eps, self.training = pre_norm, eps, training
+        # what the router and the experts see: x, or its norm
+        self.xn = torch.empty_like(self.x) if pre_norm else self.x
+        if pre_norm:
+            self.gamma, self.beta = torch.ones((H,), **f32), torch.zeros((H,), **f32)
+            self.mean, self.rstd = torch.empty((T,), **f32), torch.empty((T,), **f32)
         self.topk_idx = torch.empty((T, k), **i32)
         self.topk_w = torch.empty((T, k), dtype=torch.float32, device=d)
         self.counts = torch.empty((E,), **i32)
@@ -85,6 +108,20 @@ class MoELayer:
         self.ws_perm = torch.empty((max(1, self.ws_perm_bytes),), dtype=torch.uint8, device=d)
         self.ws_gemm_bytes = B.moe_grouped_swiglu_workspace_size(R, E, H, I, self.dt)
         self.ws_gemm = torch.empty((self.ws_gemm_bytes,), dtype=torch.uint8, device=d)
+        if training:
+            self.dy_perm = torch.empty((R, H), dtype=tdt, device=d)
+            self.dx_perm = torch.empty((R, H), dtype=tdt, device=d)
+            self.dtopk_w = torch.empty((T, k), **f32)
+            self.dlogits = torch.empty((T, E), **f32)
+            self.dxn = torch.empty((T, H), dtype=tdt, device=d)
+            self.dx = torch.empty((T, H), dtype=tdt, device=d) if pre_norm else self.dxn
+            self.dw = torch.empty((E if n_slots is None else n_slots, 3 * H * I), dtype=tdt, device=d)
+            if pre_norm:
+                self.dgamma, self.dbeta = torch.empty((H,), **f32), torch.empty((H,), **f32)
+            need = B.moe_grouped_swiglu_backward_workspace_size(R, E, H, I, self.dt)
+            if pre_norm:
+                need = max(need, B.moe_layer_norm_backward_workspace_size(T, H))
+            self.ws_backward = torch.empty((need,), dtype=torch.uint8, device=d)
         self.counts_host = torch.empty((E,), dtype=torch.int32, pin_memory=True)
         self.n_slots = E if n_slots is None else n_slots
         self.halves = []
@@ -162,10 +199,20 @@ class MoELayer:
         return self._local_t[e] if e < n_local else self._remote_t[e - n_local]
 
     # ------------------------------------------------------------------ steps
-    def route_permute(self) -> None:
+    def norm(self) -> None:
+        """Compute stream: xn = layer norm of x (a layer with pre_norm)."""
+        cfg = self.cfg
+        B.moe_layer_norm(self.x, self.gamma, self.beta, cfg.T, cfg.H, self.eps, self.dt, self.xn,
+                         self.mean, self.rstd, self.compute_stream)
+
+    def route_permute(self, normed: bool = False) -> None:
+        """``normed``: xn is already there (a caller whose router reads the normed rows calls
+        ``norm``, writes the logits from xn on the compute stream, and comes here)."""
         cfg, cs = self.cfg, self.compute_stream
+        if self.pre_norm and not normed:
+            self.norm()
         B.moe_route(self.logits, cfg.T, cfg.E, cfg.k, self.topk_idx, self.topk_w, self.status, cs)
-        B.moe_permute(self.topk_idx, cfg.T, cfg.E, cfg.k, self.x, cfg.H, self.dt, self.counts,
+        B.moe_permute(self.topk_idx, cfg.T, cfg.E, cfg.k, self.xn, cfg.H, self.dt, self.counts,
                       self.offsets, self.row_of, self.src_of,
                       None if self.fused_gather else self.x_perm, self.ws_perm,
                       self.ws_perm_bytes, self.status, cs)
@@ -176,7 +223,7 @@ class MoELayer:
         e_end = cfg.E if e_end is None else e_end
         cs = self.compute_stream if stream is None else stream
         if self.fused_gather:
-            B.moe_grouped_swiglu_gathered(self.x, self.src_of, cfg.k, self.offsets, self.R, cfg.E,
+            B.moe_grouped_swiglu_gathered(self.xn, self.src_of, cfg.k, self.offsets, self.R, cfg.E,
                                           cfg.H, cfg.I, self.dt, wbuf, e_begin, e_end, self.ws_gemm,
                                           self.ws_gemm_bytes, self.y_perm, self.status, cs)
         else:
@@ -189,7 +236,7 @@ class MoELayer:
         epilogue: writes y directly (every expert of ``wbuf``)."""
         cfg = self.cfg
         cs = self.compute_stream if stream is None else stream
-        B.moe_grouped_swiglu_combine(self.x, self.src_of, self.topk_w, cfg.T, cfg.k, self.offsets,
+        B.moe_grouped_swiglu_combine(self.xn, self.src_of, self.topk_w, cfg.T, cfg.k, self.offsets,
                                      cfg.E, cfg.H, cfg.I, self.dt, wbuf, self.ws_gemm,
                                      self.ws_gemm_bytes, self.y, self.status, cs)
 
@@ -271,7 +318,8 @@ class MoELayer:
         self.expert_output(self.wbufs[half])
         B.moe_event_record(self.free[half], cs)
 
-    def forward(self, half: int = 0, remote: str = "routed", chunks: int = 0, ev=None) -> None:
+    def forward(self, half: int = 0, remote: str = "routed", chunks: int = 0, ev=None,
+                normed: bool = False) -> None:
         """One whole layer step; remote = 'routed' (fetch only the remote experts that got
         tokens, after a count read-back), 'device' (the same set, picked on the device: no
         read-back, nothing waits on the host) or 'all' (fetch the whole remote share).
@@ -332,6 +380,45 @@ class MoELayer:
         B.moe_combine(self.y_perm, self.row_of, self.topk_w, cfg.T, cfg.k, cfg.H, self.y, cs)
         B.moe_event_record(self.free[half], cs)
         self.last_ids = list(ids)
+
+    def backward_experts(self, dy: torch.Tensor, half: int = 0) -> None:
+        """Compute stream: from dy (the gradient of y, [T, H] f32 or bf16, written on the compute
+        stream) the gradients of the logits (``dlogits``), of the experts' weights (``dw``: slot by
+        slot as the half holds the experts) and of the rows they saw (``dxn``; that is ``dx``
+        without pre_norm), for the forward step that last ran.  The half must still hold that
+        step's experts; it is released again when the weights have been read."""
+        cfg, cs = self.cfg, self.compute_stream
+        if not self.training:
+            raise ValueError("the layer was not built with training=True")
+        if tuple(dy.shape) != (cfg.T, cfg.H) or not dy.is_contiguous() or \
+                dy.dtype not in (torch.float32, torch.bfloat16) or dy.device != self.y.device:
+            raise ValueError(f"dy must be a contiguous f32 or bf16 [{cfg.T}, {cfg.H}] tensor on {self.y.device}")
+        dy_dt = B.MOE_F32 if dy.dtype == torch.float32 else B.MOE_BF16
+        dy.record_stream(cs)
+        B.moe_combine_backward(dy, dy_dt, self.y_perm, self.row_of, self.topk_w, cfg.T, cfg.k, cfg.H,
+                               self.dt, self.dy_perm, self.dtopk_w, cs)
+        B.moe_route_backward(self.topk_idx, self.topk_w, self.dtopk_w, cfg.T, cfg.E, cfg.k,
+                             self.dlogits, self.status, cs)
+        B.moe_grouped_swiglu_backward(self.x_perm, self.dy_perm, self.offsets, self.R, cfg.E, cfg.H,
+                                      cfg.I, self.dt, self.wbufs[half], self.ws_backward,
+                                      self.ws_backward.numel(), self.dx_perm, self.dw, self.status, cs)
+        B.moe_event_record(self.free[half], cs)
+        B.moe_permute_backward(self.dx_perm, self.row_of, cfg.T, cfg.k, cfg.H, self.dt, self.dxn, cs)
+
+    def backward_norm(self) -> None:
+        """Compute stream: ``dx``, ``dgamma`` and ``dbeta`` from ``dxn`` (a layer with pre_norm;
+        a caller whose router read the normed rows adds that gradient to dxn first)."""
+        cfg = self.cfg
+        B.moe_layer_norm_backward(self.dxn, self.x, self.gamma, self.mean, self.rstd, cfg.T, cfg.H,
+                                  self.dt, self.dx, self.dgamma, self.dbeta, self.ws_backward,
+                                  self.ws_backward.numel(), self.compute_stream)
+
+    def backward(self, dy: torch.Tensor, half: int = 0) -> None:
+        """The whole backward pass of the last forward step: ``backward_experts``, then, with
+        pre_norm, ``backward_norm``."""
+        self.backward_experts(dy, half)
+        if self.pre_norm:
+            self.backward_norm()
 
     def synchronize(self) -> None:
         self.compute_stream.synchronize()

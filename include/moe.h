@@ -1,5 +1,6 @@
 /*
- * moe.h -- C ABI of the DWDP-style MoE layer forward on one MI355X (gfx950).
+ * moe.h -- C ABI of the DWDP-style MoE layer on one MI355X (gfx950): the forward pass, and
+ * the gradients of its steps.
  *
  * The layer follows the pattern of "DWDP: Distributed Weight Data Parallelism
  * for High-Performance LLM Inference on NVL72" (arXiv 2604.01621v1, abstract)
@@ -354,6 +355,126 @@ int moe_grouped_swiglu_combine(const void* x, const int32_t* src_of, const float
  */
 int moe_combine(const float* y_perm, const int32_t* row_of, const float* topk_w, int T, int k,
                 int H, float* y, moe_stream_t stream);
+
+/*
+ * Training pass of the block: the layer norm in front of it and the gradients of the calls
+ * above.  With dy the gradient of moe_combine's output y, one backward pass is
+ *   moe_combine_backward         dy -> dy_perm, dtopk_w
+ *   moe_route_backward           dtopk_w -> dlogits
+ *   moe_grouped_swiglu_backward  dy_perm -> dx_perm, dw
+ *   moe_permute_backward         dx_perm -> dx
+ *   moe_layer_norm_backward      dx -> the block input's gradient, dgamma, dbeta
+ * on the forward pass's own buffers (x_perm, y_perm, row_of, offsets, topk_idx, topk_w, mean,
+ * rstd).  Sums and statistics are f32; outputs are rounded once.  No call uses atomics on its
+ * outputs: the same inputs give the same bits.  dtype is that of x, x_perm and the weights.
+ * Every call may be captured into a HIP graph; captured calls that may run at the same time
+ * need workspaces of their own.  Outputs must not alias inputs.
+ */
+
+/*
+ * moe_layer_norm -- y[t] = (x[t] - mean_t) * rstd_t * gamma + beta over rows of H, with
+ * rstd_t = 1 / sqrt(var_t + eps) and var_t the mean square of x[t] - mean_t.
+ *   x, y        device [T][H] dtype; any alignment of one element
+ *   gamma, beta device f32[H]; beta may be NULL (no shift)
+ *   mean, rstd  device f32[T] (written; what the backward pass reads); either may be NULL
+ * Errors: MOE_ERR_ARG for null pointers, bad sizes or eps negative or NaN; MOE_ERR_UNSUPPORTED
+ * for H > 2^28.  T = 0 is a no-op.
+ */
+int moe_layer_norm(const void* x, const float* gamma, const float* beta, int T, int H, float eps,
+                   moe_dtype dtype, void* y, float* mean, float* rstd, moe_stream_t stream);
+
+/* Workspace bytes moe_layer_norm_backward needs for dgamma or dbeta (none without both). */
+int moe_layer_norm_backward_workspace_size(int T, int H, size_t* bytes);
+
+/*
+ * moe_layer_norm_backward -- the gradient of moe_layer_norm: with xh = (x - mean) * rstd and
+ * a = dy * gamma,  dx = rstd * (a - mean_h(a) - xh * mean_h(a xh)),
+ * dgamma = sum_t dy * xh,  dbeta = sum_t dy.
+ *   dy, x, dx    device [T][H] dtype
+ *   mean, rstd   device f32[T] (from moe_layer_norm)
+ *   dgamma, dbeta device f32[H] (overwritten; zeros for T = 0); either may be NULL
+ *   ws           device workspace of moe_layer_norm_backward_workspace_size() bytes; may be NULL
+ *                when dgamma and dbeta are
+ * Errors: as moe_layer_norm, plus MOE_ERR_WORKSPACE when ws_bytes is too small.
+ */
+int moe_layer_norm_backward(const void* dy, const void* x, const float* gamma, const float* mean,
+                            const float* rstd, int T, int H, moe_dtype dtype, void* dx,
+                            float* dgamma, float* dbeta, void* ws, size_t ws_bytes,
+                            moe_stream_t stream);
+
+/*
+ * moe_combine_backward -- the gradient of moe_combine:
+ *   dy_perm[row_of[t*k + j]] = topk_w[t][j] * dy[t]
+ *   dtopk_w[t][j] = sum_h dy[t][h] * y_perm[row_of[t*k + j]][h]
+ *   dy      device [T][H] dy_dtype (MOE_F32, or MOE_BF16 from a bf16 residual stream)
+ *   y_perm  device f32[T*k][H]; may be NULL when dtopk_w is
+ *   dy_perm device [T*k][H] dtype
+ *   dtopk_w device f32[T][k]; may be NULL (the routing weights are not trained)
+ * Rows that row_of does not name keep what they held; an index outside [0, T*k) (an assignment
+ * that moe_permute dropped) writes no row, and its dtopk_w is 0.
+ * Errors: MOE_ERR_ARG for null pointers or bad sizes; MOE_ERR_UNSUPPORTED for k > MOE_MAX_K,
+ * T*k >= 2^31 or H > 2^28.
+ */
+int moe_combine_backward(const void* dy, moe_dtype dy_dtype, const float* y_perm,
+                         const int32_t* row_of, const float* topk_w, int T, int k, int H,
+                         moe_dtype dtype, void* dy_perm, float* dtopk_w, moe_stream_t stream);
+
+/*
+ * moe_permute_backward -- the gradient of moe_permute's row gather:
+ *   dx[t] = sum_{j=0..k-1} dx_perm[row_of[t*k + j]], summed in j order in f32.
+ *   dx_perm device [T*k][H] dtype; dx device [T][H] dtype
+ * An index outside [0, T*k) adds nothing.
+ * Errors: MOE_ERR_ARG for null pointers or bad sizes; MOE_ERR_UNSUPPORTED for T*k >= 2^31 or
+ * H > 2^28.
+ */
+int moe_permute_backward(const void* dx_perm, const int32_t* row_of, int T, int k, int H,
+                         moe_dtype dtype, void* dx, moe_stream_t stream);
+
+/*
+ * moe_route_backward -- the gradient of moe_route's weights with respect to the logits:
+ *   dlogits[t][topk_idx[t][j]] = topk_w[t][j] * (dtopk_w[t][j] - sum_i topk_w[t][i] dtopk_w[t][i])
+ * and zero for the experts that were not chosen (the choice itself has no gradient).  An id that
+ * a token lists more than once gets the sum of its slots.
+ *   topk_idx, topk_w, dtopk_w device [T][k]; dlogits device f32[T][E] (every element written)
+ *   status device i32, may be NULL (MOE_STATUS_BAD_EXPERT_ID for an id outside [0, E), which is
+ *          then left out of dlogits)
+ * Errors: as moe_route.
+ */
+int moe_route_backward(const int32_t* topk_idx, const float* topk_w, const float* dtopk_w, int T,
+                       int E, int k, float* dlogits, int32_t* status, moe_stream_t stream);
+
+/* Workspace bytes moe_grouped_swiglu_backward needs for R = T*k rows. */
+int moe_grouped_swiglu_backward_workspace_size(int R, int E, int H, int I, moe_dtype dtype,
+                                               size_t* bytes);
+
+/*
+ * moe_grouped_swiglu_backward -- the gradient of moe_grouped_swiglu (of y_perm with respect to
+ * x_perm and the weights): for the rows r of each expert e, with g, u, h as there (recomputed
+ * from x_perm), dh = dy_perm[r] Wd_e, s = sigmoid(g):
+ *   du = dh * g * s,  dg = dh * u * s * (1 + g * (1 - s))  (stored in dtype, as h is),
+ *   dx_perm[r] = dg Wg_e + du Wu_e,
+ *   dWg_e = sum_r dg^T x_perm[r],  dWu_e = sum_r du^T x_perm[r],  dWd_e = sum_r dy_perm[r]^T h.
+ * Accumulation is f32 (MFMA).
+ *   x_perm, dy_perm device [R][H] dtype
+ *   offsets device i32[E+1] (from moe_permute)
+ *   w       merged buffer, as for moe_grouped_swiglu
+ *   ws      device workspace of moe_grouped_swiglu_backward_workspace_size() bytes
+ *   dx_perm device [R][H] dtype; may be NULL (only the weights are trained)
+ *   dw      device, n_slots expert blocks laid out as w's: the gradient of the expert in slot s
+ *           is written (not added) at dw + s * expert_bytes, zeros for an expert without rows;
+ *           blocks of slots that no expert maps to keep what they held.  May be NULL (frozen
+ *           experts).  Not both dx_perm and dw NULL.
+ *   status  device i32, may be NULL (MOE_STATUS_EXPERT_ABSENT when an expert with rows has no
+ *           slot in [0, n_slots): its rows of dx_perm are left unwritten)
+ * Rows of dx_perm at or past offsets[E] are left as they were.  With R = 0 only dw is written.
+ * Errors: MOE_ERR_ARG for null pointers or sizes that disagree with w; MOE_ERR_UNSUPPORTED for
+ * E > MOE_MAX_E, H or I > 2^20, H*I >= 2^30, (MOE_BF16) H or I not a multiple of 8, or a pointer
+ * not aligned to 16 bytes (MOE_F32: to 4); MOE_ERR_WORKSPACE when ws_bytes is too small.
+ */
+int moe_grouped_swiglu_backward(const void* x_perm, const void* dy_perm, const int32_t* offsets,
+                                int R, int E, int H, int I, moe_dtype dtype, const moe_wbuf* w,
+                                void* ws, size_t ws_bytes, void* dx_perm, void* dw,
+                                int32_t* status, moe_stream_t stream);
 
 /*
  * Multi-layer pipeline helpers (the block between two MoE layers).  The
