@@ -12,15 +12,15 @@
 //   3. dX = [dG dU] [Wg; Wu]: one product of depth 2I, as Wg and Wu lie one after the other
 //   4. dW: [dWg; dWu] = [dG dU]^T X and dWd = dY^T h, one block per expert and output tile
 //
-// fp32 MFMA tiles (32x32x2), bf16 operands widened as they are staged.
+// bf16: the tile product of mfma_tile.h; dH and dX read the weights transposed, dW both operands.
+// f32: 128 x 128 tiles of the fp32 MFMA (32x32x2), staged through registers.
 #include <algorithm>
+#include <type_traits>
 
-#include "common.h"
+#include "mfma_tile.h"
 
 namespace moe {
 namespace {
-
-typedef float floatx16 __attribute__((ext_vector_type(16)));
 
 struct Tile {
   int32_t expert;
@@ -30,10 +30,15 @@ struct Tile {
 };
 
 constexpr int kMaxSide = 1 << 20;  // largest H and I: bounds the grids
-constexpr int kBM = 128, kBN = 128, kBK = 16;
-constexpr int kLd = kBM + 4;  // LDS row (one k) of an operand tile
+constexpr int kBM = 128, kBN = 128, kBK = 16;  // f32 tile
+constexpr int kLd = kBM + 4;                   // LDS row (one k) of an f32 operand tile
+constexpr int kRowTile = 256;                  // bf16: rows of a tile
 
-int64_t max_tiles(int64_t R, int E) { return ceil_div64(R, kBM) + std::min<int64_t>(E, R); }
+int tile_rows(moe_dtype dt) { return dt == MOE_BF16 ? kRowTile : kBM; }
+
+int64_t max_tiles(int64_t R, int E, moe_dtype dt) {
+  return ceil_div64(R, tile_rows(dt)) + std::min<int64_t>(E, R);
+}
 
 struct BackwardWs {
   size_t dh_off, dgu_off, h_off, tiles_off, count_off, total;
@@ -46,7 +51,7 @@ BackwardWs backward_ws(int64_t R, int E, int I, moe_dtype dt) {
   w.dgu_off = align_up(n * sizeof(float), 256);
   w.h_off = w.dgu_off + align_up(2 * n * elem_size(dt), 256);
   w.tiles_off = w.h_off + align_up(n * elem_size(dt), 256);
-  w.count_off = w.tiles_off + align_up(static_cast<size_t>(max_tiles(R, E)) * sizeof(Tile), 256);
+  w.count_off = w.tiles_off + align_up(static_cast<size_t>(max_tiles(R, E, dt)) * sizeof(Tile), 256);
   w.total = w.count_off + 256;
   return w;
 }
@@ -89,16 +94,28 @@ __global__ __launch_bounds__(MOE_MAX_E) void backward_plan_kernel(
   if (e == 0) *n_tiles = min(s[MOE_MAX_E - 1], tile_cap);
 }
 
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ float to_f32(uint16_t v) { return bf16_to_f32(v); }
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(uint16_t* p, float v) { *p = f32_to_bf16(v); }
+
+// dG, dU and h of one element, from g, u and dH.  exp2 and reciprocal are the hardware's (about 1
+// ulp each); a sigmoid that saturates gives exact zeros, not NaN.
+__device__ __forceinline__ void swiglu_grad(float g, float u, float d, float* dg, float* du, float* h) {
+  const float sg = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.4426950408889634f));
+  const float silu = g * sg;
+  *dg = d * u * (sg * (1.0f + g * (1.0f - sg)));
+  *du = d * silu;
+  *h = silu * u;
+}
+
+// ---------------------------------------------------------------------------
+// f32
+// ---------------------------------------------------------------------------
 
 // One stage of an operand: 128 "outer" indices by 16 depth steps into LDS as [depth][outer], zero
 // outside [0, n_outer) and [0, K).  KMAJOR: element (o, k) is at p[k * ld + o], else at
 // p[o * ld + k].  `at(o)` maps a tile's outer index to the operand's (or -1).
-template <bool KMAJOR, typename T, typename At>
-__device__ __forceinline__ void stage(const T* __restrict__ p, int64_t ld, int k0, int K, At at,
+template <bool KMAJOR, typename At>
+__device__ __forceinline__ void stage(const float* __restrict__ p, int64_t ld, int k0, int K, At at,
                                       float* __restrict__ lds) {
   const int tid = threadIdx.x;
 #pragma unroll
@@ -108,19 +125,19 @@ __device__ __forceinline__ void stage(const T* __restrict__ p, int64_t ld, int k
     const int src = at(o);
     float v = 0.f;
     if (src >= 0 && k0 + k < K)
-      v = to_f32(KMAJOR ? p[static_cast<int64_t>(k0 + k) * ld + src]
-                        : p[static_cast<int64_t>(src) * ld + k0 + k]);
+      v = KMAJOR ? p[static_cast<int64_t>(k0 + k) * ld + src]
+                 : p[static_cast<int64_t>(src) * ld + k0 + k];
     lds[k * kLd + o] = v;
   }
 }
 
 // acc[i][j] += A B over depth [0, K): 4 waves as 2 x 2, each 64 rows (i) by two 32-column blocks
 // whose tile columns start at wcol[j].
-template <bool A_KMAJOR, bool B_KMAJOR, typename TA, typename TB, typename AtA, typename AtB>
-__device__ __forceinline__ void tile_product(const TA* __restrict__ A, int64_t lda, AtA at_a,
-                                             const TB* __restrict__ B, int64_t ldb, AtB at_b, int K,
-                                             const int (&wcol)[2], float* As, float* Bs,
-                                             floatx16 (&acc)[2][2]) {
+template <bool A_KMAJOR, bool B_KMAJOR, typename AtA, typename AtB>
+__device__ __forceinline__ void tile_product_f32(const float* __restrict__ A, int64_t lda, AtA at_a,
+                                                 const float* __restrict__ B, int64_t ldb, AtB at_b,
+                                                 int K, const int (&wcol)[2], float* As, float* Bs,
+                                                 floatx16 (&acc)[2][2]) {
   const int lane = threadIdx.x & (kWave - 1);
   const int wm = (threadIdx.x / kWave) >> 1;
   for (int k0 = 0; k0 < K; k0 += kBK) {
@@ -162,21 +179,20 @@ __device__ __forceinline__ int acc_row(int i, int q) {
 
 // C[r][n] = sum_k A[r][k] B[k][n] for the rows of each tile; B of the tile's expert starts at
 // b_off of its block.
-template <typename T, typename O>
-__global__ __launch_bounds__(256) void rows_product_kernel(
-    const T* __restrict__ A, int64_t lda, const char* __restrict__ wbase, int64_t expert_bytes,
+__global__ __launch_bounds__(256) void rows_product_f32_kernel(
+    const float* __restrict__ A, int64_t lda, const char* __restrict__ wbase, int64_t expert_bytes,
     int64_t b_off, int N, int K, const Tile* __restrict__ tiles, const int32_t* __restrict__ n_tiles,
-    O* __restrict__ C) {
+    float* __restrict__ C) {
   __shared__ float As[kBK * kLd], Bs[kBK * kLd];
   if (static_cast<int>(blockIdx.x) >= *n_tiles) return;
   const Tile t = tiles[blockIdx.x];
   const int n0 = blockIdx.y * kBN;
   const int wn = (threadIdx.x / kWave) & 1;
-  const T* B = reinterpret_cast<const T*>(wbase + t.slot * expert_bytes + b_off);
+  const float* B = reinterpret_cast<const float*>(wbase + t.slot * expert_bytes + b_off);
   const int wcol[2] = {wn * 64, wn * 64 + 32};
   floatx16 acc[2][2];
   clear(acc);
-  tile_product<false, true>(
+  tile_product_f32<false, true>(
       A + t.row0 * lda, lda, [&](int o) { return o < t.rows ? o : -1; }, B, N,
       [&](int o) { return n0 + o < N ? n0 + o : -1; }, K, wcol, As, Bs, acc);
 #pragma unroll
@@ -188,28 +204,27 @@ __global__ __launch_bounds__(256) void rows_product_kernel(
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int c = n0 + wcol[j] + (threadIdx.x & 31);
-        if (c < N) put(C + static_cast<int64_t>(t.row0 + r) * N + c, acc[i][j][q]);
+        if (c < N) C[static_cast<int64_t>(t.row0 + r) * N + c] = acc[i][j][q];
       }
     }
 }
 
 // g and u for 64 columns, then dG, dU and h from dH.
-template <typename T>
-__global__ __launch_bounds__(256) void gate_up_backward_kernel(
-    const T* __restrict__ x, const char* __restrict__ wbase, int64_t expert_bytes, int H, int I,
+__global__ __launch_bounds__(256) void gate_up_backward_f32_kernel(
+    const float* __restrict__ x, const char* __restrict__ wbase, int64_t expert_bytes, int H, int I,
     const Tile* __restrict__ tiles, const int32_t* __restrict__ n_tiles, const float* __restrict__ dh,
-    T* __restrict__ dgu, T* __restrict__ h) {
+    float* __restrict__ dgu, float* __restrict__ h) {
   __shared__ float As[kBK * kLd], Bs[kBK * kLd];
   if (static_cast<int>(blockIdx.x) >= *n_tiles) return;
   const Tile t = tiles[blockIdx.x];
   const int n0 = blockIdx.y * (kBN / 2);
   const int wn = (threadIdx.x / kWave) & 1;
-  const T* W = reinterpret_cast<const T*>(wbase + t.slot * expert_bytes);
+  const float* W = reinterpret_cast<const float*>(wbase + t.slot * expert_bytes);
   // B tile: 64 rows of Wg, then the same 64 rows of Wu, so a wave holds matching columns of both
   const int wcol[2] = {wn * 32, 64 + wn * 32};
   floatx16 acc[2][2];
   clear(acc);
-  tile_product<false, false>(
+  tile_product_f32<false, false>(
       x + static_cast<int64_t>(t.row0) * H, H, [&](int o) { return o < t.rows ? o : -1; }, W, H,
       [&](int o) {
         const int c = n0 + (o & 63);
@@ -225,20 +240,15 @@ __global__ __launch_bounds__(256) void gate_up_backward_kernel(
       const int r = acc_row(i, q);
       if (r >= t.rows) continue;
       const int64_t row = t.row0 + r;
-      const float g = acc[i][0][q], u = acc[i][1][q], d = dh[row * I + c];
-      const float sg = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.4426950408889634f));
-      const float silu = g * sg;
-      put(dgu + row * 2 * I + c, d * u * (sg * (1.0f + g * (1.0f - sg))));
-      put(dgu + row * 2 * I + I + c, d * silu);
-      put(h + row * I + c, silu * u);
+      swiglu_grad(acc[i][0][q], acc[i][1][q], dh[row * I + c], dgu + row * 2 * I + c,
+                  dgu + row * 2 * I + I + c, h + row * I + c);
     }
 }
 
 // C[m][n] = sum over the expert's rows r of A[r][m] B[r][n], written at c_off of the expert's
 // block of dw.  An expert without rows gets zeros, one outside the buffer nothing.
-template <typename T>
-__global__ __launch_bounds__(256) void weight_grad_kernel(
-    const T* __restrict__ A, int M, const T* __restrict__ B, int N, const int32_t* __restrict__ offsets,
+__global__ __launch_bounds__(256) void weight_grad_f32_kernel(
+    const float* __restrict__ A, int M, const float* __restrict__ B, int N, const int32_t* __restrict__ offsets,
     int R, const int32_t* __restrict__ slot_of, int n_slots, int64_t expert_bytes, int64_t c_off,
     char* __restrict__ dw) {
   __shared__ float As[kBK * kLd], Bs[kBK * kLd];
@@ -252,11 +262,11 @@ __global__ __launch_bounds__(256) void weight_grad_kernel(
   const int wcol[2] = {wn * 64, wn * 64 + 32};
   floatx16 acc[2][2];
   clear(acc);
-  tile_product<true, true>(
+  tile_product_f32<true, true>(
       A + static_cast<int64_t>(lo) * M, M, [&](int o) { return m0 + o < M ? m0 + o : -1; },
       B + static_cast<int64_t>(lo) * N, N, [&](int o) { return n0 + o < N ? n0 + o : -1; }, K, wcol, As,
       Bs, acc);
-  T* C = reinterpret_cast<T*>(dw + slot * expert_bytes + c_off);
+  float* C = reinterpret_cast<float*>(dw + slot * expert_bytes + c_off);
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -266,52 +276,301 @@ __global__ __launch_bounds__(256) void weight_grad_kernel(
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int c = n0 + wcol[j] + (threadIdx.x & 31);
-        if (c < N) put(C + static_cast<int64_t>(m) * N + c, acc[i][j][q]);
+        if (c < N) C[static_cast<int64_t>(m) * N + c] = acc[i][j][q];
       }
     }
 }
 
-template <typename T>
-int run(const void* x_perm, const void* dy_perm, const int32_t* offsets, int R, int E, int H, int I,
-        moe_dtype dt, const moe_wbuf* w, char* ws, void* dx_perm, void* dw, int32_t* status,
-        hipStream_t s) {
-  const BackwardWs L = backward_ws(R, E, I, dt);
-  float* dh = reinterpret_cast<float*>(ws + L.dh_off);
-  T* dgu = reinterpret_cast<T*>(ws + L.dgu_off);
-  T* h = reinterpret_cast<T*>(ws + L.h_off);
-  Tile* tiles = reinterpret_cast<Tile*>(ws + L.tiles_off);
-  int32_t* n_tiles = reinterpret_cast<int32_t*>(ws + L.count_off);
-  const T* x = static_cast<const T*>(x_perm);
-  const T* dy = static_cast<const T*>(dy_perm);
-  const char* wbase = static_cast<const char*>(w->base);
-  const int64_t eb = w->expert_bytes;
-  const int64_t HI = static_cast<int64_t>(H) * I * sizeof(T);
-  if (R > 0) {
-    const unsigned cap = static_cast<unsigned>(max_tiles(R, E));
-    hipLaunchKernelGGL(backward_plan_kernel, dim3(1), dim3(MOE_MAX_E), 0, s, offsets, R, E, kBM,
-                       w->slot_of, w->n_slots, static_cast<int>(cap), tiles, n_tiles, status);
-    MOE_LAUNCH_CHECK("moe_grouped_swiglu_backward: plan");
-    hipLaunchKernelGGL((rows_product_kernel<T, float>), dim3(cap, ceil_div(I, kBN)), dim3(256), 0, s, dy,
+// ---------------------------------------------------------------------------
+// bf16
+// ---------------------------------------------------------------------------
+
+// Work order: units of gm x gn output tiles, unit u on XCD u % 8 (workgroup i runs on XCD i % 8),
+// so the workgroups that run together on an XCD share gm row panels and gn column panels in its L2.
+struct Order {
+  int gm, gn, n_gn;  // tiles of a unit; units across
+};
+
+__device__ __forceinline__ void place(const Order& o, int* m, int* n) {
+  const int xcd = blockIdx.x % 8, local = blockIdx.x / 8;
+  const int per = o.gm * o.gn;
+  const int unit = local / per * 8 + xcd, at = local % per;
+  *m = unit / o.n_gn * o.gm + at % o.gm;
+  *n = unit % o.n_gn * o.gn + at / o.gm;
+}
+
+Order make_order(int64_t mt, int64_t nt, int64_t* grid) {
+  // 4 x 8 tiles (32 CUs an XCD) where that leaves every XCD a few units, else single tiles
+  Order o{4, 8, 0};
+  if (ceil_div64(mt, 4) * ceil_div64(nt, 8) < 32) o = Order{1, 1, 0};
+  o.n_gn = static_cast<int>(ceil_div64(nt, o.gn));
+  const int64_t units = ceil_div64(mt, o.gm) * o.n_gn;
+  *grid = ceil_div64(units, 8) * 8 * o.gm * o.gn;
+  return o;
+}
+
+__device__ __forceinline__ Tile load_tile(const Tile* tiles, int m) {
+  const Tile t = tiles[m];
+  return Tile{__builtin_amdgcn_readfirstlane(t.expert), __builtin_amdgcn_readfirstlane(t.row0),
+              __builtin_amdgcn_readfirstlane(t.rows), __builtin_amdgcn_readfirstlane(t.slot)};
+}
+
+// Calls f with the smallest tile mode that holds `rows` rows.
+template <typename F>
+__device__ __forceinline__ void by_rows(int rows, F f) {
+  if (rows > 192) f(std::integral_constant<int, 0>{});
+  else if (rows > 128) f(std::integral_constant<int, 6>{});
+  else if (rows > 64) f(std::integral_constant<int, 4>{});
+  else if (rows > 32) f(std::integral_constant<int, 2>{});
+  else f(std::integral_constant<int, 1>{});
+}
+
+// C[r][n] = sum_k A[r][k] B[k][n] for the rows of each tile; B of the tile's expert starts at
+// b_off of its block.
+template <int MI, typename O>
+__device__ __forceinline__ void rows_product(const Tile& t, int n0, const uint16_t* A, int lda,
+                                             const uint16_t* B, int N, int K, O* C, lds_char* smem) {
+  using S = TileShape<MI, false>;
+  Operand<false, S::ROWS> oa;
+  Operand<true, 256> ob;
+  oa.init(A + static_cast<int64_t>(t.row0) * lda, lda, [&](int r) { return r < t.rows ? r : -1; });
+  ob.init(B + n0, N, [&](int c) { return n0 + c < N ? c : -1; });
+  floatx16 acc[S::MW][S::NJ];
+  tile_product<MI, false, false, true>(oa, ob, K, smem, acc);
+  const int c0 = n0 + S::first_col() + (threadIdx.x & 31);
+#pragma unroll
+  for (int i = 0; i < S::MW; ++i)
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      const int r = tile_row<MI, false>(i, q);
+      if (r >= t.rows) continue;
+      O* row = C + static_cast<int64_t>(t.row0 + r) * N;
+#pragma unroll
+      for (int j = 0; j < S::NJ; ++j)
+        if (c0 + S::col(j) < N) put(row + c0 + S::col(j), acc[i][j][q]);
+    }
+}
+
+template <typename O>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void rows_product_kernel(
+    const uint16_t* __restrict__ A, int lda, const char* __restrict__ wbase, int64_t expert_bytes,
+    int64_t b_off, int N, int K, const Tile* __restrict__ tiles, const int32_t* __restrict__ n_tiles,
+    Order order, O* __restrict__ C) {
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  int m, n;
+  place(order, &m, &n);
+  if (m >= *n_tiles || n * kTileN >= N) return;
+  const Tile t = load_tile(tiles, m);
+  const uint16_t* B = reinterpret_cast<const uint16_t*>(wbase + t.slot * expert_bytes + b_off);
+  by_rows(t.rows, [&](auto mi) {
+    rows_product<decltype(mi)::value>(t, n * kTileN, A, lda, B, N, K, C, (lds_char*)smem);
+  });
+}
+
+// g and u for 128 columns, then dG, dU and h from dH.
+template <int MI>
+__device__ __forceinline__ void gate_up_backward(const Tile& t, int n0, const uint16_t* x,
+                                                 const uint16_t* W, int H, int I, const float* dh,
+                                                 uint16_t* dgu, uint16_t* h, lds_char* smem) {
+  using S = TileShape<MI, true>;
+  Operand<false, S::ROWS> oa;
+  Operand<false, 256> ob;
+  oa.init(x + static_cast<int64_t>(t.row0) * H, H, [&](int r) { return r < t.rows ? r : -1; });
+  ob.init(W + static_cast<int64_t>(n0) * H, H,
+          [&](int r) { return n0 + (r & 127) < I ? (r & 127) + (r >> 7) * I : -1; });
+  floatx16 acc[S::MW][S::NJ];
+  tile_product<MI, true, false, false>(oa, ob, H, smem, acc);
+  const int c0 = n0 + S::first_col() + (threadIdx.x & 31);
+#pragma unroll
+  for (int i = 0; i < S::MW; ++i)
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      const int r = tile_row<MI, true>(i, q);
+      if (r >= t.rows) continue;
+      const int64_t row = t.row0 + r;
+#pragma unroll
+      for (int j = 0; j < S::NJ / 2; ++j) {
+        const int c = c0 + S::col(j);
+        if (c >= I) continue;
+        float dg, du, hv;
+        swiglu_grad(acc[i][j][q], acc[i][j + S::NJ / 2][q], dh[row * I + c], &dg, &du, &hv);
+        put(dgu + row * 2 * I + c, dg);
+        put(dgu + row * 2 * I + I + c, du);
+        put(h + row * I + c, hv);
+      }
+    }
+}
+
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void
+gate_up_backward_kernel(const uint16_t* __restrict__ x, const char* __restrict__ wbase,
+                        int64_t expert_bytes, int H, int I, const Tile* __restrict__ tiles,
+                        const int32_t* __restrict__ n_tiles, Order order, const float* __restrict__ dh,
+                        uint16_t* __restrict__ dgu, uint16_t* __restrict__ h) {
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  int m, n;
+  place(order, &m, &n);
+  if (m >= *n_tiles || n * (kTileN / 2) >= I) return;
+  const Tile t = load_tile(tiles, m);
+  const uint16_t* W = reinterpret_cast<const uint16_t*>(wbase + t.slot * expert_bytes);
+  by_rows(t.rows, [&](auto mi) {
+    gate_up_backward<decltype(mi)::value>(t, n * (kTileN / 2), x, W, H, I, dh, dgu, h, (lds_char*)smem);
+  });
+}
+
+// C[m][n] = sum over the expert's rows r of A[r][m] B[r][n], written at c_off of the expert's
+// block of dw.  An expert without rows gets zeros, one outside the buffer nothing.
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void weight_grad_kernel(
+    const uint16_t* __restrict__ A, int M, const uint16_t* __restrict__ B, int N,
+    const int32_t* __restrict__ offsets, int R, const int32_t* __restrict__ slot_of, int n_slots,
+    int64_t expert_bytes, int64_t c_off, Order order, char* __restrict__ dw) {
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  using S = TileShape<0, false>;
+  int m, n;
+  place(order, &m, &n);
+  const int e = blockIdx.y;
+  const int m0 = m * kRowTile, n0 = n * kTileN;
+  if (m0 >= M || n0 >= N) return;
+  const int slot = __builtin_amdgcn_readfirstlane(slot_of[e]);
+  if (slot < 0 || slot >= n_slots) return;
+  int lo;
+  const int K = __builtin_amdgcn_readfirstlane(expert_rows(offsets, e, R, &lo));
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  Operand<true, 256> oa, ob;
+  oa.init(A + static_cast<int64_t>(lo) * M + m0, M, [&](int c) { return m0 + c < M ? c : -1; });
+  ob.init(B + static_cast<int64_t>(lo) * N + n0, N, [&](int c) { return n0 + c < N ? c : -1; });
+  floatx16 acc[S::MW][S::NJ];
+  tile_product<0, false, true, true>(oa, ob, K, (lds_char*)smem, acc);
+  uint16_t* C = reinterpret_cast<uint16_t*>(dw + slot * expert_bytes + c_off);
+  const int c0 = n0 + S::first_col() + (threadIdx.x & 31);
+#pragma unroll
+  for (int i = 0; i < S::MW; ++i)
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      const int r = m0 + tile_row<0, false>(i, q);
+      if (r >= M) continue;
+      uint16_t* row = C + static_cast<int64_t>(r) * N;
+#pragma unroll
+      for (int j = 0; j < S::NJ; ++j)
+        if (c0 + S::col(j) < N) put(row + c0 + S::col(j), acc[i][j][q]);
+    }
+}
+
+struct Call {
+  const int32_t* offsets;
+  int R, E, H, I;
+  const moe_wbuf* w;
+  char* ws;
+  BackwardWs L;
+  void* dx_perm;
+  char* dw;
+  int32_t* status;
+  hipStream_t s;
+};
+
+int launch_plan(const Call& c, moe_dtype dt, Tile** tiles, int32_t** n_tiles, int64_t* cap) {
+  *tiles = reinterpret_cast<Tile*>(c.ws + c.L.tiles_off);
+  *n_tiles = reinterpret_cast<int32_t*>(c.ws + c.L.count_off);
+  *cap = max_tiles(c.R, c.E, dt);
+  hipLaunchKernelGGL(backward_plan_kernel, dim3(1), dim3(MOE_MAX_E), 0, c.s, c.offsets, c.R, c.E,
+                     tile_rows(dt), c.w->slot_of, c.w->n_slots, static_cast<int>(*cap), *tiles, *n_tiles,
+                     c.status);
+  MOE_LAUNCH_CHECK("moe_grouped_swiglu_backward: plan");
+  return MOE_OK;
+}
+
+int run_f32(const Call& c, const float* x, const float* dy) {
+  const int E = c.E, H = c.H, I = c.I;
+  float* dh = reinterpret_cast<float*>(c.ws + c.L.dh_off);
+  float* dgu = reinterpret_cast<float*>(c.ws + c.L.dgu_off);
+  float* h = reinterpret_cast<float*>(c.ws + c.L.h_off);
+  const char* wbase = static_cast<const char*>(c.w->base);
+  const int64_t eb = c.w->expert_bytes, HI = static_cast<int64_t>(H) * I * sizeof(float);
+  if (c.R > 0) {
+    Tile* tiles;
+    int32_t* n_tiles;
+    int64_t cap64;
+    const int rc = launch_plan(c, MOE_F32, &tiles, &n_tiles, &cap64);
+    if (rc) return rc;
+    const unsigned cap = static_cast<unsigned>(cap64);
+    hipLaunchKernelGGL(rows_product_f32_kernel, dim3(cap, ceil_div(I, kBN)), dim3(256), 0, c.s, dy,
                        static_cast<int64_t>(H), wbase, eb, 2 * HI, I, H, tiles, n_tiles, dh);
     MOE_LAUNCH_CHECK("moe_grouped_swiglu_backward: dh");
-    hipLaunchKernelGGL(gate_up_backward_kernel<T>, dim3(cap, ceil_div(I, kBN / 2)), dim3(256), 0, s, x,
+    hipLaunchKernelGGL(gate_up_backward_f32_kernel, dim3(cap, ceil_div(I, kBN / 2)), dim3(256), 0, c.s, x,
                        wbase, eb, H, I, tiles, n_tiles, dh, dgu, h);
     MOE_LAUNCH_CHECK("moe_grouped_swiglu_backward: gate/up");
-    if (dx_perm) {
-      hipLaunchKernelGGL((rows_product_kernel<T, T>), dim3(cap, ceil_div(H, kBN)), dim3(256), 0, s, dgu,
+    if (c.dx_perm) {
+      hipLaunchKernelGGL(rows_product_f32_kernel, dim3(cap, ceil_div(H, kBN)), dim3(256), 0, c.s, dgu,
                          2 * static_cast<int64_t>(I), wbase, eb, int64_t{0}, H, 2 * I, tiles, n_tiles,
-                         static_cast<T*>(dx_perm));
+                         static_cast<float*>(c.dx_perm));
       MOE_LAUNCH_CHECK("moe_grouped_swiglu_backward: dx");
     }
   }
-  if (dw) {
-    char* out = static_cast<char*>(dw);
-    hipLaunchKernelGGL(weight_grad_kernel<T>, dim3(ceil_div(2 * I, kBM), ceil_div(H, kBN), E), dim3(256),
-                       0, s, dgu, 2 * I, x, H, offsets, R, w->slot_of, w->n_slots, eb, int64_t{0}, out);
+  if (c.dw) {
+    hipLaunchKernelGGL(weight_grad_f32_kernel, dim3(ceil_div(2 * I, kBM), ceil_div(H, kBN), E), dim3(256),
+                       0, c.s, dgu, 2 * I, x, H, c.offsets, c.R, c.w->slot_of, c.w->n_slots, eb,
+                       int64_t{0}, c.dw);
     MOE_LAUNCH_CHECK("moe_grouped_swiglu_backward: gate/up weights");
-    hipLaunchKernelGGL(weight_grad_kernel<T>, dim3(ceil_div(H, kBM), ceil_div(I, kBN), E), dim3(256), 0,
-                       s, dy, H, h, I, offsets, R, w->slot_of, w->n_slots, eb, 2 * HI, out);
+    hipLaunchKernelGGL(weight_grad_f32_kernel, dim3(ceil_div(H, kBM), ceil_div(I, kBN), E), dim3(256), 0,
+                       c.s, dy, H, h, I, c.offsets, c.R, c.w->slot_of, c.w->n_slots, eb, 2 * HI, c.dw);
     MOE_LAUNCH_CHECK("moe_grouped_swiglu_backward: down weights");
+  }
+  return MOE_OK;
+}
+
+// Enqueue a tile kernel: its 128 KB of LDS are above the default limit of a launch.
+template <typename K, typename... A>
+int launch_tiles(const char* what, K kernel, dim3 grid, hipStream_t s, A... args) {
+  MOE_HIP_CHECK(hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                    hipFuncAttributeMaxDynamicSharedMemorySize, kTileLds));
+  hipLaunchKernelGGL(kernel, grid, dim3(256), kTileLds, s, args...);
+  MOE_LAUNCH_CHECK(what);
+  return MOE_OK;
+}
+
+int run_bf16(const Call& c, const uint16_t* x, const uint16_t* dy) {
+  const int H = c.H, I = c.I;
+  float* dh = reinterpret_cast<float*>(c.ws + c.L.dh_off);
+  uint16_t* dgu = reinterpret_cast<uint16_t*>(c.ws + c.L.dgu_off);
+  uint16_t* h = reinterpret_cast<uint16_t*>(c.ws + c.L.h_off);
+  const char* wbase = static_cast<const char*>(c.w->base);
+  const int64_t eb = c.w->expert_bytes, HI = static_cast<int64_t>(H) * I * 2;
+  int64_t grid;
+  int rc;
+  if (c.R > 0) {
+    Tile* tiles;
+    int32_t* n_tiles;
+    int64_t cap;
+    rc = launch_plan(c, MOE_BF16, &tiles, &n_tiles, &cap);
+    if (rc) return rc;
+    Order o = make_order(cap, ceil_div(I, kTileN), &grid);
+    rc = launch_tiles("moe_grouped_swiglu_backward: dh", rows_product_kernel<float>,
+                      dim3(static_cast<unsigned>(grid)), c.s, dy, H, wbase, eb, 2 * HI, I, H, tiles,
+                      n_tiles, o, dh);
+    if (rc) return rc;
+    o = make_order(cap, ceil_div(I, kTileN / 2), &grid);
+    rc = launch_tiles("moe_grouped_swiglu_backward: gate/up", gate_up_backward_kernel,
+                      dim3(static_cast<unsigned>(grid)), c.s, x, wbase, eb, H, I, tiles, n_tiles, o, dh,
+                      dgu, h);
+    if (rc) return rc;
+    if (c.dx_perm) {
+      o = make_order(cap, ceil_div(H, kTileN), &grid);
+      rc = launch_tiles("moe_grouped_swiglu_backward: dx", rows_product_kernel<uint16_t>,
+                        dim3(static_cast<unsigned>(grid)), c.s, dgu, 2 * I, wbase, eb, int64_t{0}, H,
+                        2 * I, tiles, n_tiles, o, static_cast<uint16_t*>(c.dx_perm));
+      if (rc) return rc;
+    }
+  }
+  if (c.dw) {
+    Order o = make_order(ceil_div(2 * I, kRowTile), ceil_div(H, kTileN), &grid);
+    rc = launch_tiles("moe_grouped_swiglu_backward: gate/up weights", weight_grad_kernel,
+                      dim3(static_cast<unsigned>(grid), c.E), c.s, dgu, 2 * I, x, H, c.offsets, c.R,
+                      c.w->slot_of, c.w->n_slots, eb, int64_t{0}, o, c.dw);
+    if (rc) return rc;
+    o = make_order(ceil_div(H, kRowTile), ceil_div(I, kTileN), &grid);
+    rc = launch_tiles("moe_grouped_swiglu_backward: down weights", weight_grad_kernel,
+                      dim3(static_cast<unsigned>(grid), c.E), c.s, dy, H, h, I, c.offsets, c.R,
+                      c.w->slot_of, c.w->n_slots, eb, 2 * HI, o, c.dw);
+    if (rc) return rc;
   }
   return MOE_OK;
 }
@@ -344,8 +603,8 @@ extern "C" int moe_grouped_swiglu_backward(const void* x_perm, const void* dy_pe
   if (w->expert_bytes != eb || w->n_experts != E)
     return fail(MOE_ERR_ARG, "%s: merged buffer holds %lld-byte blocks for E=%d, expected %lld for E=%d",
                 who, static_cast<long long>(w->expert_bytes), w->n_experts, static_cast<long long>(eb), E);
-  if (static_cast<int64_t>(H) * I >= (int64_t{1} << 30) || H > kMaxSide || I > kMaxSide)
-    return fail(MOE_ERR_UNSUPPORTED, "%s: H=%d or I=%d above %d, or H*I 2^30 or more", who, H, I, kMaxSide);
+  if (static_cast<int64_t>(H) * I >= (int64_t{1} << 29) || H > kMaxSide || I > kMaxSide)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: H=%d or I=%d above %d, or H*I 2^29 or more", who, H, I, kMaxSide);
   if (dtype == MOE_BF16 && (H % 8 != 0 || I % 8 != 0))
     return fail(MOE_ERR_UNSUPPORTED, "%s: H=%d and I=%d must be multiples of 8", who, H, I);
   const uintptr_t all = reinterpret_cast<uintptr_t>(x_perm) | reinterpret_cast<uintptr_t>(dy_perm) |
@@ -359,10 +618,9 @@ extern "C" int moe_grouped_swiglu_backward(const void* x_perm, const void* dy_pe
     return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", who, ws_bytes, L.total);
   if (R > 0 && (!x_perm || !dy_perm)) return fail(MOE_ERR_ARG, "%s: null pointer", who);
   hipStream_t s = as_stream(stream);
-  char* wsb = static_cast<char*>(ws);
-  const int rc = dtype == MOE_F32 ? run<float>(x_perm, dy_perm, offsets, R, E, H, I, dtype, w, wsb,
-                                               dx_perm, dw, status, s)
-                                  : run<uint16_t>(x_perm, dy_perm, offsets, R, E, H, I, dtype, w, wsb,
-                                                  dx_perm, dw, status, s);
+  const Call c{offsets, R, E, H, I, w, static_cast<char*>(ws), L, dx_perm, static_cast<char*>(dw), status, s};
+  const int rc = dtype == MOE_F32
+                     ? run_f32(c, static_cast<const float*>(x_perm), static_cast<const float*>(dy_perm))
+                     : run_bf16(c, static_cast<const uint16_t*>(x_perm), static_cast<const uint16_t*>(dy_perm));
   return debug_check(rc, who, s, status);
 }
