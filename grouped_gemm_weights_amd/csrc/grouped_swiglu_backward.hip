@@ -94,9 +94,6 @@ __global__ __launch_bounds__(MOE_MAX_E) void backward_plan_kernel(
   if (e == 0) *n_tiles = min(s[MOE_MAX_E - 1], tile_cap);
 }
 
-__device__ __forceinline__ void put(float* p, float v) { *p = v; }
-__device__ __forceinline__ void put(uint16_t* p, float v) { *p = f32_to_bf16(v); }
-
 // dG, dU and h of one element, from g, u and dH.  exp2 and reciprocal are the hardware's (about 1
 // ulp each); a sigmoid that saturates gives exact zeros, not NaN.
 __device__ __forceinline__ void swiglu_grad(float g, float u, float d, float* dg, float* du, float* h) {
@@ -300,9 +297,10 @@ __device__ __forceinline__ void place(const Order& o, int* m, int* n) {
 }
 
 Order make_order(int64_t mt, int64_t nt, int64_t* grid) {
-  // 4 x 8 tiles (32 CUs an XCD) where that leaves every XCD a few units, else single tiles
-  Order o{4, 8, 0};
-  if (ceil_div64(mt, 4) * ceil_div64(nt, 8) < 32) o = Order{1, 1, 0};
+  // up to 4 x 8 tiles (32 CUs an XCD), the columns cut evenly, where that leaves every XCD a few
+  // units, else single tiles
+  Order o{4, static_cast<int>(ceil_div64(nt, ceil_div64(nt, 8))), 0};
+  if (ceil_div64(mt, o.gm) * ceil_div64(nt, o.gn) < 32) o.gm = o.gn = 1;
   o.n_gn = static_cast<int>(ceil_div64(nt, o.gn));
   const int64_t units = ceil_div64(mt, o.gm) * o.n_gn;
   *grid = ceil_div64(units, 8) * 8 * o.gm * o.gn;
@@ -325,6 +323,42 @@ __device__ __forceinline__ void by_rows(int rows, F f) {
   else f(std::integral_constant<int, 1>{});
 }
 
+// A tile's accumulators to C (its first row and column), of which rows x cols exist.
+template <int MI>
+__device__ __forceinline__ void store_tile(
+    const floatx16 (&acc)[TileShape<MI, false>::MW][TileShape<MI, false>::NJ], lds_char* smem,
+    uint16_t* C, int64_t ld, int rows, int cols) {
+  using S = TileShape<MI, false>;
+#pragma unroll
+  for (int i = 0; i < S::MW; ++i) {
+    const int r0 = S::first_row() + i * 32, c0 = S::first_col();
+    store_block<S::NJ * 32>(smem, C + r0 * ld + c0, ld, rows - r0, cols - c0, [&](int j, int v) {
+      return pack4(acc[i][j][v * 4], acc[i][j][v * 4 + 1], acc[i][j][v * 4 + 2], acc[i][j][v * 4 + 3]);
+    });
+  }
+}
+
+template <int MI>
+__device__ __forceinline__ void store_tile(
+    const floatx16 (&acc)[TileShape<MI, false>::MW][TileShape<MI, false>::NJ], lds_char*, float* C,
+    int64_t ld, int rows, int cols) {
+  using S = TileShape<MI, false>;
+#pragma unroll
+  for (int i = 0; i < S::MW; ++i) {
+    const int r = lane_row<MI, false>(i);
+    if (r >= rows) continue;
+#pragma unroll
+    for (int j = 0; j < S::NJ; ++j)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int c = S::first_col() + S::col(j) + lane_col(v);
+        if (c < cols)
+          *reinterpret_cast<floatx4*>(C + r * ld + c) =
+              floatx4{acc[i][j][v * 4], acc[i][j][v * 4 + 1], acc[i][j][v * 4 + 2], acc[i][j][v * 4 + 3]};
+      }
+  }
+}
+
 // C[r][n] = sum_k A[r][k] B[k][n] for the rows of each tile; B of the tile's expert starts at
 // b_off of its block.
 template <int MI, typename O>
@@ -337,18 +371,7 @@ __device__ __forceinline__ void rows_product(const Tile& t, int n0, const uint16
   ob.init(B + n0, N, [&](int c) { return n0 + c < N ? c : -1; });
   floatx16 acc[S::MW][S::NJ];
   tile_product<MI, false, false, true>(oa, ob, K, smem, acc);
-  const int c0 = n0 + S::first_col() + (threadIdx.x & 31);
-#pragma unroll
-  for (int i = 0; i < S::MW; ++i)
-#pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      const int r = tile_row<MI, false>(i, q);
-      if (r >= t.rows) continue;
-      O* row = C + static_cast<int64_t>(t.row0 + r) * N;
-#pragma unroll
-      for (int j = 0; j < S::NJ; ++j)
-        if (c0 + S::col(j) < N) put(row + c0 + S::col(j), acc[i][j][q]);
-    }
+  store_tile<MI>(acc, smem, C + static_cast<int64_t>(t.row0) * N + n0, N, t.rows, N - n0);
 }
 
 template <typename O>
@@ -380,25 +403,37 @@ __device__ __forceinline__ void gate_up_backward(const Tile& t, int n0, const ui
           [&](int r) { return n0 + (r & 127) < I ? (r & 127) + (r >> 7) * I : -1; });
   floatx16 acc[S::MW][S::NJ];
   tile_product<MI, true, false, false>(oa, ob, H, smem, acc);
-  const int c0 = n0 + S::first_col() + (threadIdx.x & 31);
+  constexpr int HALF = S::NJ / 2, COLS = HALF * 32;
+  const int c0 = n0 + S::first_col(), cols = I - c0;
+  if (cols <= 0) return;
 #pragma unroll
-  for (int i = 0; i < S::MW; ++i)
+  for (int i = 0; i < S::MW; ++i) {
+    const int r0 = S::first_row() + i * 32, rows = t.rows - r0;
+    if (rows <= 0) return;
+    // dH of the lane's row, all of it in flight at once; a lane past the tile or past I reads a
+    // place inside and its values are not stored
+    const float* drow = dh + static_cast<int64_t>(t.row0 + min(lane_row<MI, true>(i), t.rows - 1)) * I;
+    floatx4 d[HALF][4];
 #pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      const int r = tile_row<MI, true>(i, q);
-      if (r >= t.rows) continue;
-      const int64_t row = t.row0 + r;
+    for (int j = 0; j < HALF; ++j)
 #pragma unroll
-      for (int j = 0; j < S::NJ / 2; ++j) {
-        const int c = c0 + S::col(j);
-        if (c >= I) continue;
-        float dg, du, hv;
-        swiglu_grad(acc[i][j][q], acc[i][j + S::NJ / 2][q], dh[row * I + c], &dg, &du, &hv);
-        put(dgu + row * 2 * I + c, dg);
-        put(dgu + row * 2 * I + I + c, du);
-        put(h + row * I + c, hv);
-      }
-    }
+      for (int v = 0; v < 4; ++v)
+        d[j][v] = *reinterpret_cast<const floatx4*>(drow + min(c0 + j * 32 + lane_col(v), I - 4));
+    u32x2 du[HALF][4], hv[HALF][4];
+    const int64_t row = t.row0 + r0;
+    store_block<COLS>(smem, dgu + row * 2 * I + c0, 2 * I, rows, cols, [&](int j, int v) {
+      float a[4], b[4], c[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        swiglu_grad(acc[i][j][v * 4 + q], acc[i][j + HALF][v * 4 + q], d[j][v][q], &a[q], &b[q], &c[q]);
+      du[j][v] = pack4(b[0], b[1], b[2], b[3]);
+      hv[j][v] = pack4(c[0], c[1], c[2], c[3]);
+      return pack4(a[0], a[1], a[2], a[3]);
+    });
+    store_block<COLS>(smem, dgu + row * 2 * I + I + c0, 2 * I, rows, cols,
+                      [&](int j, int v) { return du[j][v]; });
+    store_block<COLS>(smem, h + row * I + c0, I, rows, cols, [&](int j, int v) { return hv[j][v]; });
+  }
 }
 
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void
@@ -441,18 +476,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
   floatx16 acc[S::MW][S::NJ];
   tile_product<0, false, true, true>(oa, ob, K, (lds_char*)smem, acc);
   uint16_t* C = reinterpret_cast<uint16_t*>(dw + slot * expert_bytes + c_off);
-  const int c0 = n0 + S::first_col() + (threadIdx.x & 31);
-#pragma unroll
-  for (int i = 0; i < S::MW; ++i)
-#pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      const int r = m0 + tile_row<0, false>(i, q);
-      if (r >= M) continue;
-      uint16_t* row = C + static_cast<int64_t>(r) * N;
-#pragma unroll
-      for (int j = 0; j < S::NJ; ++j)
-        if (c0 + S::col(j) < N) put(row + c0 + S::col(j), acc[i][j][q]);
-    }
+  store_tile<0>(acc, (lds_char*)smem, C + static_cast<int64_t>(m0) * N + n0, N, M - m0, N - n0);
 }
 
 struct Call {

@@ -19,6 +19,9 @@
 //   linearly, so both permutations are applied to the global address of each lane.
 // * The operands of the next 16 k are read while the MFMAs of the current 16 issue, one read or
 //   copy per MFMA.  One barrier a stage.
+// * The MFMAs compute the transposed block (B's columns as their rows), so a lane ends with four
+//   consecutive columns of one row: 16 bytes of an fp32 output, 8 of a bf16 one.  bf16 blocks go
+//   through LDS once more (store_block) and leave as 16-byte stores of whole row segments.
 #pragma once
 
 #include "common.h"
@@ -28,6 +31,9 @@ namespace moe {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef float floatx16 __attribute__((ext_vector_type(16)));
+typedef float floatx4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) char lds_char;
 
 constexpr int kStageK = 32, kStages = 4, kTileN = 256;
@@ -227,7 +233,7 @@ __device__ __forceinline__ void tile_product(
     for (int t = 0; t < NS; ++t) {
       if (t < NMF)
         acc[t / NJ % MW][t % NJ] =
-            __builtin_amdgcn_mfma_f32_32x32x16_bf16(pa[t / NJ % MW], pb[t % NJ], acc[t / NJ % MW][t % NJ], 0, 0, 0);
+            __builtin_amdgcn_mfma_f32_32x32x16_bf16(pb[t % NJ], pa[t / NJ % MW], acc[t / NJ % MW][t % NJ], 0, 0, 0);
       if (t < NRD) READ(qa, qb, t, cur, 1);
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -238,7 +244,7 @@ __device__ __forceinline__ void tile_product(
     for (int t = 0; t < NS; ++t) {
       if (t < NMF)
         acc[t / NJ % MW][t % NJ] =
-            __builtin_amdgcn_mfma_f32_32x32x16_bf16(qa[t / NJ % MW], qb[t % NJ], acc[t / NJ % MW][t % NJ], 0, 0, 0);
+            __builtin_amdgcn_mfma_f32_32x32x16_bf16(qb[t % NJ], qa[t / NJ % MW], acc[t / NJ % MW][t % NJ], 0, 0, 0);
       if (t < NRD) READ(pa, pb, t, next, 0);
 #pragma unroll
       for (int c = 0; c < NL; ++c)
@@ -251,16 +257,56 @@ __device__ __forceinline__ void tile_product(
 #undef COPY
 #undef NEXT_STAGE
 #undef READ
-  // no copy may land after the workgroup has ended
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  // the epilogue writes LDS: every wave's copies have landed and its reads are done
+  wait_copies_and_sync<0>();
 }
 
-// Row within the tile of element q of accumulator block i; columns are first_col() + col(j) +
-// lane % 32.
+// Row within the tile that this lane holds of accumulator block i, and the first of the four
+// consecutive columns, within block j, of its elements 4 v .. 4 v + 3.
 template <int MI, bool DUAL>
-__device__ __forceinline__ int tile_row(int i, int q) {
+__device__ __forceinline__ int lane_row(int i) {
+  return TileShape<MI, DUAL>::first_row() + i * 32 + (threadIdx.x & 31);
+}
+__device__ __forceinline__ int lane_col(int v) {
+  return v * 8 + ((threadIdx.x & 63) >> 5) * 4;
+}
+
+// 32 rows x COLS columns of bf16 from this wave's accumulators to memory.  put(j, v) gives the
+// four values of column block j, elements 4 v .. 4 v + 3, as packed bf16.  The LDS rows are padded
+// by 16 bytes, which spreads the 16 rows of a write over all banks.  out: the block's first row
+// and column; rows, cols: how many exist (cols a multiple of 8).
+template <int COLS, typename Put>
+__device__ __forceinline__ void store_block(lds_char* smem, uint16_t* out, int64_t ld, int rows,
+                                            int cols, Put put) {
+  constexpr int PITCH = COLS * 2 + 16, LANES = COLS / 8, PER = kWave / LANES;
+  typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
+  typedef __attribute__((address_space(3))) const u32x4 lds_u32x4;
   const int lane = threadIdx.x & (kWave - 1);
-  return TileShape<MI, DUAL>::first_row() + i * 32 + (q >> 2) * 8 + (lane >> 5) * 4 + (q & 3);
+  lds_char* mine = smem + (threadIdx.x / kWave) * 16384;
+#pragma unroll
+  for (int j = 0; j < COLS / 32; ++j)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      *reinterpret_cast<lds_u32x2*>(mine + (lane & 31) * PITCH + (j * 32 + lane_col(v)) * 2) = put(j, v);
+    }
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  const int c = (lane % LANES) * 8;
+#pragma unroll
+  for (int i = 0; i < 32 / PER; ++i) {
+    const int r = i * PER + lane / LANES;
+    const u32x4 d = *reinterpret_cast<lds_u32x4*>(mine + r * PITCH + c * 2);
+    if (r < rows && c < cols) *reinterpret_cast<u32x4*>(out + r * ld + c) = d;
+  }
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+__device__ __forceinline__ u32x2 pack4(float a, float b, float c, float d) {
+  return u32x2{f32_to_bf16(a) | (static_cast<uint32_t>(f32_to_bf16(b)) << 16),
+               f32_to_bf16(c) | (static_cast<uint32_t>(f32_to_bf16(d)) << 16)};
 }
 
 }  // namespace moe
