@@ -367,8 +367,8 @@ __device__ __forceinline__ void rows_product(const Tile& t, int n0, const uint16
   using S = TileShape<MI, false>;
   Operand<false, S::ROWS> oa;
   Operand<true, 256> ob;
-  oa.init(A + static_cast<int64_t>(t.row0) * lda, lda, [&](int r) { return r < t.rows ? r : -1; });
-  ob.init(B + n0, N, [&](int c) { return n0 + c < N ? c : -1; });
+  oa.init(A + static_cast<int64_t>(t.row0) * lda, lda, K, [&](int r) { return r < t.rows ? r : -1; });
+  ob.init(B + n0, N, K, [&](int c) { return n0 + c < N ? c : -1; });
   floatx16 acc[S::MW][S::NJ];
   tile_product<MI, false, false, true>(oa, ob, K, smem, acc);
   store_tile<MI>(acc, smem, C + static_cast<int64_t>(t.row0) * N + n0, N, t.rows, N - n0);
@@ -398,8 +398,8 @@ __device__ __forceinline__ void gate_up_backward(const Tile& t, int n0, const ui
   using S = TileShape<MI, true>;
   Operand<false, S::ROWS> oa;
   Operand<false, 256> ob;
-  oa.init(x + static_cast<int64_t>(t.row0) * H, H, [&](int r) { return r < t.rows ? r : -1; });
-  ob.init(W + static_cast<int64_t>(n0) * H, H,
+  oa.init(x + static_cast<int64_t>(t.row0) * H, H, H, [&](int r) { return r < t.rows ? r : -1; });
+  ob.init(W + static_cast<int64_t>(n0) * H, H, H,
           [&](int r) { return n0 + (r & 127) < I ? (r & 127) + (r >> 7) * I : -1; });
   floatx16 acc[S::MW][S::NJ];
   tile_product<MI, true, false, false>(oa, ob, H, smem, acc);
@@ -471,8 +471,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
   const int K = __builtin_amdgcn_readfirstlane(expert_rows(offsets, e, R, &lo));
   lo = __builtin_amdgcn_readfirstlane(lo);
   Operand<true, 256> oa, ob;
-  oa.init(A + static_cast<int64_t>(lo) * M + m0, M, [&](int c) { return m0 + c < M ? c : -1; });
-  ob.init(B + static_cast<int64_t>(lo) * N + n0, N, [&](int c) { return n0 + c < N ? c : -1; });
+  oa.init(A + static_cast<int64_t>(lo) * M + m0, M, K, [&](int c) { return m0 + c < M ? c : -1; });
+  ob.init(B + static_cast<int64_t>(lo) * N + n0, N, K, [&](int c) { return n0 + c < N ? c : -1; });
   floatx16 acc[S::MW][S::NJ];
   tile_product<0, false, true, true>(oa, ob, K, (lds_char*)smem, acc);
   uint16_t* C = reinterpret_cast<uint16_t*>(dw + slot * expert_bytes + c_off);

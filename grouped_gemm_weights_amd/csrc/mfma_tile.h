@@ -24,6 +24,8 @@
 //   through LDS once more (store_block) and leave as 16-byte stores of whole row segments.
 #pragma once
 
+#include <type_traits>
+
 #include "common.h"
 
 namespace moe {
@@ -42,16 +44,15 @@ constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kTileLds = kStages * kStageBytes;         // 128 KB
 constexpr uint32_t kOutside = 0x80000000u;              // lane offsets from here on read zeros
 
-// 16 bytes per lane from base + voff to LDS at `lds` + 16 lane (wave-uniform).  The scalar move of
-// m0 needs one wait state before the copy reads it.
-__device__ __forceinline__ void copy_to_lds(const void* base, uint32_t voff, uint32_t lds) {
-  __amdgpu_buffer_rsrc_t r =
-      __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, kOutside, 0x00020000);
+// 16 bytes per lane from buffer r + voff to LDS at `lds` + OFF + 16 lane (lds wave-uniform).  The
+// scalar write of m0 needs one wait state before the copy reads it.
+template <int OFF>
+__device__ __forceinline__ void copy_to_lds(u32x4 r, uint32_t voff, uint32_t lds) {
   asm volatile(
-      "s_mov_b32 m0, %0\n\t"
+      "s_add_u32 m0, %0, %3\n\t"
       "s_nop 0\n\t"
-      "buffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(voff), "s"(r)
-      : "memory");
+      "buffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(voff), "s"(r), "n"(OFF)
+      : "memory", "scc");
 }
 
 template <int N>
@@ -59,24 +60,31 @@ __device__ __forceinline__ void wait_copies_and_sync() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-// One operand: how its stages are copied and its fragments read.  COLS: a column operand.
-// ROWS: rows (or, for a column operand, columns) of the tile that are staged.
+// One operand: how its stages are copied.  COLS: a column operand.  ROWS: rows (or, for a column
+// operand, columns) of the tile that are staged.
 template <bool COLS, int ROWS>
 struct Operand {
-  static constexpr int N = COLS ? 4 : ROWS / 64;  // copies per wave and stage
-  const char* base;    // wave-uniform: where the stage to issue next starts
-  int64_t step;        // bytes from a stage to the next
-  uint32_t voff[N];    // this lane's offset in each copy, kOutside for a row it does not have
+  static constexpr int N = COLS ? 4 : ROWS / 64;           // copies per wave and stage
+  static constexpr int WAVE_STEP = COLS ? 4096 : 1024;     // LDS bytes from a wave's copy to the next wave's
+  static constexpr int COPY_STEP = COLS ? 1024 : 4096;     // and from a wave's copy to its next
+  uint64_t base;       // wave-uniform: where the stage to issue next starts
+  uint32_t step;       // bytes from a stage to the next
+  int left;            // steps of depth from there on
+  uint32_t voff[N];    // this lane's offset in each copy, kOutside for what does not exist
   int k_at;            // depth of this lane's copy 0 within a stage
 
-  // Row operand: tile row r is at base + src(r) * ld elements, src(r) < 0 for none.
-  // Column operand: depth k is at base + k * ld, tile column c at src(c), 8 columns at a time.
+  // Row operand: tile row r is at p + src(r) * ld elements, src(r) < 0 for none.
+  // Column operand: depth k is at p + k * ld, tile column c at src(c), 8 columns at a time.
   template <typename Src>
-  __device__ __forceinline__ void init(const uint16_t* p, int64_t ld, Src src) {
+  __device__ __forceinline__ void init(const uint16_t* p, int64_t ld, int K, Src src) {
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-    base = reinterpret_cast<const char*>(p);
+    const uint64_t at = reinterpret_cast<uint64_t>(p);
+    base = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at))) |
+           static_cast<uint64_t>(static_cast<uint32_t>(
+               __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at >> 32)))) << 32;
+    left = K;
     if constexpr (COLS) {
-      step = kStageK * ld * 2;
+      step = static_cast<uint32_t>(kStageK * ld * 2);
       k_at = wave * 8 + (lane >> 5);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
@@ -94,14 +102,30 @@ struct Operand {
         voff[i] = r < 0 ? kOutside : static_cast<uint32_t>(r * ld + k_at) * 2u;
       }
     }
+    bound();
   }
 
-  // Copy i of the stage at `base`, of which `left` steps of depth exist.
-  __device__ __forceinline__ void copy(int i, int left, uint32_t lds) const {
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const bool in = k_at + (COLS ? 2 * i : 0) < left;
-    copy_to_lds(base, in ? voff[i] : kOutside,
-                lds + (COLS ? (wave * 4 + i) * 1024 : (i * 4 + wave) * 1024));
+  // The last stage may be short and the ones after it are empty: lanes past the depth copy zeros
+  // from there on.
+  __device__ __forceinline__ void bound() {
+    if (left < kStageK) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (k_at + (COLS ? 2 * i : 0) >= left) voff[i] = kOutside;
+    }
+  }
+  __device__ __forceinline__ void next_stage() {
+    base += step;
+    left -= kStageK;
+    bound();
+  }
+
+  // Copy I of the stage at `base` to LDS offset OFF (the operand's stage buffer); lds is this
+  // wave's place: the tile's LDS + wave * WAVE_STEP.
+  template <int I, int OFF>
+  __device__ __forceinline__ void copy(uint32_t lds) const {
+    const u32x4 r = {static_cast<uint32_t>(base), static_cast<uint32_t>(base >> 32), kOutside, 0x00020000u};
+    copy_to_lds<OFF + I * COPY_STEP>(r, voff[I], lds);
   }
 };
 
@@ -110,30 +134,31 @@ struct Operand {
 template <bool COLS, int BLOCKS>
 struct Fragments {
   static constexpr int N = COLS ? BLOCKS : 2;
-  int at[N];
+  int at[2][N];  // for stages 0, 1 and 2, 3: an LDS read's own offset reaches 64 KB
 
   // first(b): tile row (column) of block b, a multiple of 32; for rows, first(b) - first(0) is
-  // a compile-time constant.
+  // a compile-time constant.  lds: the operand's buffer of stage 0.
   template <typename First>
-  __device__ __forceinline__ void init(First first) {
+  __device__ __forceinline__ void init(int lds, First first) {
     const int lane = threadIdx.x & (kWave - 1);
-    if constexpr (COLS) {
-      const int k = (lane >> 5) * 8 + ((lane & 15) >> 2);
 #pragma unroll
-      for (int b = 0; b < BLOCKS; ++b)
-        at[b] = k * 512 + (((first(b) >> 4) + ((lane >> 4) & 1)) ^ (2 * (k & 3))) * 32 + (lane & 3) * 8;
-    } else {
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-        at[s] = (first(0) + (lane & 31)) * 64 + ((s * 2 + (lane >> 5)) ^ ((lane >> 2) & 3)) * 16;
+    for (int i = 0; i < N; ++i) {
+      if constexpr (COLS) {
+        const int k = (lane >> 5) * 8 + ((lane & 15) >> 2);
+        at[0][i] = lds + k * 512 + (((first(i) >> 4) + ((lane >> 4) & 1)) ^ (2 * (k & 3))) * 32 + (lane & 3) * 8;
+      } else {
+        at[0][i] = lds + (first(0) + (lane & 31)) * 64 + ((i * 2 + (lane >> 5)) ^ ((lane >> 2) & 3)) * 16;
+      }
+      at[1][i] = at[0][i] + 2 * kStageBytes;
     }
   }
 
-  // Block b (delta rows from block 0) of the 16 k at half s of the stage at `lds`.
-  __device__ __forceinline__ bf16x8 read(const lds_char* lds, int b, int delta, int s) const {
+  // Block b (delta rows from block 0) of the 16 k at half s of stage buffer `buf`.
+  __device__ __forceinline__ bf16x8 read(int buf, int b, int delta, int s) const {
+    const int off = (buf & 1) * kStageBytes;
     if constexpr (COLS) {
       typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
-      const lds_char* p = lds + at[b] + s * 16 * 512;
+      const lds_char* p = reinterpret_cast<const lds_char*>(at[buf >> 1][b]) + off + s * 16 * 512;
       union {
         i16x4 h[2];
         bf16x8 v;
@@ -145,7 +170,7 @@ struct Fragments {
       return u.v;
     } else {
       typedef const __attribute__((address_space(3))) bf16x8 lds_bf16x8;
-      return *reinterpret_cast<lds_bf16x8*>(lds + at[s] + delta * 64);
+      return *reinterpret_cast<lds_bf16x8*>(reinterpret_cast<const lds_char*>(at[buf >> 1][s]) + off + delta * 64);
     }
   }
 };
@@ -169,96 +194,120 @@ struct TileShape {
   }
 };
 
+// Calls f(integral_constant<int, I>) for I in [LO, HI).
+template <int LO, int HI, typename F>
+__device__ __forceinline__ void each(F f) {
+  if constexpr (LO < HI) {
+    f(std::integral_constant<int, LO>{});
+    each<LO + 1, HI>(f);
+  }
+}
+
+template <int MI, bool DUAL, bool A_COLS, bool B_COLS>
+struct TileProduct {
+  using S = TileShape<MI, DUAL>;
+  using OA = Operand<A_COLS, S::ROWS>;
+  using OB = Operand<B_COLS, 256>;
+  static constexpr int MW = S::MW, NJ = S::NJ;
+  static constexpr int NA = OA::N, NL = NA + OB::N;   // copies per wave and stage
+  static constexpr int NF = NL / 2;                   // of these, issued in a stage's second half
+  static constexpr int NMF = MW * NJ, NRD = MW + NJ;  // MFMAs and fragments per 16 k
+  static constexpr int NS = NMF > NRD ? NMF : NRD;
+  OA& A;
+  OB& B;
+  floatx16 (&acc)[MW][NJ];
+  Fragments<A_COLS, MW> fa;
+  Fragments<B_COLS, NJ> fb;
+  uint32_t lds_a, lds_b;
+  bf16x8 pa[MW], pb[NJ], qa[MW], qb[NJ];
+
+  template <int C, int BUF>
+  __device__ __forceinline__ void copy() {
+    if constexpr (C < NA) A.template copy<C, BUF * kStageBytes>(lds_a);
+    else B.template copy<C - NA, BUF * kStageBytes + kOperandBytes>(lds_b);
+  }
+  __device__ __forceinline__ void next_stage() {
+    A.next_stage();
+    B.next_stage();
+  }
+  __device__ __forceinline__ void read(bf16x8 (&ra)[MW], bf16x8 (&rb)[NJ], int t, int buf, int s) {
+    if (t < MW) ra[t % MW] = fa.read(buf, t % MW, t % MW * 32, s);
+    else rb[(t - MW) % NJ] = fb.read(buf, (t - MW) % NJ, S::col((t - MW) % NJ), s);
+  }
+
+  // The 16 k held in (ra, rb): one MFMA per slot; beside them the reads of the 16 k at half s of
+  // stage buffer RBUF into (na, nb), and copies LO .. HI - 1 of the stage to issue into CBUF.
+  template <int RBUF, int RS, int CBUF, int LO, int HI>
+  __device__ __forceinline__ void half(bf16x8 (&ra)[MW], bf16x8 (&rb)[NJ], bf16x8 (&na)[MW],
+                                       bf16x8 (&nb)[NJ]) {
+    each<0, NS>([&](auto slot) {
+      constexpr int t = decltype(slot)::value;
+      if constexpr (t < NMF)
+        acc[t / NJ][t % NJ] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(rb[t % NJ], ra[t / NJ],
+                                                                     acc[t / NJ][t % NJ], 0, 0, 0);
+      if constexpr (t < NRD) read(na, nb, t, RBUF, RS);
+      each<LO, HI>([&](auto c) {
+        if constexpr ((decltype(c)::value - LO) * NS / (HI - LO) == t) copy<decltype(c)::value, CBUF>();
+      });
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  }
+
+  // One stage, in buffer BUF.  Its first half also issues the second part of the copies of the
+  // stage three ahead.  Then this wave's copies of the next stage are there and its reads of this
+  // one done; past the barrier that holds for every wave, and this buffer takes the stage four ahead.
+  template <int BUF>
+  __device__ __forceinline__ void stage() {
+    half<BUF, 1, (BUF + 3) % kStages, NF, NL>(pa, pb, qa, qb);
+    next_stage();
+    wait_copies_and_sync<2 * NL>();
+    half<(BUF + 1) % kStages, 0, BUF, 0, NF>(qa, qb, pa, pb);
+  }
+
+  __device__ __forceinline__ void run(int K, lds_char* smem) {
+#pragma unroll
+    for (int i = 0; i < MW; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
+    if (K <= 0) return;
+    const int lds = static_cast<int>(reinterpret_cast<uintptr_t>(smem));
+    fa.init(lds, [](int b) { return S::first_row() + b * 32; });
+    fb.init(lds + kOperandBytes, [](int b) { return S::first_col() + S::col(b); });
+    lds_a = lds + S::wave() * OA::WAVE_STEP;
+    lds_b = lds + S::wave() * OB::WAVE_STEP;
+    // the stages past the last are copied too, as zeros: the copies in flight stay countable
+    each<0, kStages>([&](auto s) {
+      constexpr int BUF = decltype(s)::value;
+      each<0, (BUF < kStages - 1 ? NL : NF)>([&](auto c) { copy<decltype(c)::value, BUF>(); });
+      if constexpr (BUF < kStages - 1) next_stage();
+    });
+    wait_copies_and_sync<2 * NL + NF>();
+#pragma unroll
+    for (int t = 0; t < NRD; ++t) read(pa, pb, t, 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    int stages = (K + kStageK - 1) / kStageK;
+    for (; stages >= kStages; stages -= kStages) {
+      stage<0>();
+      stage<1>();
+      stage<2>();
+      stage<3>();
+    }
+    if (stages > 0) stage<0>();
+    if (stages > 1) stage<1>();
+    if (stages > 2) stage<2>();
+    // the epilogue writes LDS: every wave's copies have landed and its reads are done
+    wait_copies_and_sync<0>();
+  }
+};
+
 template <int MI, bool DUAL, bool A_COLS, bool B_COLS>
 __device__ __forceinline__ void tile_product(
     Operand<A_COLS, TileShape<MI, DUAL>::ROWS>& A, Operand<B_COLS, 256>& B, int K, lds_char* smem,
     floatx16 (&acc)[TileShape<MI, DUAL>::MW][TileShape<MI, DUAL>::NJ]) {
-  using S = TileShape<MI, DUAL>;
-  constexpr int MW = S::MW, NJ = S::NJ;
-  constexpr int NA = Operand<A_COLS, S::ROWS>::N, NL = NA + Operand<B_COLS, 256>::N;
-  constexpr int NMF = MW * NJ, NRD = MW + NJ;
-  constexpr int NS = NMF > NRD ? NMF : NRD;
-  Fragments<A_COLS, MW> fa;
-  Fragments<B_COLS, NJ> fb;
-  fa.init([](int b) { return S::first_row() + b * 32; });
-  fb.init([](int b) { return S::first_col() + S::col(b); });
-  const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(smem));
-
-#pragma unroll
-  for (int i = 0; i < MW; ++i)
-#pragma unroll
-    for (int j = 0; j < NJ; ++j)
-#pragma unroll
-      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
-  const int nk = (K + kStageK - 1) / kStageK;
-  if (nk == 0) return;
-
-  // the stages past the last are copied too, as zeros: the copies in flight stay countable
-  int left = K;
-#define COPY(c, buf)                                                                     \
-  do {                                                                                   \
-    if ((c) < NA) A.copy((c) % NA, left, lds0 + (buf) * kStageBytes);                    \
-    else B.copy(((c) - NA) % (NL - NA), left, lds0 + (buf) * kStageBytes + kOperandBytes); \
-  } while (0)
-#define NEXT_STAGE()   \
-  do {                 \
-    A.base += A.step;  \
-    B.base += B.step;  \
-    left -= kStageK;   \
-  } while (0)
-#pragma unroll
-  for (int s = 0; s < kStages; ++s) {
-#pragma unroll
-    for (int c = 0; c < NL; ++c) COPY(c, s);
-    NEXT_STAGE();
-  }
-  bf16x8 pa[MW], pb[NJ], qa[MW], qb[NJ];
-#define READ(RA, RB, t, stage, s)                                                        \
-  do {                                                                                   \
-    if ((t) < MW) RA[(t) % MW] = fa.read(stage, (t) % MW, ((t) % MW) * 32, s);           \
-    else RB[((t) - MW) % NJ] = fb.read((stage) + kOperandBytes, ((t) - MW) % NJ,         \
-                                       S::col(((t) - MW) % NJ), s);                      \
-  } while (0)
-  wait_copies_and_sync<3 * NL>();
-#pragma unroll
-  for (int t = 0; t < NRD; ++t) READ(pa, pb, t, smem, 0);
-  __builtin_amdgcn_sched_barrier(0);
-
-  int buf = 0;
-  for (int kt = 0; kt < nk; ++kt) {
-    const lds_char* cur = smem + buf * kStageBytes;
-    const int nbuf = (buf + 1) % kStages;
-    const lds_char* next = smem + nbuf * kStageBytes;
-#pragma unroll
-    for (int t = 0; t < NS; ++t) {
-      if (t < NMF)
-        acc[t / NJ % MW][t % NJ] =
-            __builtin_amdgcn_mfma_f32_32x32x16_bf16(pb[t % NJ], pa[t / NJ % MW], acc[t / NJ % MW][t % NJ], 0, 0, 0);
-      if (t < NRD) READ(qa, qb, t, cur, 1);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    // this wave's copies of stage kt + 1 are there and its reads of stage kt done; past the
-    // barrier that holds for every wave, and stage kt's buffer takes stage kt + 4
-    wait_copies_and_sync<2 * NL>();
-#pragma unroll
-    for (int t = 0; t < NS; ++t) {
-      if (t < NMF)
-        acc[t / NJ % MW][t % NJ] =
-            __builtin_amdgcn_mfma_f32_32x32x16_bf16(qb[t % NJ], qa[t / NJ % MW], acc[t / NJ % MW][t % NJ], 0, 0, 0);
-      if (t < NRD) READ(pa, pb, t, next, 0);
-#pragma unroll
-      for (int c = 0; c < NL; ++c)
-        if (c * NS / NL == t) COPY(c, buf);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    NEXT_STAGE();
-    buf = nbuf;
-  }
-#undef COPY
-#undef NEXT_STAGE
-#undef READ
-  // the epilogue writes LDS: every wave's copies have landed and its reads are done
-  wait_copies_and_sync<0>();
+  TileProduct<MI, DUAL, A_COLS, B_COLS> p{A, B, acc};
+  p.run(K, smem);
 }
 
 // Row within the tile that this lane holds of accumulator block i, and the first of the four
