@@ -120,50 +120,68 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(
   }
 }
 
-// Backward over rows [blockIdx.x, rows) in steps of gridDim.x; a block's threads own fixed
-// columns, so the sums over its rows for dgamma and dbeta stay in registers and leave as one
-// partial row of 2 H floats per block (partial != nullptr).
+// Backward.  WPR waves share a row; a group of WPR waves takes rows `group`, `group` + groups, ...
+// and its lanes own fixed columns, so the sums over its rows for dgamma and dbeta stay in
+// registers; a block's groups (WPR = 1: four) are joined in LDS and leave as one partial row of
+// 2 H floats (partial != nullptr).  The next row's loads are issued before this row's sums, so
+// they are in flight while the waves wait for one another.
 template <typename T, int WPR, int NV>
-__global__ __launch_bounds__(WPR* kWave) void norm_backward_kernel(
+__global__ __launch_bounds__(WPR == 1 ? 256 : WPR * kWave) void norm_backward_kernel(
     const T* __restrict__ dy, const T* __restrict__ x, const float* __restrict__ gamma,
     const float* __restrict__ mean, const float* __restrict__ rstd, int rows, int H,
     T* __restrict__ dx, float* __restrict__ partial) {
+  constexpr int GROUPS = WPR == 1 ? 4 : 1, LANES = WPR * kWave;
   __shared__ float part[2][2][WPR];
-  const int tid = threadIdx.x;
-  float sg[NV][kVec], sb[NV][kVec];
+  __shared__ float joined[GROUPS > 1 ? 2 * LANES * NV * kVec : 1];
+  const int tid = threadIdx.x % LANES;
+  const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / LANES);
+  const int step = gridDim.x * GROUPS;
+  float sg[NV][kVec], sb[NV][kVec], g[NV][kVec];
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+  for (int i = 0; i < NV; ++i) {
+    load8<false>(gamma, tid + i * LANES, H, g[i]);
 #pragma unroll
     for (int j = 0; j < kVec; ++j) sg[i][j] = sb[i][j] = 0.f;
-  int turn = 0;
-  for (int row = blockIdx.x; row < rows; row += gridDim.x, turn ^= 1) {
-    const T* xr = x + static_cast<int64_t>(row) * H;
-    const T* dr = dy + static_cast<int64_t>(row) * H;
-    const float mu = mean[row], r = rstd[row];
+  }
+  int row = blockIdx.x * GROUPS + group;
+  Raw8<T> xn[NV], dn[NV];
+  float mu_n = 0.f, r_n = 0.f;
+  auto fetch = [&](int r) {
+    mu_n = mean[r];
+    r_n = rstd[r];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      load_raw<true>(x + static_cast<int64_t>(r) * H, tid + i * LANES, H, xn[i]);
+      load_raw<true>(dy + static_cast<int64_t>(r) * H, tid + i * LANES, H, dn[i]);
+    }
+  };
+  if (row < rows) fetch(row);
+  for (int turn = 0; row < rows; row += step, turn ^= 1) {
+    const float mu = mu_n, r = r_n;
     float a[NV][kVec], xh[NV][kVec];
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int at = tid + i * WPR * kWave;
-      float g[kVec];
-      load8<true>(xr, at, H, xh[i]);
-      load8<true>(dr, at, H, a[i]);
-      load8<false>(gamma, at, H, g);
+      unpack(xn[i], xh[i]);
+      unpack(dn[i], a[i]);
+    }
+    if (row + step < rows) fetch(row + step);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int j = 0; j < kVec; ++j) {
         // past the row a is zero, so what xh holds there does not count
         xh[i][j] = (xh[i][j] - mu) * r;
         sg[i][j] = fmaf(a[i][j], xh[i][j], sg[i][j]);
         sb[i][j] += a[i][j];
-        a[i][j] *= g[j];
+        a[i][j] *= g[i][j];
         s1 += a[i][j];
         s2 = fmaf(a[i][j], xh[i][j], s2);
       }
-    }
-    // the buffers alternate from row to row, so one barrier a row is enough
     s1 = wave_sum(s1);
     s2 = wave_sum(s2);
     if (WPR > 1) {
+      // the buffers alternate from row to row, so one barrier a row is enough
       if ((tid & (kWave - 1)) == 0) {
         part[turn][0][tid / kWave] = s1;
         part[turn][1][tid / kWave] = s2;
@@ -183,16 +201,35 @@ __global__ __launch_bounds__(WPR* kWave) void norm_backward_kernel(
     for (int i = 0; i < NV; ++i) {
 #pragma unroll
       for (int j = 0; j < kVec; ++j) a[i][j] = r * (a[i][j] - s1 - xh[i][j] * s2);
-      store8<true>(out, tid + i * WPR * kWave, H, a[i]);
+      store8<true>(out, tid + i * LANES, H, a[i]);
     }
   }
-  if (partial) {
-    float* p = partial + static_cast<int64_t>(blockIdx.x) * 2 * H;
+  if (!partial) return;
+  if (GROUPS > 1) {
+    // the groups add their sums in group order
+    for (int k = 0; k < GROUPS; ++k) {
+      if (group == k)
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      store8<false>(p, tid + i * WPR * kWave, H, sg[i]);
-      store8<false>(p + H, tid + i * WPR * kWave, H, sb[i]);
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int j = 0; j < kVec; ++j) {
+            float* at = joined + ((i * kVec + j) * 2) * LANES + tid;
+            if (k > 0) {
+              sg[i][j] += at[0];
+              sb[i][j] += at[LANES];
+            }
+            at[0] = sg[i][j];
+            at[LANES] = sb[i][j];
+          }
+      __syncthreads();
     }
+    if (group != GROUPS - 1) return;
+  }
+  float* p = partial + static_cast<int64_t>(blockIdx.x) * 2 * H;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    store8<false>(p, tid + i * LANES, H, sg[i]);
+    store8<false>(p + H, tid + i * LANES, H, sb[i]);
   }
 }
 
@@ -323,7 +360,7 @@ int norm(const void* x, const float* gamma, const float* beta, int T, int H, flo
 template <typename E, int WPR, int NV>
 int launch_norm_backward(const void* dy, const void* x, const float* gamma, const float* mean,
                          const float* rstd, int T, int H, void* dx, float* partial, hipStream_t s) {
-  hipLaunchKernelGGL((norm_backward_kernel<E, WPR, NV>), dim3(norm_partials(T)), dim3(WPR * kWave), 0, s,
+  hipLaunchKernelGGL((norm_backward_kernel<E, WPR, NV>), dim3(norm_partials(T)), dim3(WPR == 1 ? 256 : WPR * kWave), 0, s,
                      static_cast<const E*>(dy), static_cast<const E*>(x), gamma, mean, rstd, T, H,
                      static_cast<E*>(dx), partial);
   MOE_LAUNCH_CHECK("moe_layer_norm_backward: launch");
@@ -337,8 +374,8 @@ int norm_backward(const void* dy, const void* x, const float* gamma, const float
   if (H <= 512) NORM(1, 1);
   if (H <= 1024) NORM(1, 2);
   if (H <= 2048) NORM(4, 1);
-  if (H <= 4096) NORM(4, 2);
-  if (H <= 8192) NORM(4, 4);
+  if (H <= 4096) NORM(8, 1);
+  if (H <= 8192) NORM(16, 1);
   if (H <= 16384) NORM(16, 2);
 #undef NORM
   hipLaunchKernelGGL(norm_backward_long_kernel<E>, dim3(T), dim3(1024), 0, s, static_cast<const E*>(dy),
