@@ -6,6 +6,8 @@
 // (k independent 16-byte loads in flight per step) and accumulates in j order
 // with fused multiply-adds.  Every y_perm row is read exactly once, so its loads
 // are non-temporal (9 % faster on prefill-sized layers than cached loads).
+#include <algorithm>
+
 #include "rows.h"
 
 namespace moe {
@@ -65,69 +67,97 @@ __global__ __launch_bounds__(256) void residual_kernel(const uint16_t* x, const 
 // Gradient of y[t] = sum_j w[t][j] y_perm[row_of[t k + j]]:
 //   dy_perm[row] = w[t][j] dy[t],   dw[t][j] = <dy[t], y_perm[row]>.
 // Bound by HBM: y_perm is read once (4 R H bytes) and dy_perm written once, so both bypass the
-// caches; dy[t] stays in registers for the token's k rows.  One block per token; a wave's share
-// of a dot product goes to its own LDS slot, so the k sums cost one barrier, and the slots are
-// added in wave order (the same bits every run).
-constexpr int kCbVecs = 4;  // vectors of 8 columns a thread holds: 8192 columns per sweep
-
-template <typename D, typename O>
-__global__ __launch_bounds__(256) void combine_backward_kernel(
+// caches; dy[t] stays in registers for the token's k rows.  A token has one to four waves, each
+// lane NV vectors of 8 columns and sweep; a wave's share of a dot product goes to its own LDS
+// slot, so the k sums cost one barrier, and the slots are added in wave order (the same bits
+// every run).  Tokens of one wave go four to a block.  TAIL: H is not a multiple of 8.
+template <typename D, typename O, int NV, int WAVES, bool TAIL>
+__global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * kWave) void combine_backward_kernel(
     const D* __restrict__ dy, const float* __restrict__ y_perm, const int32_t* __restrict__ row_of,
     const float* __restrict__ topk_w, int T, int k, int H, O* __restrict__ dy_perm,
     float* __restrict__ dtopk_w) {
   __shared__ float dot[MOE_MAX_K][4];
-  const int t = blockIdx.x;
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int t = WAVES == 1 ? blockIdx.x * 4 + wave : blockIdx.x;
+  if (t >= T) return;
+  constexpr int threads = WAVES * kWave;
+  const int tid = WAVES == 1 ? lane : threadIdx.x;
   const int64_t R = static_cast<int64_t>(T) * k;
+  const int32_t* rows = row_of + static_cast<int64_t>(t) * k;
+  const float* ws = topk_w + static_cast<int64_t>(t) * k;
   const D* dr = dy + static_cast<int64_t>(t) * H;
-  for (int c0 = 0; c0 == 0 || c0 * kVec < H; c0 += kCbVecs * 256) {
-    float d[kCbVecs][kVec];
+  const int pieces = (H + kVec - 1) / kVec;
+  for (int c0 = 0; c0 < pieces; c0 += NV * threads) {
+    float d[NV][kVec];
 #pragma unroll
-    for (int i = 0; i < kCbVecs; ++i) load8<true>(dr, c0 + threadIdx.x + i * 256, H, d[i]);
+    for (int i = 0; i < NV; ++i) load8<true, TAIL>(dr, c0 + tid + i * threads, H, d[i]);
     for (int j = 0; j < k; ++j) {
-      const int r = row_of[static_cast<int64_t>(t) * k + j];
+      const int r = rows[j];
+      const float w = ws[j];
       // an unwritten row index (after an out-of-range expert id) must not fault
       const bool ok = r >= 0 && r < R;
-      const float w = topk_w[static_cast<int64_t>(t) * k + j];
       float s = 0.f;
       if (ok) {
         O* out = dy_perm + static_cast<int64_t>(r) * H;
-        const float* yr = y_perm + static_cast<int64_t>(r) * H;
+        if (dtopk_w) {
+          const float* yr = y_perm + static_cast<int64_t>(r) * H;
+          Raw8<float> y[NV];
 #pragma unroll
-        for (int i = 0; i < kCbVecs; ++i) {
-          const int at = c0 + threadIdx.x + i * 256;
-          float v[kVec];
-          if (dtopk_w) {
-            load8<true>(yr, at, H, v);
+          for (int i = 0; i < NV; ++i) load_raw<true, TAIL>(yr, c0 + tid + i * threads, H, y[i]);
 #pragma unroll
-            for (int q = 0; q < kVec; ++q) s = fmaf(d[i][q], v[q], s);
+          for (int i = 0; i < NV; ++i) {
+            float f[kVec];
+            unpack<TAIL>(y[i], c0 + tid + i * threads, H, f);
+#pragma unroll
+            for (int q = 0; q < kVec; ++q) s = fmaf(d[i][q], f[q], s);
           }
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          float v[kVec];
 #pragma unroll
           for (int q = 0; q < kVec; ++q) v[q] = w * d[i][q];
-          store8<true>(out, at, H, v);
+          store8<true, TAIL>(out, c0 + tid + i * threads, H, v);
         }
       }
       if (dtopk_w) {
         s = wave_sum(s);
-        if (lane == 0) dot[j][wave] = c0 ? dot[j][wave] + s : s;
+        if (lane == 0) {
+          if (WAVES == 1) dtopk_w[static_cast<int64_t>(t) * k + j] = s;  // one sweep: the whole sum
+          else dot[j][wave] = c0 ? dot[j][wave] + s : s;
+        }
       }
     }
   }
-  if (dtopk_w) {
+  if (dtopk_w && WAVES > 1) {
     __syncthreads();
     const int j = threadIdx.x;
-    if (j < k)
-      dtopk_w[static_cast<int64_t>(t) * k + j] = (dot[j][0] + dot[j][1]) + (dot[j][2] + dot[j][3]);
+    if (j < k) {
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < WAVES; ++i) s += dot[j][i];
+      dtopk_w[static_cast<int64_t>(t) * k + j] = s;
+    }
   }
 }
 
-template <typename D, typename O>
+template <typename D, typename O, bool TAIL>
 void launch_combine_backward(const void* dy, const float* y_perm, const int32_t* row_of,
                              const float* topk_w, int T, int k, int H, void* dy_perm, float* dtopk_w,
                              hipStream_t s) {
-  hipLaunchKernelGGL((combine_backward_kernel<D, O>), dim3(T), dim3(256), 0, s,
-                     static_cast<const D*>(dy), y_perm, row_of, topk_w, T, k, H,
-                     static_cast<O*>(dy_perm), dtopk_w);
+  const int pieces = ceil_div(H, kVec);
+  // one vector a lane up to 4 waves, then two and four; rows over 8192 columns are swept
+  auto kernel = pieces <= 64    ? combine_backward_kernel<D, O, 1, 1, TAIL>
+                : pieces <= 128 ? combine_backward_kernel<D, O, 1, 2, TAIL>
+                : pieces <= 192 ? combine_backward_kernel<D, O, 1, 3, TAIL>
+                : pieces <= 256 ? combine_backward_kernel<D, O, 1, 4, TAIL>
+                : pieces <= 512 ? combine_backward_kernel<D, O, 2, 4, TAIL>
+                                : combine_backward_kernel<D, O, 4, 4, TAIL>;
+  const int waves = std::min(ceil_div(pieces, kWave), 4);
+  hipLaunchKernelGGL(kernel, dim3(waves == 1 ? ceil_div(T, 4) : T),
+                     dim3(waves == 1 ? 256 : waves * kWave), 0, s, static_cast<const D*>(dy), y_perm,
+                     row_of, topk_w, T, k, H, static_cast<O*>(dy_perm), dtopk_w);
 }
 
 }  // namespace
@@ -166,14 +196,17 @@ extern "C" int moe_combine_backward(const void* dy, moe_dtype dy_dtype, const fl
   if (!dy || !row_of || !topk_w || !dy_perm || (dtopk_w && !y_perm))
     return fail(MOE_ERR_ARG, "moe_combine_backward: null pointer");
   hipStream_t s = as_stream(stream);
+  auto launch = H % kVec == 0 ? launch_combine_backward<uint16_t, uint16_t, false>
+                              : launch_combine_backward<uint16_t, uint16_t, true>;
   if (dy_dtype == MOE_F32 && dtype == MOE_F32)
-    launch_combine_backward<float, float>(dy, y_perm, row_of, topk_w, T, k, H, dy_perm, dtopk_w, s);
+    launch = H % kVec == 0 ? launch_combine_backward<float, float, false> : launch_combine_backward<float, float, true>;
   else if (dy_dtype == MOE_F32)
-    launch_combine_backward<float, uint16_t>(dy, y_perm, row_of, topk_w, T, k, H, dy_perm, dtopk_w, s);
+    launch = H % kVec == 0 ? launch_combine_backward<float, uint16_t, false>
+                           : launch_combine_backward<float, uint16_t, true>;
   else if (dtype == MOE_F32)
-    launch_combine_backward<uint16_t, float>(dy, y_perm, row_of, topk_w, T, k, H, dy_perm, dtopk_w, s);
-  else
-    launch_combine_backward<uint16_t, uint16_t>(dy, y_perm, row_of, topk_w, T, k, H, dy_perm, dtopk_w, s);
+    launch = H % kVec == 0 ? launch_combine_backward<uint16_t, float, false>
+                           : launch_combine_backward<uint16_t, float, true>;
+  launch(dy, y_perm, row_of, topk_w, T, k, H, dy_perm, dtopk_w, s);
   MOE_LAUNCH_CHECK("moe_combine_backward: launch");
   return debug_check(MOE_OK, "moe_combine_backward", s, nullptr);
 }

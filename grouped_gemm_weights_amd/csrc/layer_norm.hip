@@ -7,71 +7,107 @@
 // Both are bound by HBM: a row is read once, held in registers as fp32, and every statistic is an
 // fp32 sum over it (the variance from the centred values, not from a difference of two sums, so
 // a row far from zero loses nothing).
+#include <algorithm>
+
 #include "rows.h"
 
 namespace moe {
 namespace {
 
-// Sum of one value over the WPR waves that share a row.  `part` is a buffer of WPR floats that
-// no other sum of the same barrier interval uses.
-template <int WPR>
-__device__ __forceinline__ float row_sum(float v, float* part) {
-  v = wave_sum(v);
-  if (WPR == 1) return v;
-  if ((threadIdx.x & (kWave - 1)) == 0) part[threadIdx.x / kWave] = v;
-  __syncthreads();
+constexpr int kMaxWaves = 16;
+
+// The sum of 16 floats of LDS, in order: an entry per wave, zeros where there are fewer.
+__device__ __forceinline__ float sum16(const float* part) {
+  typedef float f32x4 __attribute__((ext_vector_type(4)));
   float s = 0.f;
 #pragma unroll
-  for (int w = 0; w < WPR; ++w) s += part[w];
+  for (int i = 0; i < kMaxWaves / 4; ++i) {
+    const f32x4 v = reinterpret_cast<const f32x4*>(part)[i];
+    s += (v[0] + v[1]) + (v[2] + v[3]);
+  }
   return s;
 }
 
-// WPR waves per row, each lane NV vectors of 8 elements: H <= WPR * 64 * NV * 8.
-template <typename T, int WPR, int NV>
-__global__ __launch_bounds__(WPR == 1 ? 256 : WPR * kWave) void norm_kernel(
+// Sum of one value over the waves of a block that share a row.  `part` is 16 floats of LDS that no
+// other sum of the same barrier interval uses, zero past the block's waves.
+__device__ __forceinline__ float row_sum(float v, int waves, float* part) {
+  v = wave_sum(v);
+  if (waves == 1) return v;
+  if ((threadIdx.x & (kWave - 1)) == 0) part[threadIdx.x / kWave] = v;
+  __syncthreads();
+  return sum16(part);
+}
+
+// `waves` waves per row, each lane NV vectors of 8 elements: H <= waves * 64 * NV * 8.  Rows of one
+// wave go four to a block, each wave on its own.  A block (wave) takes every `step`-th row.  KEEP:
+// gamma and beta stay in registers from row to row (as fp32 they are twice a bf16 row and would
+// come from L2 again for each) and the next row's loads are issued before this row's sums.
+// TAIL: H is not a multiple of 8.
+template <typename T, int NV, bool KEEP, bool TAIL>
+__global__ __launch_bounds__(1024) void norm_kernel(
     const T* __restrict__ x, const float* __restrict__ gamma, const float* __restrict__ beta,
-    int rows, int H, float eps, T* __restrict__ y, float* __restrict__ mean,
+    int rows, int H, int waves, float eps, T* __restrict__ y, float* __restrict__ mean,
     float* __restrict__ rstd) {
-  __shared__ float part[2][WPR];
-  const int row = WPR == 1 ? blockIdx.x * 4 + threadIdx.x / kWave : blockIdx.x;
-  if (row >= rows) return;
-  const int tid = WPR == 1 ? threadIdx.x & (kWave - 1) : threadIdx.x;
-  const T* xr = x + static_cast<int64_t>(row) * H;
-  float v[NV][kVec];
-  float s = 0.f;
+  __shared__ __attribute__((aligned(16))) float part[2][2][kMaxWaves];
+  // entries without a wave: nobody else writes them, and a barrier comes before the first read
+  if (waves > 1 && threadIdx.x < 4 * kMaxWaves && threadIdx.x % kMaxWaves >= waves)
+    (&part[0][0][0])[threadIdx.x] = 0.f;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int tid = waves == 1 ? threadIdx.x & (kWave - 1) : threadIdx.x, lanes = waves * kWave;
+  const int64_t step = waves == 1 ? static_cast<int64_t>(gridDim.x) * 4 : gridDim.x;
+  int64_t row = waves == 1 ? static_cast<int64_t>(blockIdx.x) * 4 + wave : blockIdx.x;
+  Raw8<T> raw[NV];
+  float g[NV][kVec], b[NV][kVec];
+  auto fetch = [&]() {
+    const int n = row < rows ? H : 0;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    load8<true>(xr, tid + i * WPR * kWave, H, v[i]);
+    for (int i = 0; i < NV; ++i) load_raw<true, TAIL>(x + (n ? row * H : 0), tid + i * lanes, n, raw[i]);
+  };
+  auto scale = [&](int i) {
+    load8<false, TAIL>(gamma, tid + i * lanes, H, g[i]);
+    load8<false, TAIL>(beta, tid + i * lanes, beta ? H : 0, b[i]);
+  };
+  fetch();
+  if (KEEP)
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) s += v[i][j];
-  }
-  const float mu = row_sum<WPR>(s, part[0]) / H;
-  float q = 0.f;
+    for (int i = 0; i < NV; ++i) scale(i);
+  for (int turn = 0; row < rows; turn ^= 1) {
+    const int64_t at_row = row;
+    float v[NV][kVec];
+    float s = 0.f;
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+      unpack<TAIL>(raw[i], tid + i * lanes, H, v[i]);
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-      const int at = (tid + i * WPR * kWave) * kVec + j;
-      v[i][j] = at < H ? v[i][j] - mu : 0.f;
-      q = fmaf(v[i][j], v[i][j], q);
+      for (int j = 0; j < kVec; ++j) s += v[i][j];
     }
-  const float r = 1.f / sqrtf(row_sum<WPR>(q, part[1]) / H + eps);
-  T* yr = y + static_cast<int64_t>(row) * H;
+    row += step;
+    if (KEEP) fetch();
+    // the sums' buffers alternate from row to row
+    const float mu = row_sum(s, waves, part[turn][0]) / H;
+    float q = 0.f;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int at = tid + i * WPR * kWave;
-    float g[kVec], b[kVec];
-    load8<false>(gamma, at, H, g);
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) b[j] = 0.f;
-    if (beta) load8<false>(beta, at, H, b);
+      for (int j = 0; j < kVec; ++j) {
+        const int at = (tid + i * lanes) * kVec + j;
+        v[i][j] = at < H ? v[i][j] - mu : 0.f;
+        q = fmaf(v[i][j], v[i][j], q);
+      }
+    const float r = 1.f / sqrtf(row_sum(q, waves, part[turn][1]) / H + eps);
+    T* yr = y + at_row * H;
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) v[i][j] = fmaf(v[i][j] * r, g[j], b[j]);
-    store8<true>(yr, at, H, v[i]);
-  }
-  if (tid == 0) {
-    if (mean) mean[row] = mu;
-    if (rstd) rstd[row] = r;
+    for (int i = 0; i < NV; ++i) {
+      if (!KEEP) scale(i);
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) v[i][j] = fmaf(v[i][j] * r, g[i][j], b[i][j]);
+      store8<true, TAIL>(yr, tid + i * lanes, H, v[i]);
+    }
+    if (tid == 0) {
+      if (mean) mean[at_row] = mu;
+      if (rstd) rstd[at_row] = r;
+    }
+    if (!KEEP) fetch();
   }
 }
 
@@ -80,39 +116,40 @@ template <typename T>
 __global__ __launch_bounds__(1024) void norm_long_kernel(
     const T* __restrict__ x, const float* __restrict__ gamma, const float* __restrict__ beta, int H,
     float eps, T* __restrict__ y, float* __restrict__ mean, float* __restrict__ rstd) {
-  __shared__ float part[2][16];
+  constexpr bool TAIL = true;
+  __shared__ __attribute__((aligned(16))) float part[2][kMaxWaves];
   const int row = blockIdx.x;
   const T* xr = x + static_cast<int64_t>(row) * H;
   const int64_t n_vec = (static_cast<int64_t>(H) + kVec - 1) / kVec;
   float v[kVec];
   float s = 0.f;
   for (int64_t at = threadIdx.x; at < n_vec; at += 1024) {
-    load8<false>(xr, at, H, v);
+    load8<false, TAIL>(xr, at, H, v);
 #pragma unroll
     for (int j = 0; j < kVec; ++j) s += v[j];
   }
-  const float mu = row_sum<16>(s, part[0]) / H;
+  const float mu = row_sum(s, kMaxWaves, part[0]) / H;
   float q = 0.f;
   for (int64_t at = threadIdx.x; at < n_vec; at += 1024) {
-    load8<false>(xr, at, H, v);
+    load8<false, TAIL>(xr, at, H, v);
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
       const float c = at * kVec + j < H ? v[j] - mu : 0.f;
       q = fmaf(c, c, q);
     }
   }
-  const float r = 1.f / sqrtf(row_sum<16>(q, part[1]) / H + eps);
+  const float r = 1.f / sqrtf(row_sum(q, kMaxWaves, part[1]) / H + eps);
   T* yr = y + static_cast<int64_t>(row) * H;
   for (int64_t at = threadIdx.x; at < n_vec; at += 1024) {
     float g[kVec], b[kVec];
-    load8<false>(xr, at, H, v);
-    load8<false>(gamma, at, H, g);
+    load8<false, TAIL>(xr, at, H, v);
+    load8<false, TAIL>(gamma, at, H, g);
 #pragma unroll
     for (int j = 0; j < kVec; ++j) b[j] = 0.f;
-    if (beta) load8<false>(beta, at, H, b);
+    if (beta) load8<false, TAIL>(beta, at, H, b);
 #pragma unroll
     for (int j = 0; j < kVec; ++j) v[j] = fmaf((v[j] - mu) * r, g[j], b[j]);
-    store8<true>(yr, at, H, v);
+    store8<true, TAIL>(yr, at, H, v);
   }
   if (threadIdx.x == 0) {
     if (mean) mean[row] = mu;
@@ -120,54 +157,66 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(
   }
 }
 
-// Backward.  WPR waves share a row; a group of WPR waves takes rows `group`, `group` + groups, ...
-// and its lanes own fixed columns, so the sums over its rows for dgamma and dbeta stay in
-// registers; a block's groups (WPR = 1: four) are joined in LDS and leave as one partial row of
-// 2 H floats (partial != nullptr).  The next row's loads are issued before this row's sums, so
-// they are in flight while the waves wait for one another.
-template <typename T, int WPR, int NV>
-__global__ __launch_bounds__(WPR == 1 ? 256 : WPR * kWave) void norm_backward_kernel(
+// Backward.  `waves` waves share a row and the block has groups = blockDim / (64 waves) such
+// teams; team g takes rows blockIdx * groups + g, then gridDim * groups further on.  Its lanes own
+// fixed columns, so the sums over its rows for dgamma and dbeta stay in registers; the block's
+// teams are joined in LDS in team order and leave as one partial row of 2 H floats
+// (partial != nullptr).  Every team makes the same number of turns, so all waves meet at the
+// barriers.  AHEAD: the next row's loads are issued before this row's sums, so they are in
+// flight while the waves wait for one another, and gamma stays in registers (one vector a lane;
+// with two, the registers go to the sums and gamma comes from L2).
+template <typename T, int NV, bool AHEAD, bool TAIL>
+__global__ __launch_bounds__(1024) void norm_backward_kernel(
     const T* __restrict__ dy, const T* __restrict__ x, const float* __restrict__ gamma,
-    const float* __restrict__ mean, const float* __restrict__ rstd, int rows, int H,
-    T* __restrict__ dx, float* __restrict__ partial) {
-  constexpr int GROUPS = WPR == 1 ? 4 : 1, LANES = WPR * kWave;
-  __shared__ float part[2][2][WPR];
-  __shared__ float joined[GROUPS > 1 ? 2 * LANES * NV * kVec : 1];
-  const int tid = threadIdx.x % LANES;
-  const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / LANES);
-  const int step = gridDim.x * GROUPS;
+    const float* __restrict__ mean, const float* __restrict__ rstd, int rows, int H, int waves,
+    int groups, T* __restrict__ dx, float* __restrict__ partial) {
+  extern __shared__ __attribute__((aligned(16))) float joined[];  // [groups][2 H]
+  __shared__ __attribute__((aligned(16))) float part[2][2][kMaxWaves][kMaxWaves];  // [team][wave]
+  const int lanes = waves * kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int group = wave / waves, tid = threadIdx.x - group * lanes;
+  const int step = gridDim.x * groups;
+  const int in_team = wave - group * waves;
+  // entries past a team's waves: nobody else writes them, and a barrier comes before the first read
+  if (waves > 1)
+    for (int i = threadIdx.x; i < 4 * kMaxWaves * kMaxWaves; i += blockDim.x)
+      if (i % kMaxWaves >= waves) (&part[0][0][0][0])[i] = 0.f;
   float sg[NV][kVec], sb[NV][kVec], g[NV][kVec];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    load8<false>(gamma, tid + i * LANES, H, g[i]);
+    if (AHEAD) load8<false, TAIL>(gamma, tid + i * lanes, H, g[i]);
 #pragma unroll
     for (int j = 0; j < kVec; ++j) sg[i][j] = sb[i][j] = 0.f;
   }
-  int row = blockIdx.x * GROUPS + group;
   Raw8<T> xn[NV], dn[NV];
   float mu_n = 0.f, r_n = 0.f;
-  auto fetch = [&](int r) {
-    mu_n = mean[r];
-    r_n = rstd[r];
+  auto fetch = [&](int64_t r) {
+    const int n = r < rows ? H : 0;  // a turn without a row: zeros
+    const int64_t at = r < rows ? r : 0;
+    mu_n = n ? mean[at] : 0.f;
+    r_n = n ? rstd[at] : 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      load_raw<true>(x + static_cast<int64_t>(r) * H, tid + i * LANES, H, xn[i]);
-      load_raw<true>(dy + static_cast<int64_t>(r) * H, tid + i * LANES, H, dn[i]);
+      load_raw<true, TAIL>(x + at * H, tid + i * lanes, n, xn[i]);
+      load_raw<true, TAIL>(dy + at * H, tid + i * lanes, n, dn[i]);
     }
   };
-  if (row < rows) fetch(row);
-  for (int turn = 0; row < rows; row += step, turn ^= 1) {
+  int64_t first = static_cast<int64_t>(blockIdx.x) * groups, row = first + group;
+  if (AHEAD) fetch(row);
+  for (int turn = 0; first < rows; first += step, row += step, turn ^= 1) {
+    if (!AHEAD) fetch(row);
     const float mu = mu_n, r = r_n;
     float a[NV][kVec], xh[NV][kVec];
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      unpack(xn[i], xh[i]);
-      unpack(dn[i], a[i]);
+      unpack<TAIL>(xn[i], tid + i * lanes, H, xh[i]);
+      unpack<TAIL>(dn[i], tid + i * lanes, H, a[i]);
     }
-    if (row + step < rows) fetch(row + step);
+    if (AHEAD) fetch(row + step);
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+      if (!AHEAD) load8<false, TAIL>(gamma, tid + i * lanes, H, g[i]);
 #pragma unroll
       for (int j = 0; j < kVec; ++j) {
         // past the row a is zero, so what xh holds there does not count
@@ -178,58 +227,51 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : WPR * kWave) void norm_backward_ke
         s1 += a[i][j];
         s2 = fmaf(a[i][j], xh[i][j], s2);
       }
+    }
     s1 = wave_sum(s1);
     s2 = wave_sum(s2);
-    if (WPR > 1) {
+    if (waves > 1) {
       // the buffers alternate from row to row, so one barrier a row is enough
-      if ((tid & (kWave - 1)) == 0) {
-        part[turn][0][tid / kWave] = s1;
-        part[turn][1][tid / kWave] = s2;
+      if ((threadIdx.x & (kWave - 1)) == 0) {
+        part[turn][0][group][in_team] = s1;
+        part[turn][1][group][in_team] = s2;
       }
       __syncthreads();
-      s1 = s2 = 0.f;
-#pragma unroll
-      for (int w = 0; w < WPR; ++w) {
-        s1 += part[turn][0][w];
-        s2 += part[turn][1][w];
-      }
+      s1 = sum16(part[turn][0][group]);
+      s2 = sum16(part[turn][1][group]);
     }
     s1 /= H;
     s2 /= H;
-    T* out = dx + static_cast<int64_t>(row) * H;
+    if (row >= rows) continue;
+    T* out = dx + row * H;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
 #pragma unroll
       for (int j = 0; j < kVec; ++j) a[i][j] = r * (a[i][j] - s1 - xh[i][j] * s2);
-      store8<true>(out, tid + i * LANES, H, a[i]);
+      store8<true, TAIL>(out, tid + i * lanes, H, a[i]);
     }
   }
   if (!partial) return;
-  if (GROUPS > 1) {
-    // the groups add their sums in group order
-    for (int k = 0; k < GROUPS; ++k) {
-      if (group == k)
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-          for (int j = 0; j < kVec; ++j) {
-            float* at = joined + ((i * kVec + j) * 2) * LANES + tid;
-            if (k > 0) {
-              sg[i][j] += at[0];
-              sb[i][j] += at[LANES];
-            }
-            at[0] = sg[i][j];
-            at[LANES] = sb[i][j];
-          }
-      __syncthreads();
-    }
-    if (group != GROUPS - 1) return;
-  }
   float* p = partial + static_cast<int64_t>(blockIdx.x) * 2 * H;
+  if (groups == 1) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      store8<false, TAIL>(p, tid + i * lanes, H, sg[i]);
+      store8<false, TAIL>(p + H, tid + i * lanes, H, sb[i]);
+    }
+    return;
+  }
+  float* mine = joined + group * 2 * H;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    store8<false>(p, tid + i * LANES, H, sg[i]);
-    store8<false>(p + H, tid + i * LANES, H, sb[i]);
+    store8<false, TAIL>(mine, tid + i * lanes, H, sg[i]);
+    store8<false, TAIL>(mine + H, tid + i * lanes, H, sb[i]);
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c < 2 * H; c += blockDim.x) {
+    float s = 0.f;
+    for (int k = 0; k < groups; ++k) s += joined[k * 2 * H + c];
+    p[c] = s;
   }
 }
 
@@ -238,7 +280,8 @@ template <typename T>
 __global__ __launch_bounds__(1024) void norm_backward_long_kernel(
     const T* __restrict__ dy, const T* __restrict__ x, const float* __restrict__ gamma,
     const float* __restrict__ mean, const float* __restrict__ rstd, int H, T* __restrict__ dx) {
-  __shared__ float part[2][16];
+  constexpr bool TAIL = true;
+  __shared__ __attribute__((aligned(16))) float part[2][kMaxWaves];
   const int row = blockIdx.x;
   const T* xr = x + static_cast<int64_t>(row) * H;
   const T* dr = dy + static_cast<int64_t>(row) * H;
@@ -247,25 +290,25 @@ __global__ __launch_bounds__(1024) void norm_backward_long_kernel(
   float a[kVec], xh[kVec], g[kVec];
   float s1 = 0.f, s2 = 0.f;
   for (int64_t at = threadIdx.x; at < n_vec; at += 1024) {
-    load8<false>(xr, at, H, xh);
-    load8<false>(dr, at, H, a);
-    load8<false>(gamma, at, H, g);
+    load8<false, TAIL>(xr, at, H, xh);
+    load8<false, TAIL>(dr, at, H, a);
+    load8<false, TAIL>(gamma, at, H, g);
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
       s1 = fmaf(a[j], g[j], s1);
       s2 = fmaf(a[j] * g[j], (xh[j] - mu) * r, s2);
     }
   }
-  s1 = row_sum<16>(s1, part[0]) / H;
-  s2 = row_sum<16>(s2, part[1]) / H;
+  s1 = row_sum(s1, kMaxWaves, part[0]) / H;
+  s2 = row_sum(s2, kMaxWaves, part[1]) / H;
   T* out = dx + static_cast<int64_t>(row) * H;
   for (int64_t at = threadIdx.x; at < n_vec; at += 1024) {
-    load8<false>(xr, at, H, xh);
-    load8<false>(dr, at, H, a);
-    load8<false>(gamma, at, H, g);
+    load8<false, TAIL>(xr, at, H, xh);
+    load8<false, TAIL>(dr, at, H, a);
+    load8<false, TAIL>(gamma, at, H, g);
 #pragma unroll
     for (int j = 0; j < kVec; ++j) a[j] = r * (a[j] * g[j] - s1 - (xh[j] - mu) * r * s2);
-    store8<true>(out, at, H, a);
+    store8<true, TAIL>(out, at, H, a);
   }
 }
 
@@ -307,7 +350,7 @@ __global__ __launch_bounds__(kSumWaves* kWave) void norm_sum_kernel(
   const int64_t H2 = 2 * static_cast<int64_t>(H);
   float v = 0.f;
   if (c < H2) {
-#pragma unroll 8
+#pragma unroll 16
     for (int i = w; i < n; i += kSumWaves) v += partial[i * H2 + c];
   }
   s[w][lane] = v;
@@ -324,17 +367,41 @@ __global__ __launch_bounds__(kSumWaves* kWave) void norm_sum_kernel(
   }
 }
 
-constexpr int kMaxH = 16 * kWave * 4 * kVec;  // 32768: the longest row that stays in registers
-constexpr int kPartials = 512;                // blocks of the backward pass, two a CU
+constexpr int kMaxH = kMaxWaves * kWave * 4 * kVec;          // 32768: the longest row norm_kernel holds
+constexpr int kMaxBackwardH = kMaxWaves * kWave * 2 * kVec;  // 16384: the longest of the backward kernel
+constexpr int kCus = 256;
+constexpr int kPartials = kCus;                              // most blocks of the backward pass
+constexpr int kJoinBytes = kMaxWaves * kWave * kVec * 2 * sizeof(float);  // 64 KB: 16 waves' sums
 
-int norm_partials(int T) { return T < kPartials ? T : kPartials; }
+// Waves per row and rows at once per block of the backward pass: as many waves as the row has 512
+// columns, as many rows as 16 waves hold.
+struct BackwardShape {
+  int nv, waves, groups, blocks;
+};
 
-template <typename E, int WPR, int NV>
+BackwardShape backward_shape(int T, int H) {
+  BackwardShape b;
+  b.nv = H <= kMaxBackwardH / 2 ? 1 : 2;
+  b.waves = ceil_div(H, b.nv * kWave * kVec);
+  b.groups = std::max(1, kMaxWaves / b.waves);
+  b.blocks = std::min(kPartials, ceil_div(T, b.groups));
+  return b;
+}
+
+int norm_partials(int T, int H) {
+  return H <= kMaxBackwardH ? backward_shape(T, H).blocks : std::min(T, kPartials);
+}
+
+template <typename E, int NV>
 int launch_norm(const void* x, const float* gamma, const float* beta, int T, int H, float eps, void* y,
                 float* mean, float* rstd, hipStream_t s) {
-  const int blocks = WPR == 1 ? ceil_div(T, 4) : T;
-  hipLaunchKernelGGL((norm_kernel<E, WPR, NV>), dim3(blocks), dim3(WPR == 1 ? 256 : WPR * kWave), 0, s,
-                     static_cast<const E*>(x), gamma, beta, T, H, eps, static_cast<E*>(y), mean, rstd);
+  const int waves = ceil_div(H, NV * kWave * kVec), rows = waves == 1 ? 4 : 1;
+  // as many blocks as the CUs hold at once (20 waves a CU at these kernels' registers)
+  const int blocks = std::min(ceil_div(T, rows), kCus * std::max(1, 20 / (waves * rows)));
+  auto kernel = H % kVec == 0 ? norm_kernel<E, NV, NV <= 2, false> : norm_kernel<E, NV, NV <= 2, true>;
+  hipLaunchKernelGGL(kernel, dim3(blocks), dim3(waves * rows * kWave), 0, s,
+                     static_cast<const E*>(x), gamma, beta, T, H, waves, eps, static_cast<E*>(y), mean,
+                     rstd);
   MOE_LAUNCH_CHECK("moe_layer_norm: launch");
   return MOE_OK;
 }
@@ -342,14 +409,13 @@ int launch_norm(const void* x, const float* gamma, const float* beta, int T, int
 template <typename E>
 int norm(const void* x, const float* gamma, const float* beta, int T, int H, float eps, void* y,
          float* mean, float* rstd, hipStream_t s) {
-#define NORM(WPR, NV) return launch_norm<E, WPR, NV>(x, gamma, beta, T, H, eps, y, mean, rstd, s)
-  if (H <= 512) NORM(1, 1);
-  if (H <= 1024) NORM(1, 2);
-  if (H <= 2048) NORM(4, 1);
-  if (H <= 4096) NORM(4, 2);
-  if (H <= 8192) NORM(4, 4);
-  if (H <= 16384) NORM(16, 2);
-  if (H <= kMaxH) NORM(16, 4);
+#define NORM(NV) return launch_norm<E, NV>(x, gamma, beta, T, H, eps, y, mean, rstd, s)
+  // Few rows, which leave CUs idle: a vector a lane, so that a row's loads spread over more waves.
+  // Many rows: two, so that fewer waves wait for one another.
+  const int per = kWave * kVec;
+  if (H <= per || (T <= kCus && H <= kMaxWaves * per)) NORM(1);
+  if (H <= kMaxWaves * 2 * per) NORM(2);
+  if (H <= kMaxH) NORM(4);
 #undef NORM
   hipLaunchKernelGGL(norm_long_kernel<E>, dim3(T), dim3(1024), 0, s, static_cast<const E*>(x), gamma,
                      beta, H, eps, static_cast<E*>(y), mean, rstd);
@@ -357,32 +423,28 @@ int norm(const void* x, const float* gamma, const float* beta, int T, int H, flo
   return MOE_OK;
 }
 
-template <typename E, int WPR, int NV>
-int launch_norm_backward(const void* dy, const void* x, const float* gamma, const float* mean,
-                         const float* rstd, int T, int H, void* dx, float* partial, hipStream_t s) {
-  hipLaunchKernelGGL((norm_backward_kernel<E, WPR, NV>), dim3(norm_partials(T)), dim3(WPR == 1 ? 256 : WPR * kWave), 0, s,
-                     static_cast<const E*>(dy), static_cast<const E*>(x), gamma, mean, rstd, T, H,
-                     static_cast<E*>(dx), partial);
-  MOE_LAUNCH_CHECK("moe_layer_norm_backward: launch");
-  return MOE_OK;
-}
-
 template <typename E>
 int norm_backward(const void* dy, const void* x, const float* gamma, const float* mean, const float* rstd,
                   int T, int H, void* dx, float* partial, hipStream_t s) {
-#define NORM(WPR, NV) return launch_norm_backward<E, WPR, NV>(dy, x, gamma, mean, rstd, T, H, dx, partial, s)
-  if (H <= 512) NORM(1, 1);
-  if (H <= 1024) NORM(1, 2);
-  if (H <= 2048) NORM(4, 1);
-  if (H <= 4096) NORM(8, 1);
-  if (H <= 8192) NORM(16, 1);
-  if (H <= 16384) NORM(16, 2);
-#undef NORM
+  if (H <= kMaxBackwardH) {
+    const BackwardShape b = backward_shape(T, H);
+    auto kernel = H % kVec == 0
+                      ? (b.nv == 1 ? norm_backward_kernel<E, 1, true, false> : norm_backward_kernel<E, 2, false, false>)
+                      : (b.nv == 1 ? norm_backward_kernel<E, 1, true, true> : norm_backward_kernel<E, 2, false, true>);
+    const size_t lds = b.groups > 1 && partial ? b.groups * 2 * static_cast<size_t>(H) * sizeof(float) : 0;
+    MOE_HIP_CHECK(hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                      hipFuncAttributeMaxDynamicSharedMemorySize, kJoinBytes));
+    hipLaunchKernelGGL(kernel, dim3(b.blocks), dim3(b.groups * b.waves * kWave), lds, s,
+                       static_cast<const E*>(dy), static_cast<const E*>(x), gamma, mean, rstd, T, H,
+                       b.waves, b.groups, static_cast<E*>(dx), partial);
+    MOE_LAUNCH_CHECK("moe_layer_norm_backward: launch");
+    return MOE_OK;
+  }
   hipLaunchKernelGGL(norm_backward_long_kernel<E>, dim3(T), dim3(1024), 0, s, static_cast<const E*>(dy),
                      static_cast<const E*>(x), gamma, mean, rstd, H, static_cast<E*>(dx));
   MOE_LAUNCH_CHECK("moe_layer_norm_backward: launch");
   if (partial) {
-    hipLaunchKernelGGL(norm_columns_kernel<E>, dim3(ceil_div(H, 256), norm_partials(T)), dim3(256), 0, s,
+    hipLaunchKernelGGL(norm_columns_kernel<E>, dim3(ceil_div(H, 256), norm_partials(T, H)), dim3(256), 0, s,
                        static_cast<const E*>(dy), static_cast<const E*>(x), mean, rstd, T, H, partial);
     MOE_LAUNCH_CHECK("moe_layer_norm_backward: columns launch");
   }
@@ -390,7 +452,7 @@ int norm_backward(const void* dy, const void* x, const float* gamma, const float
 }
 
 size_t norm_backward_ws(int T, int H) {
-  return align_up(static_cast<size_t>(norm_partials(T)) * 2 * H * sizeof(float), 256);
+  return align_up(static_cast<size_t>(norm_partials(T, H)) * 2 * H * sizeof(float), 256);
 }
 
 }  // namespace
@@ -447,7 +509,7 @@ extern "C" int moe_layer_norm_backward(const void* dy, const void* x, const floa
     // no rows: zero sums
     hipLaunchKernelGGL(norm_sum_kernel,
                        dim3(static_cast<unsigned>(ceil_div64(2 * static_cast<int64_t>(H), kWave))),
-                       dim3(kSumWaves * kWave), 0, s, partial, norm_partials(T), H, dgamma, dbeta);
+                       dim3(kSumWaves * kWave), 0, s, partial, norm_partials(T, H), H, dgamma, dbeta);
     MOE_LAUNCH_CHECK("moe_layer_norm_backward: sum launch");
   }
   return debug_check(MOE_OK, "moe_layer_norm_backward", s, nullptr);

@@ -225,41 +225,49 @@ __global__ __launch_bounds__(256) void gather_kernel(const char* __restrict__ x,
 
 // Gradient of x_perm[row_of[t k + j]] = x[t]:  dx[t] = sum_j dx_perm[row_of[t k + j]], summed in
 // j order in fp32 and rounded once.  Bound by HBM: R H elements are read once (non-temporal) and
-// T H written.  One wave per 512 columns of a token, up to 8 rows' loads in flight per lane.
+// T H written.  A lane takes 8 columns of one token with up to 8 rows' loads in flight; a block
+// takes `tokens` whole tokens of fewer than 64 such pieces, or a run of waves of one token.
+// TAIL: H is not a multiple of 8.
 constexpr int kPbRows = 8;
 
-template <typename E>
-__global__ __launch_bounds__(256) void permute_backward_kernel(const E* __restrict__ dx_perm,
+template <typename E, bool TAIL>
+__global__ __launch_bounds__(512) void permute_backward_kernel(const E* __restrict__ dx_perm,
                                                                const int32_t* __restrict__ row_of,
-                                                               int T, int k, int H, int chunks,
-                                                               E* __restrict__ dx) {
-  const int64_t job = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / kWave;
-  const int t = static_cast<int>(job / chunks);
-  if (t >= T) return;
-  const int at = static_cast<int>(job % chunks) * kWave + (threadIdx.x & (kWave - 1));
+                                                               int T, int k, int H, int pieces,
+                                                               int tokens, E* __restrict__ dx) {
+  int t = blockIdx.x, at = blockIdx.y * blockDim.x + threadIdx.x;
+  if (tokens > 1) {
+    const int mine = threadIdx.x / pieces;
+    if (mine >= tokens) return;
+    t = t * tokens + mine;
+    at = threadIdx.x - mine * pieces;
+  }
+  if (t >= T || at >= pieces) return;
   const int64_t R = static_cast<int64_t>(T) * k;
+  const int32_t* rows = row_of + static_cast<int64_t>(t) * k;
   float acc[kVec];
 #pragma unroll
   for (int q = 0; q < kVec; ++q) acc[q] = 0.f;
   for (int j0 = 0; j0 < k; j0 += kPbRows) {
-    float v[kPbRows][kVec];
+    Raw8<E> v[kPbRows];
+    int r[kPbRows];
+#pragma unroll
+    for (int j = 0; j < kPbRows; ++j) r[j] = j0 + j < k ? rows[j0 + j] : -1;
 #pragma unroll
     for (int j = 0; j < kPbRows; ++j) {
-      const int r = j0 + j < k ? row_of[static_cast<int64_t>(t) * k + j0 + j] : -1;
       // an unwritten row index (after an out-of-range expert id) must not fault: it adds nothing
-      if (r >= 0 && r < R) {
-        load8<true>(dx_perm + static_cast<int64_t>(r) * H, at, H, v[j]);
-      } else {
-#pragma unroll
-        for (int q = 0; q < kVec; ++q) v[j][q] = 0.f;
-      }
+      const bool ok = r[j] >= 0 && r[j] < R;
+      load_raw<true, TAIL>(dx_perm + static_cast<int64_t>(ok ? r[j] : 0) * H, at, ok ? H : 0, v[j]);
     }
 #pragma unroll
-    for (int j = 0; j < kPbRows; ++j)
+    for (int j = 0; j < kPbRows; ++j) {
+      float f[kVec];
+      unpack<TAIL>(v[j], at, H, f);
 #pragma unroll
-      for (int q = 0; q < kVec; ++q) acc[q] += v[j][q];
+      for (int q = 0; q < kVec; ++q) acc[q] += f[q];
+    }
   }
-  store8<true>(dx + static_cast<int64_t>(t) * H, at, H, acc);
+  store8<true, TAIL>(dx + static_cast<int64_t>(t) * H, at, H, acc);
 }
 
 }  // namespace
@@ -391,22 +399,27 @@ extern "C" int moe_permute_backward(const void* dx_perm, const int32_t* row_of, 
   using namespace moe;
   if (T < 0 || k < 1 || H < 1 || (dtype != MOE_F32 && dtype != MOE_BF16))
     return fail(MOE_ERR_ARG, "moe_permute_backward: bad sizes T=%d k=%d H=%d or dtype", T, k, H);
-  const int chunks = ceil_div(H, kWave * kVec);
-  const int64_t blocks = ceil_div64(static_cast<int64_t>(T) * chunks, 4);
-  if (static_cast<int64_t>(T) * k > INT32_MAX || H > kMaxRow || blocks > INT32_MAX)
+  if (static_cast<int64_t>(T) * k > INT32_MAX || H > kMaxRow)
     return fail(MOE_ERR_UNSUPPORTED, "moe_permute_backward: T=%d k=%d H=%d too large", T, k, H);
   if (T == 0) return MOE_OK;
   if (!dx_perm || !row_of || !dx) return fail(MOE_ERR_ARG, "moe_permute_backward: null pointer");
   hipStream_t s = as_stream(stream);
-  const dim3 grid(static_cast<unsigned>(blocks));
-  if (dtype == MOE_F32)
-    hipLaunchKernelGGL(permute_backward_kernel<float>, grid, dim3(256), 0, s,
-                       static_cast<const float*>(dx_perm), row_of, T, k, H, chunks,
-                       static_cast<float*>(dx));
-  else
-    hipLaunchKernelGGL(permute_backward_kernel<uint16_t>, grid, dim3(256), 0, s,
-                       static_cast<const uint16_t*>(dx_perm), row_of, T, k, H, chunks,
-                       static_cast<uint16_t*>(dx));
+  const int pieces = ceil_div(H, kVec);
+  const bool tail = H % kVec != 0;
+  // short rows: 256 threads hold several tokens; long ones: the row's waves in blocks of up to 8
+  const int tokens = pieces < kWave ? 256 / pieces : 1;
+  const int waves = ceil_div(pieces, kWave), across = ceil_div(waves, 8);
+  const dim3 grid(ceil_div(T, tokens), tokens > 1 ? 1 : across);
+  const dim3 block(tokens > 1 ? 256 : ceil_div(waves, across) * kWave);
+  if (dtype == MOE_F32) {
+    auto kernel = tail ? permute_backward_kernel<float, true> : permute_backward_kernel<float, false>;
+    hipLaunchKernelGGL(kernel, grid, block, 0, s, static_cast<const float*>(dx_perm), row_of, T, k, H,
+                       pieces, tokens, static_cast<float*>(dx));
+  } else {
+    auto kernel = tail ? permute_backward_kernel<uint16_t, true> : permute_backward_kernel<uint16_t, false>;
+    hipLaunchKernelGGL(kernel, grid, block, 0, s, static_cast<const uint16_t*>(dx_perm), row_of, T, k, H,
+                       pieces, tokens, static_cast<uint16_t*>(dx));
+  }
   MOE_LAUNCH_CHECK("moe_permute_backward: launch");
   return debug_check(MOE_OK, "moe_permute_backward", s, nullptr);
 }

@@ -8,7 +8,7 @@
 // the weights exp(l_j - l_0) / sum_i exp(l_i - l_0) are formed in fp32.
 //
 // moe_route_backward: the gradient of those weights with respect to the logits.
-#include "common.h"
+#include "rows.h"
 
 namespace moe {
 namespace {
@@ -98,11 +98,15 @@ void launch_route(const float* logits, int T, int E, int k, int32_t* idx, float*
 // chosen ids, zero at the other E - k.  Bound by writing the dense row (4 E bytes a token).  One
 // wave per token: lane j holds slot j, the row is built in the wave's own LDS and leaves in wide
 // stores.  An id that a token lists twice gets the sum of its slots, added in slot order.
+// WIDE: E a multiple of 4 and dlogits aligned to 16 bytes.
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+template <bool WIDE>
 __global__ __launch_bounds__(kRouteWaves * kWave) void route_backward_kernel(
     const int32_t* __restrict__ topk_idx, const float* __restrict__ topk_w,
     const float* __restrict__ dtopk_w, int T, int E, int k, float* __restrict__ dlogits,
     int32_t* status) {
-  extern __shared__ float rows[];
+  extern __shared__ __attribute__((aligned(16))) float rows[];
   const int lane = threadIdx.x & (kWave - 1);
   const int t = blockIdx.x * kRouteWaves + (threadIdx.x / kWave);
   if (t >= T) return;
@@ -119,27 +123,33 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_backward_kernel(
       id = -1;
     }
   }
-  float s = w * dw;
-#pragma unroll
-  for (int off = kWave / 2; off >= 1; off >>= 1) s += __shfl_xor(s, off);
-  const float mine = w * (dw - s);
+  const float mine = w * (dw - wave_sum(w * dw));
   // the first slot of an id adds up the slots that share it
   float g = 0.f;
   bool first = id >= 0;
   for (int j = 0; j < k; ++j) {
-    const int oid = __shfl(id, j);
-    const float og = __shfl(mine, j);
+    const int oid = __builtin_amdgcn_readlane(id, j);
+    const float og = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(mine), j));
     if (oid == id) {
       g += og;
       if (j < lane) first = false;
     }
   }
-  for (int e = lane; e < E; e += kWave) row[e] = 0.f;
+  float* out = dlogits + static_cast<int64_t>(t) * E;
+  if (WIDE) {
+    for (int e = lane * 4; e < E; e += kWave * 4) *reinterpret_cast<f32x4*>(row + e) = f32x4{0.f, 0.f, 0.f, 0.f};
+  } else {
+    for (int e = lane; e < E; e += kWave) row[e] = 0.f;
+  }
   __builtin_amdgcn_wave_barrier();
   if (first) row[id] = g;
   __builtin_amdgcn_wave_barrier();
-  float* out = dlogits + static_cast<int64_t>(t) * E;
-  for (int e = lane; e < E; e += kWave) out[e] = row[e];
+  if (WIDE) {
+    for (int e = lane * 4; e < E; e += kWave * 4)
+      __builtin_nontemporal_store(*reinterpret_cast<const f32x4*>(row + e), reinterpret_cast<f32x4*>(out + e));
+  } else {
+    for (int e = lane; e < E; e += kWave) __builtin_nontemporal_store(row[e], out + e);
+  }
 }
 
 }  // namespace
@@ -176,7 +186,9 @@ extern "C" int moe_route_backward(const int32_t* topk_idx, const float* topk_w, 
   if (!topk_idx || !topk_w || !dtopk_w || !dlogits)
     return fail(MOE_ERR_ARG, "moe_route_backward: null pointer");
   hipStream_t s = as_stream(stream);
-  hipLaunchKernelGGL(route_backward_kernel, dim3(ceil_div(T, kRouteWaves)), dim3(kRouteWaves * kWave),
+  const bool wide = E % 4 == 0 && reinterpret_cast<uintptr_t>(dlogits) % 16 == 0;
+  hipLaunchKernelGGL(wide ? route_backward_kernel<true> : route_backward_kernel<false>,
+                     dim3(ceil_div(T, kRouteWaves)), dim3(kRouteWaves * kWave),
                      kRouteWaves * E * sizeof(float), s, topk_idx, topk_w, dtopk_w, T, E, k, dlogits,
                      status);
   MOE_LAUNCH_CHECK("moe_route_backward: launch");

@@ -14,7 +14,7 @@ typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
 typedef float f32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
 
 constexpr int kVec = 8;             // elements per lane and step
-constexpr int kMaxRow = 1 << 28;    // longest row: column indices stay in 31 bits
+constexpr int kMaxRow = 1 << 26;    // longest row: grids and column indices stay in range
 
 // Eight elements as they lie in memory: a row's loads can be in flight before they are unpacked.
 template <typename T>
@@ -28,67 +28,108 @@ struct Raw8<float> {
   float w[8];
 };
 
-// Elements [8 v, 8 v + 8) of a row of n elements; elements past n read as zero.  NT: a
-// non-temporal load, for rows that are read exactly once.
-template <bool NT>
+// Elements [8 v, 8 v + 8) of a row of n elements, to be unpacked with the same v and n.  A piece
+// that ends past the row is loaded 8 - n % 8 elements early, as one whole vector, and shifted when
+// it is unpacked, so that no load waits for another's value.  TAIL = false: n is a multiple of 8,
+// and none of that is needed.  NT: a non-temporal load, for rows that are read exactly once.
+template <bool NT, bool TAIL>
 __device__ __forceinline__ void load_raw(const uint16_t* row, int64_t v, int n, Raw8<uint16_t>& out) {
   const int64_t at = v * kVec;
-  if (at + kVec <= n) {
-    const u32x4_a2* p = reinterpret_cast<const u32x4_a2*>(row + at);
-    const u32x4_a2 b = NT ? __builtin_nontemporal_load(p) : *p;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) out.w[i] = b[i];
-  } else {
+  for (int i = 0; i < 4; ++i) out.w[i] = 0;
+  if (!TAIL || n >= kVec) {
+    if (at < n) {
+      const u32x4_a2* p = reinterpret_cast<const u32x4_a2*>(row + (!TAIL || at + kVec <= n ? at : n - kVec));
+      const u32x4_a2 b = NT ? __builtin_nontemporal_load(p) : *p;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t lo = at + 2 * i < n ? row[at + 2 * i] : 0;
-      const uint32_t hi = at + 2 * i + 1 < n ? row[at + 2 * i + 1] : 0;
-      out.w[i] = lo | hi << 16;
+      for (int i = 0; i < 4; ++i) out.w[i] = b[i];
     }
+  } else if (at == 0) {  // a row of fewer than 8: its last element last, as the shift expects
+#pragma unroll
+    for (int i = 0; i < kVec; ++i)
+      if (i >= kVec - n) out.w[i / 2] |= static_cast<uint32_t>(row[i - (kVec - n)]) << (i % 2 * 16);
   }
 }
 
-template <bool NT>
+template <bool NT, bool TAIL>
 __device__ __forceinline__ void load_raw(const float* row, int64_t v, int n, Raw8<float>& out) {
   const int64_t at = v * kVec;
-  if (at + kVec <= n) {
-    const f32x4_a4* p = reinterpret_cast<const f32x4_a4*>(row + at);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const f32x4_a4 b = NT ? __builtin_nontemporal_load(p + h) : p[h];
+  for (int i = 0; i < kVec; ++i) out.w[i] = 0.f;
+  if (!TAIL || n >= kVec) {
+    if (at < n) {
+      const f32x4_a4* p = reinterpret_cast<const f32x4_a4*>(row + (!TAIL || at + kVec <= n ? at : n - kVec));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) out.w[4 * h + i] = b[i];
+      for (int h = 0; h < 2; ++h) {
+        const f32x4_a4 b = NT ? __builtin_nontemporal_load(p + h) : p[h];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) out.w[4 * h + i] = b[i];
+      }
     }
-  } else {
+  } else if (at == 0) {
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) out.w[i] = at + i < n ? row[at + i] : 0.f;
+    for (int i = 0; i < kVec; ++i)
+      if (i >= kVec - n) out.w[i] = row[i - (kVec - n)];
   }
 }
 
-__device__ __forceinline__ void unpack(const Raw8<uint16_t>& r, float* out) {
+template <bool TAIL>
+__device__ __forceinline__ void unpack(const Raw8<uint16_t>& r, int64_t v, int n, float* out) {
+  uint32_t w[4] = {r.w[0], r.w[1], r.w[2], r.w[3]};
+  const int64_t over = v * kVec + kVec - n;
+  if (TAIL && over > 0) {
+    const int sh = static_cast<int>(over);
+    if (sh & 4) {
+      w[0] = w[2];
+      w[1] = w[3];
+      w[2] = w[3] = 0;
+    }
+    if (sh & 2) {
+      w[0] = w[1];
+      w[1] = w[2];
+      w[2] = w[3];
+      w[3] = 0;
+    }
+    if (sh & 1) {
+      w[0] = w[0] >> 16 | w[1] << 16;
+      w[1] = w[1] >> 16 | w[2] << 16;
+      w[2] = w[2] >> 16 | w[3] << 16;
+      w[3] >>= 16;
+    }
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    out[2 * i] = __uint_as_float(r.w[i] << 16);
-    out[2 * i + 1] = __uint_as_float(r.w[i] & 0xffff0000u);
+    out[2 * i] = __uint_as_float(w[i] << 16);
+    out[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 }
 
-__device__ __forceinline__ void unpack(const Raw8<float>& r, float* out) {
+template <bool TAIL>
+__device__ __forceinline__ void unpack(const Raw8<float>& r, int64_t v, int n, float* out) {
 #pragma unroll
   for (int i = 0; i < kVec; ++i) out[i] = r.w[i];
+  const int64_t over = v * kVec + kVec - n;
+  if (TAIL && over > 0) {
+    const int sh = static_cast<int>(over);
+#pragma unroll
+    for (int step = 4; step >= 1; step /= 2)
+      if (sh & step)
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) out[i] = i + step < kVec ? out[i + step] : 0.f;
+  }
 }
 
-template <bool NT, typename T>
+template <bool NT, bool TAIL, typename T>
 __device__ __forceinline__ void load8(const T* row, int64_t v, int n, float* out) {
   Raw8<T> r;
-  load_raw<NT>(row, v, n, r);
-  unpack(r, out);
+  load_raw<NT, TAIL>(row, v, n, r);
+  unpack<TAIL>(r, v, n, out);
 }
 
-template <bool NT>
+template <bool NT, bool TAIL>
 __device__ __forceinline__ void store8(uint16_t* row, int64_t v, int n, const float* in) {
   const int64_t at = v * kVec;
-  if (at + kVec <= n) {
+  if (TAIL ? at + kVec <= n : at < n) {
     u32x4_a2 b;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -96,17 +137,17 @@ __device__ __forceinline__ void store8(uint16_t* row, int64_t v, int n, const fl
     u32x4_a2* p = reinterpret_cast<u32x4_a2*>(row + at);
     if (NT) __builtin_nontemporal_store(b, p);
     else *p = b;
-  } else {
+  } else if (TAIL && at < n) {
 #pragma unroll
     for (int i = 0; i < kVec; ++i)
       if (at + i < n) row[at + i] = f32_to_bf16(in[i]);
   }
 }
 
-template <bool NT>
+template <bool NT, bool TAIL>
 __device__ __forceinline__ void store8(float* row, int64_t v, int n, const float* in) {
   const int64_t at = v * kVec;
-  if (at + kVec <= n) {
+  if (TAIL ? at + kVec <= n : at < n) {
     f32x4_a4* p = reinterpret_cast<f32x4_a4*>(row + at);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -114,7 +155,7 @@ __device__ __forceinline__ void store8(float* row, int64_t v, int n, const float
       if (NT) __builtin_nontemporal_store(b, p + h);
       else p[h] = b;
     }
-  } else {
+  } else if (TAIL && at < n) {
 #pragma unroll
     for (int i = 0; i < kVec; ++i)
       if (at + i < n) row[at + i] = in[i];

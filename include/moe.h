@@ -378,7 +378,7 @@ int moe_combine(const float* y_perm, const int32_t* row_of, const float* topk_w,
  *   gamma, beta device f32[H]; beta may be NULL (no shift)
  *   mean, rstd  device f32[T] (written; what the backward pass reads); either may be NULL
  * Errors: MOE_ERR_ARG for null pointers, bad sizes or eps negative or NaN; MOE_ERR_UNSUPPORTED
- * for H > 2^28.  T = 0 is a no-op.
+ * for H > 2^26.  T = 0 is a no-op.
  */
 int moe_layer_norm(const void* x, const float* gamma, const float* beta, int T, int H, float eps,
                    moe_dtype dtype, void* y, float* mean, float* rstd, moe_stream_t stream);
@@ -413,7 +413,7 @@ int moe_layer_norm_backward(const void* dy, const void* x, const float* gamma, c
  * Rows that row_of does not name keep what they held; an index outside [0, T*k) (an assignment
  * that moe_permute dropped) writes no row, and its dtopk_w is 0.
  * Errors: MOE_ERR_ARG for null pointers or bad sizes; MOE_ERR_UNSUPPORTED for k > MOE_MAX_K,
- * T*k >= 2^31 or H > 2^28.
+ * T*k >= 2^31 or H > 2^26.
  */
 int moe_combine_backward(const void* dy, moe_dtype dy_dtype, const float* y_perm,
                          const int32_t* row_of, const float* topk_w, int T, int k, int H,
@@ -425,7 +425,7 @@ int moe_combine_backward(const void* dy, moe_dtype dy_dtype, const float* y_perm
  *   dx_perm device [T*k][H] dtype; dx device [T][H] dtype
  * An index outside [0, T*k) adds nothing.
  * Errors: MOE_ERR_ARG for null pointers or bad sizes; MOE_ERR_UNSUPPORTED for T*k >= 2^31 or
- * H > 2^28.
+ * H > 2^26.
  */
 int moe_permute_backward(const void* dx_perm, const int32_t* row_of, int T, int k, int H,
                          moe_dtype dtype, void* dx, moe_stream_t stream);
