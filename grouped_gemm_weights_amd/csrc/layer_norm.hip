@@ -374,7 +374,8 @@ constexpr int kPartials = kCus;                              // most blocks of t
 constexpr int kJoinBytes = kMaxWaves * kWave * kVec * 2 * sizeof(float);  // 64 KB: 16 waves' sums
 
 // Waves per row and rows at once per block of the backward pass: as many waves as the row has 512
-// columns, as many rows as 16 waves hold.
+// columns, as many rows as 16 waves hold, and a block a CU: twice the blocks at 10 waves each mean
+// twice the partial rows, which cost more than they gain (4099 x 1001 f32: 24.6 against 19.6 us).
 struct BackwardShape {
   int nv, waves, groups, blocks;
 };
@@ -396,9 +397,14 @@ template <typename E, int NV>
 int launch_norm(const void* x, const float* gamma, const float* beta, int T, int H, float eps, void* y,
                 float* mean, float* rstd, hipStream_t s) {
   const int waves = ceil_div(H, NV * kWave * kVec), rows = waves == 1 ? 4 : 1;
-  // as many blocks as the CUs hold at once (20 waves a CU at these kernels' registers)
-  const int blocks = std::min(ceil_div(T, rows), kCus * std::max(1, 20 / (waves * rows)));
-  auto kernel = H % kVec == 0 ? norm_kernel<E, NV, NV <= 2, false> : norm_kernel<E, NV, NV <= 2, true>;
+  // as many blocks as the CUs hold at once (16 waves a CU at the registers of KEEP); when that is
+  // every row, KEEP has nothing to keep for, and its registers only take waves from the CU
+  const int all = ceil_div(T, rows), most = kCus * std::max(1, 16 / (waves * rows));
+  const bool keep = NV <= 2 && all > 2 * most;
+  const int blocks = keep ? std::min(all, most) : all;
+  auto kernel = H % kVec == 0
+                    ? (keep ? norm_kernel<E, NV, NV <= 2, false> : norm_kernel<E, NV, false, false>)
+                    : (keep ? norm_kernel<E, NV, NV <= 2, true> : norm_kernel<E, NV, false, true>);
   hipLaunchKernelGGL(kernel, dim3(blocks), dim3(waves * rows * kWave), 0, s,
                      static_cast<const E*>(x), gamma, beta, T, H, waves, eps, static_cast<E*>(y), mean,
                      rstd);

@@ -73,29 +73,26 @@ __device__ __forceinline__ void load_raw(const float* row, int64_t v, int n, Raw
   }
 }
 
+// Whole waves branch over the shift (one wave of a row has a piece to shift), lanes select.
 template <bool TAIL>
 __device__ __forceinline__ void unpack(const Raw8<uint16_t>& r, int64_t v, int n, float* out) {
   uint32_t w[4] = {r.w[0], r.w[1], r.w[2], r.w[3]};
   const int64_t over = v * kVec + kVec - n;
-  if (TAIL && over > 0) {
-    const int sh = static_cast<int>(over);
-    if (sh & 4) {
-      w[0] = w[2];
-      w[1] = w[3];
-      w[2] = w[3] = 0;
-    }
-    if (sh & 2) {
-      w[0] = w[1];
-      w[1] = w[2];
-      w[2] = w[3];
-      w[3] = 0;
-    }
-    if (sh & 1) {
-      w[0] = w[0] >> 16 | w[1] << 16;
-      w[1] = w[1] >> 16 | w[2] << 16;
-      w[2] = w[2] >> 16 | w[3] << 16;
-      w[3] >>= 16;
-    }
+  if (TAIL && __any(over > 0)) {
+    const int sh = over > 0 ? static_cast<int>(over) : 0;
+    const bool four = sh & 4, two = sh & 2, one = sh & 1;
+    w[0] = four ? w[2] : w[0];
+    w[1] = four ? w[3] : w[1];
+    w[2] = four ? 0 : w[2];
+    w[3] = four ? 0 : w[3];
+    w[0] = two ? w[1] : w[0];
+    w[1] = two ? w[2] : w[1];
+    w[2] = two ? w[3] : w[2];
+    w[3] = two ? 0 : w[3];
+    w[0] = one ? w[0] >> 16 | w[1] << 16 : w[0];
+    w[1] = one ? w[1] >> 16 | w[2] << 16 : w[1];
+    w[2] = one ? w[2] >> 16 | w[3] << 16 : w[2];
+    w[3] = one ? w[3] >> 16 : w[3];
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -109,13 +106,17 @@ __device__ __forceinline__ void unpack(const Raw8<float>& r, int64_t v, int n, f
 #pragma unroll
   for (int i = 0; i < kVec; ++i) out[i] = r.w[i];
   const int64_t over = v * kVec + kVec - n;
-  if (TAIL && over > 0) {
-    const int sh = static_cast<int>(over);
+  if (TAIL && __any(over > 0)) {
+    const int sh = over > 0 ? static_cast<int>(over) : 0;
 #pragma unroll
-    for (int step = 4; step >= 1; step /= 2)
-      if (sh & step)
+    for (int step = 4; step >= 1; step /= 2) {
+      const bool take = sh & step;
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) out[i] = i + step < kVec ? out[i + step] : 0.f;
+      for (int i = 0; i < kVec; ++i) {
+        const float next = i + step < kVec ? out[i + step] : 0.f;
+        out[i] = take ? next : out[i];
+      }
+    }
   }
 }
 
