@@ -13,7 +13,7 @@
 //   4. dW: [dWg; dWu] = [dG dU]^T X and dWd = dY^T h, one block per expert and output tile
 //
 // bf16: the tile product of mfma_tile.h; dH and dX read the weights transposed, dW both operands.
-// f32: 128 x 128 tiles of the fp32 MFMA (32x32x2), staged through registers.
+// f32: 64 x 64 tiles of the fp32 MFMA (32x32x2), staged through registers.
 #include <algorithm>
 #include <type_traits>
 
@@ -30,9 +30,9 @@ struct Tile {
 };
 
 constexpr int kMaxSide = 1 << 20;  // largest H and I: bounds the grids
-constexpr int kBM = 128, kBN = 128, kBK = 16;  // f32 tile
-constexpr int kLd = kBM + 4;                   // LDS row (one k) of an f32 operand tile
-constexpr int kRowTile = 256;                  // bf16: rows of a tile
+constexpr int kBM = 64, kBN = 64, kBK = 32;  // f32 tile
+constexpr int kLd = kBM + 33;                // LDS row (one k) of an f32 operand tile
+constexpr int kRowTile = 256;                // bf16: rows of a tile
 
 int tile_rows(moe_dtype dt) { return dt == MOE_BF16 ? kRowTile : kBM; }
 
@@ -108,71 +108,135 @@ __device__ __forceinline__ void swiglu_grad(float g, float u, float d, float* dg
 // f32
 // ---------------------------------------------------------------------------
 
-// One stage of an operand: 128 "outer" indices by 16 depth steps into LDS as [depth][outer], zero
-// outside [0, n_outer) and [0, K).  KMAJOR: element (o, k) is at p[k * ld + o], else at
-// p[o * ld + k].  `at(o)` maps a tile's outer index to the operand's (or -1).
-template <bool KMAJOR, typename At>
-__device__ __forceinline__ void stage(const float* __restrict__ p, int64_t ld, int k0, int K, At at,
-                                      float* __restrict__ lds) {
-  const int tid = threadIdx.x;
-#pragma unroll
-  for (int i = 0; i < kBM * kBK / 256; ++i) {
-    const int o = KMAJOR ? tid % kBM : tid / kBK + i * (256 / kBK);
-    const int k = KMAJOR ? tid / kBM + i * (256 / kBM) : tid % kBK;
-    const int src = at(o);
-    float v = 0.f;
-    if (src >= 0 && k0 + k < K)
-      v = KMAJOR ? p[static_cast<int64_t>(k0 + k) * ld + src]
-                 : p[static_cast<int64_t>(src) * ld + k0 + k];
-    lds[k * kLd + o] = v;
-  }
-}
+// Tiles of 64 x 64, four waves of one 32 x 32 block each: small enough that the few rows of an
+// expert still make blocks for every CU, several of which share a CU and hide one another's
+// latency.  A stage is 32 of depth; the next two stages' loads are in flight while this one's
+// MFMAs run, LDS is double-buffered and an even and an odd accumulator keep two MFMAs independent.
 
-// acc[i][j] += A B over depth [0, K): 4 waves as 2 x 2, each 64 rows (i) by two 32-column blocks
-// whose tile columns start at wcol[j].
-template <bool A_KMAJOR, bool B_KMAJOR, typename AtA, typename AtB>
-__device__ __forceinline__ void tile_product_f32(const float* __restrict__ A, int64_t lda, AtA at_a,
-                                                 const float* __restrict__ B, int64_t ldb, AtB at_b,
-                                                 int K, const int (&wcol)[2], float* As, float* Bs,
-                                                 floatx16 (&acc)[2][2]) {
-  const int lane = threadIdx.x & (kWave - 1);
-  const int wm = (threadIdx.x / kWave) >> 1;
-  for (int k0 = 0; k0 < K; k0 += kBK) {
-    stage<A_KMAJOR>(A, lda, k0, K, at_a, As);
-    stage<B_KMAJOR>(B, ldb, k0, K, at_b, Bs);
-    __syncthreads();
+typedef float f32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
+
+// This thread's 8 elements of a stage of an operand: 64 "outer" indices by 32 of depth, zero outside
+// the operand.  KMAJOR: element (o, k) is at p[k * ld + o], else at p[o * ld + k]; either way four
+// elements that lie together in memory are one load where all four exist.  Two pieces alternate,
+// each a stage ahead of the other.  at(o) maps a tile's outer index to the operand's, or to -1;
+// four from a multiple of 4 stay together (KMAJOR).
+template <bool KMAJOR>
+struct Piece {
+  const float* p[2];  // this thread's elements of the stage to load next
+  int n[2];           // how many of the four exist (KMAJOR: columns; else 4 or 0)
+  int64_t step;       // two stages on
+  int k;              // depth of the first of them within the operand
+  float v[2][4];
+
+  template <typename At>
+  __device__ __forceinline__ void init(const float* base, int64_t ld, int k0, At at) {
+    const int tid = threadIdx.x;
+    k = k0 + (KMAJOR ? tid >> 4 : (tid & 7) * 4);
+    step = 2 * kBK * (KMAJOR ? ld : 1);
 #pragma unroll
-    for (int k = 0; k < kBK; k += 2) {
-      const int row = (k + (lane >> 5)) * kLd + (lane & 31);
-      float a[2], b[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) a[i] = As[row + wm * 64 + i * 32];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) b[j] = Bs[row + wcol[j]];
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i], b[j], acc[i][j], 0, 0, 0);
+    for (int i = 0; i < 2; ++i) {
+      const int o = KMAJOR ? (tid & 15) * 4 : (tid >> 3) + i * 32;
+      n[i] = 0;
+      if (KMAJOR) {
+        while (n[i] < 4 && at(o + n[i]) >= 0) ++n[i];
+      } else if (at(o) >= 0) {
+        n[i] = 4;
+      }
+      const int src = n[i] ? at(o) : 0;
+      p[i] = base + (KMAJOR ? static_cast<int64_t>(k + 16 * i) * ld + src : static_cast<int64_t>(src) * ld + k);
     }
-    __syncthreads();
   }
+
+  __device__ __forceinline__ void load(int K) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      // of the four, those inside the depth too
+      const int left = K - k;
+      const int m = KMAJOR ? (left > 16 * i ? n[i] : 0) : min(n[i], left);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[i][j] = 0.f;
+      if (m == 4) {
+        const f32x4_a4 q = *reinterpret_cast<const f32x4_a4*>(p[i]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[i][j] = q[j];
+      } else if (m > 0) {
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+          if (j < m) v[i][j] = p[i][j];
+      }
+      p[i] += step;
+    }
+    k += 2 * kBK;
+  }
+
+  // To LDS as [depth][outer], rows of 97 floats: the transposing writes of a row operand and the
+  // fragment reads (two depths of 32) spread over the banks.
+  __device__ __forceinline__ void store(float* __restrict__ lds) const {
+    const int tid = threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int o = KMAJOR ? (tid & 15) * 4 + j : (tid >> 3) + i * 32;
+        const int k = KMAJOR ? (tid >> 4) + i * 16 : (tid & 7) * 4 + j;
+        lds[k * kLd + o] = v[i][j];
+      }
+  }
+};
+
+constexpr int kF32Lds = kBK * kLd;  // floats of one operand's stage
+
+// The wave's 32 x 32 block (rows 32 (wave / 2), tile columns 32 (wave % 2)) of A B over depth
+// [0, K).  lds: two stages of two operands.
+template <bool A_KMAJOR, bool B_KMAJOR, typename AtA, typename AtB>
+__device__ __forceinline__ floatx16 tile_product_f32(const float* __restrict__ A, int64_t lda, AtA at_a,
+                                                     const float* __restrict__ B, int64_t ldb, AtB at_b,
+                                                     int K, float* lds) {
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  const int ra = (lane >> 5) * kLd + (wave >> 1) * 32 + (lane & 31);
+  const int rb = (lane >> 5) * kLd + (wave & 1) * 32 + (lane & 31) + kF32Lds;
+  floatx16 even, odd;
+#pragma unroll
+  for (int q = 0; q < 16; ++q) even[q] = odd[q] = 0.f;
+  Piece<A_KMAJOR> pa[2];
+  Piece<B_KMAJOR> pb[2];
+  auto load = [&](int i) {
+    pa[i].load(K);
+    pb[i].load(K);
+  };
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    pa[i].init(A, lda, i * kBK, at_a);
+    pb[i].init(B, ldb, i * kBK, at_b);
+    load(i);
+  }
+  // stage i & 1, from its registers and into its LDS.  The barrier of the next stage orders these
+  // reads before the same buffer is written again.
+  auto stage = [&](int i) {
+    float* cur = lds + i * 2 * kF32Lds;
+    pa[i].store(cur);
+    pb[i].store(cur + kF32Lds);
+    __syncthreads();
+    load(i);
+#pragma unroll
+    for (int k = 0; k < kBK; k += 4) {
+      even = __builtin_amdgcn_mfma_f32_32x32x2f32(cur[k * kLd + ra], cur[k * kLd + rb], even, 0, 0, 0);
+      odd = __builtin_amdgcn_mfma_f32_32x32x2f32(cur[(k + 2) * kLd + ra], cur[(k + 2) * kLd + rb], odd, 0, 0, 0);
+    }
+  };
+  for (int k0 = 0; k0 < K; k0 += 2 * kBK) {
+    stage(0);
+    if (k0 + kBK < K) stage(1);
+  }
+  return even + odd;
 }
 
-__device__ __forceinline__ void clear(floatx16 (&acc)[2][2]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
-}
-
-// Element q of 32x32 block i of this lane: row within the tile.
-__device__ __forceinline__ int acc_row(int i, int q) {
+// Row within the tile of element q of this lane's block; its tile column is 32 (wave % 2) + lane % 32.
+__device__ __forceinline__ int acc_row(int q) {
   const int lane = threadIdx.x & (kWave - 1);
-  return ((threadIdx.x / kWave) >> 1) * 64 + i * 32 + (q >> 2) * 8 + (lane >> 5) * 4 + (q & 3);
+  return (threadIdx.x / kWave >> 1) * 32 + (q >> 2) * 8 + (lane >> 5) * 4 + (q & 3);
 }
+__device__ __forceinline__ int acc_col() { return (threadIdx.x / kWave & 1) * 32 + (threadIdx.x & 31); }
 
 // C[r][n] = sum_k A[r][k] B[k][n] for the rows of each tile; B of the tile's expert starts at
 // b_off of its block.
@@ -180,102 +244,84 @@ __global__ __launch_bounds__(256) void rows_product_f32_kernel(
     const float* __restrict__ A, int64_t lda, const char* __restrict__ wbase, int64_t expert_bytes,
     int64_t b_off, int N, int K, const Tile* __restrict__ tiles, const int32_t* __restrict__ n_tiles,
     float* __restrict__ C) {
-  __shared__ float As[kBK * kLd], Bs[kBK * kLd];
+  __shared__ float lds[4 * kF32Lds];
   if (static_cast<int>(blockIdx.x) >= *n_tiles) return;
   const Tile t = tiles[blockIdx.x];
   const int n0 = blockIdx.y * kBN;
-  const int wn = (threadIdx.x / kWave) & 1;
   const float* B = reinterpret_cast<const float*>(wbase + t.slot * expert_bytes + b_off);
-  const int wcol[2] = {wn * 64, wn * 64 + 32};
-  floatx16 acc[2][2];
-  clear(acc);
-  tile_product_f32<false, true>(
+  const floatx16 acc = tile_product_f32<false, true>(
       A + t.row0 * lda, lda, [&](int o) { return o < t.rows ? o : -1; }, B, N,
-      [&](int o) { return n0 + o < N ? n0 + o : -1; }, K, wcol, As, Bs, acc);
+      [&](int o) { return n0 + o < N ? n0 + o : -1; }, K, lds);
+  const int c = n0 + acc_col();
+  if (c >= N) return;
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      const int r = acc_row(i, q);
-      if (r >= t.rows) continue;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int c = n0 + wcol[j] + (threadIdx.x & 31);
-        if (c < N) C[static_cast<int64_t>(t.row0 + r) * N + c] = acc[i][j][q];
-      }
-    }
+  for (int q = 0; q < 16; ++q)
+    if (acc_row(q) < t.rows) C[static_cast<int64_t>(t.row0 + acc_row(q)) * N + c] = acc[q];
 }
 
-// g and u for 64 columns, then dG, dU and h from dH.
+// g and u for 32 columns, then dG, dU and h from dH.  Each wave's 32 tile columns are 16 of Wg and
+// the same 16 of Wu: lanes l and l ^ 16 hold g and u of one element.
 __global__ __launch_bounds__(256) void gate_up_backward_f32_kernel(
     const float* __restrict__ x, const char* __restrict__ wbase, int64_t expert_bytes, int H, int I,
     const Tile* __restrict__ tiles, const int32_t* __restrict__ n_tiles, const float* __restrict__ dh,
     float* __restrict__ dgu, float* __restrict__ h) {
-  __shared__ float As[kBK * kLd], Bs[kBK * kLd];
+  __shared__ float lds[4 * kF32Lds];
   if (static_cast<int>(blockIdx.x) >= *n_tiles) return;
   const Tile t = tiles[blockIdx.x];
   const int n0 = blockIdx.y * (kBN / 2);
-  const int wn = (threadIdx.x / kWave) & 1;
   const float* W = reinterpret_cast<const float*>(wbase + t.slot * expert_bytes);
-  // B tile: 64 rows of Wg, then the same 64 rows of Wu, so a wave holds matching columns of both
-  const int wcol[2] = {wn * 32, 64 + wn * 32};
-  floatx16 acc[2][2];
-  clear(acc);
-  tile_product_f32<false, false>(
+  const int c = n0 + (threadIdx.x / kWave & 1) * 16 + (threadIdx.x & 15);
+  const bool up = threadIdx.x & 16;
+  // dH arrives while the products run; a lane past the tile or past I reads a place inside
+  float d[16];
+#pragma unroll
+  for (int q = 0; q < 16; ++q)
+    d[q] = dh[static_cast<int64_t>(t.row0 + min(acc_row(q), t.rows - 1)) * I + min(c, I - 1)];
+  const floatx16 acc = tile_product_f32<false, false>(
       x + static_cast<int64_t>(t.row0) * H, H, [&](int o) { return o < t.rows ? o : -1; }, W, H,
       [&](int o) {
-        const int c = n0 + (o & 63);
-        return c < I ? c + (o >> 6) * I : -1;
+        const int c = n0 + (o >> 5) * 16 + (o & 15);
+        return c < I ? c + (o >> 4 & 1) * I : -1;
       },
-      H, wcol, As, Bs, acc);
-  const int c = n0 + wn * 32 + (threadIdx.x & 31);
-  if (c >= I) return;
+      H, lds);
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      const int r = acc_row(i, q);
-      if (r >= t.rows) continue;
-      const int64_t row = t.row0 + r;
-      swiglu_grad(acc[i][0][q], acc[i][1][q], dh[row * I + c], dgu + row * 2 * I + c,
-                  dgu + row * 2 * I + I + c, h + row * I + c);
+  for (int q = 0; q < 16; ++q) {
+    const float mate = __shfl_xor(acc[q], 16);
+    if (acc_row(q) >= t.rows || c >= I) continue;
+    const int64_t row = t.row0 + acc_row(q);
+    float dg, du, hv;
+    swiglu_grad(up ? mate : acc[q], up ? acc[q] : mate, d[q], &dg, &du, &hv);
+    if (up) {
+      dgu[row * 2 * I + I + c] = du;
+    } else {
+      dgu[row * 2 * I + c] = dg;
+      h[row * I + c] = hv;
     }
+  }
 }
 
 // C[m][n] = sum over the expert's rows r of A[r][m] B[r][n], written at c_off of the expert's
 // block of dw.  An expert without rows gets zeros, one outside the buffer nothing.
 __global__ __launch_bounds__(256) void weight_grad_f32_kernel(
-    const float* __restrict__ A, int M, const float* __restrict__ B, int N, const int32_t* __restrict__ offsets,
-    int R, const int32_t* __restrict__ slot_of, int n_slots, int64_t expert_bytes, int64_t c_off,
-    char* __restrict__ dw) {
-  __shared__ float As[kBK * kLd], Bs[kBK * kLd];
+    const float* __restrict__ A, int M, const float* __restrict__ B, int N,
+    const int32_t* __restrict__ offsets, int R, const int32_t* __restrict__ slot_of, int n_slots,
+    int64_t expert_bytes, int64_t c_off, char* __restrict__ dw) {
+  __shared__ float lds[4 * kF32Lds];
   const int e = blockIdx.z;
   const int slot = slot_of[e];
   if (slot < 0 || slot >= n_slots) return;
   int lo;
   const int K = expert_rows(offsets, e, R, &lo);
   const int m0 = blockIdx.x * kBM, n0 = blockIdx.y * kBN;
-  const int wn = (threadIdx.x / kWave) & 1;
-  const int wcol[2] = {wn * 64, wn * 64 + 32};
-  floatx16 acc[2][2];
-  clear(acc);
-  tile_product_f32<true, true>(
+  const floatx16 acc = tile_product_f32<true, true>(
       A + static_cast<int64_t>(lo) * M, M, [&](int o) { return m0 + o < M ? m0 + o : -1; },
-      B + static_cast<int64_t>(lo) * N, N, [&](int o) { return n0 + o < N ? n0 + o : -1; }, K, wcol, As,
-      Bs, acc);
+      B + static_cast<int64_t>(lo) * N, N, [&](int o) { return n0 + o < N ? n0 + o : -1; }, K, lds);
   float* C = reinterpret_cast<float*>(dw + slot * expert_bytes + c_off);
+  const int c = n0 + acc_col();
+  if (c >= N) return;
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      const int m = m0 + acc_row(i, q);
-      if (m >= M) continue;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int c = n0 + wcol[j] + (threadIdx.x & 31);
-        if (c < N) C[static_cast<int64_t>(m) * N + c] = acc[i][j][q];
-      }
-    }
+  for (int q = 0; q < 16; ++q)
+    if (m0 + acc_row(q) < M) C[static_cast<int64_t>(m0 + acc_row(q)) * N + c] = acc[q];
 }
 
 // ---------------------------------------------------------------------------
