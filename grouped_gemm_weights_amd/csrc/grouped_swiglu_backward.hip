@@ -6,11 +6,14 @@
 //   h = g sg u,  dU = dH g sg,  dG = dH u sg (1 + g (1 - sg))
 //   dX = dG Wg + dU Wu
 //   dWg = dG^T X,  dWu = dU^T X,  dWd = dY^T h
-// 16 R H I operations, in four launches after the tile plan:
+// 16 R H I operations, in three launches:
 //   1. dH            (kept in fp32: dG and dU are its only roundings on the way to dX and dW)
 //   2. g, u, then in the epilogue dG | dU as one [R][2I] matrix and h
-//   3. dX = [dG dU] [Wg; Wu]: one product of depth 2I, as Wg and Wu lie one after the other
-//   4. dW: [dWg; dWu] = [dG dU]^T X and dWd = dY^T h, one block per expert and output tile
+//   3. dX = [dG dU] [Wg; Wu], one product of depth 2I, as Wg and Wu lie one after the other, and
+//      dW: [dWg; dWu] = [dG dU]^T X and dWd = dY^T h, one block per expert and output tile.  The
+//      three are independent, so the blocks of one fill the CUs that the last of another leave.
+// A block finds its tile of rows from offsets by itself (find_tile: a scan over the experts in
+// each wave, about 1 us of a block's time, against 4-5 us for a launch that lists the tiles).
 //
 // bf16: the tile product of mfma_tile.h; dH and dX read the weights transposed, dW both operands.
 // f32: 64 x 64 tiles of the fp32 MFMA (32x32x2), staged through registers.
@@ -22,76 +25,89 @@
 namespace moe {
 namespace {
 
-struct Tile {
-  int32_t expert;
-  int32_t row0;
-  int32_t rows;
-  int32_t slot;
-};
-
 constexpr int kMaxSide = 1 << 20;  // largest H and I: bounds the grids
 constexpr int kBM = 64, kBN = 64, kBK = 32;  // f32 tile
 constexpr int kLd = kBM + 33;                // LDS row (one k) of an f32 operand tile
-constexpr int kRowTile = 256;                // bf16: rows of a tile
-
-int tile_rows(moe_dtype dt) { return dt == MOE_BF16 ? kRowTile : kBM; }
-
-int64_t max_tiles(int64_t R, int E, moe_dtype dt) {
-  return ceil_div64(R, tile_rows(dt)) + std::min<int64_t>(E, R);
-}
 
 struct BackwardWs {
-  size_t dh_off, dgu_off, h_off, tiles_off, count_off, total;
+  size_t dh_off, dgu_off, h_off, total;
 };
 
-BackwardWs backward_ws(int64_t R, int E, int I, moe_dtype dt) {
+BackwardWs backward_ws(int64_t R, int I, moe_dtype dt) {
   const size_t n = static_cast<size_t>(R) * I;
   BackwardWs w;
   w.dh_off = 0;
   w.dgu_off = align_up(n * sizeof(float), 256);
   w.h_off = w.dgu_off + align_up(2 * n * elem_size(dt), 256);
-  w.tiles_off = w.h_off + align_up(n * elem_size(dt), 256);
-  w.count_off = w.tiles_off + align_up(static_cast<size_t>(max_tiles(R, E, dt)) * sizeof(Tile), 256);
-  w.total = w.count_off + 256;
+  w.total = w.h_off + align_up(n * elem_size(dt), 256) + 256;
   return w;
 }
 
+// Most tiles of `tr` rows that R rows of E experts can make.
+int64_t max_tiles(int64_t R, int E, int tr) { return ceil_div64(R, tr) + std::min<int64_t>(E, R); }
+
+// The experts' rows and slots.
+struct Experts {
+  const int32_t* offsets;
+  const int32_t* slot_of;
+  int R, E, n_slots;
+  int32_t* status;
+};
+
 // Rows [lo, lo + count) of expert e, held to [0, R) whatever offsets says.
-__device__ __forceinline__ int expert_rows(const int32_t* offsets, int e, int R, int* lo) {
-  const int a = min(max(offsets[e], 0), R), b = min(max(offsets[e + 1], 0), R);
+__device__ __forceinline__ int expert_rows(const Experts& x, int e, int* lo) {
+  const int a = min(max(x.offsets[e], 0), x.R), b = min(max(x.offsets[e + 1], 0), x.R);
   *lo = a;
   return max(b - a, 0);
 }
 
-// Row tiles of BM rows per expert, expert-major.
-__global__ __launch_bounds__(MOE_MAX_E) void backward_plan_kernel(
-    const int32_t* __restrict__ offsets, int R, int E, int BM, const int32_t* __restrict__ slot_of,
-    int n_slots, int tile_cap, Tile* __restrict__ tiles, int32_t* __restrict__ n_tiles,
-    int32_t* status) {
-  __shared__ int32_t s[MOE_MAX_E];
-  const int e = threadIdx.x;
-  int n = 0, lo = 0, cnt = 0, slot = -1;
-  if (e < E) {
-    cnt = expert_rows(offsets, e, R, &lo);
-    if (cnt > 0) {
-      slot = slot_of[e];
-      // a slot outside the merged buffer is treated as absent, never read
-      if (slot < 0 || slot >= n_slots) status_or(status, MOE_STATUS_EXPERT_ABSENT);
-      else n = (cnt + BM - 1) / BM;
+struct Tile {
+  int row0, rows, slot;
+};
+
+// Tile m of the list that cuts each expert's rows into tiles of TR, expert by expert, leaving out
+// experts without a slot in the merged buffer (a slot outside it is treated as absent, never
+// read; `report`: their status bit is set).  False past the last tile.  Wave-uniform.
+template <int TR>
+__device__ __forceinline__ bool find_tile(const Experts& x, int m, bool report, Tile* t) {
+  const int lane = threadIdx.x & (kWave - 1);
+  const int per = (x.E + kWave - 1) / kWave;  // experts of a lane
+  const int e0 = min(lane * per, x.E), e1 = min(e0 + per, x.E);
+  int n = 0, lo;
+  for (int e = e0; e < e1; ++e) {
+    const int cnt = expert_rows(x, e, &lo);
+    if (cnt == 0) continue;
+    const int slot = x.slot_of[e];
+    if (slot >= 0 && slot < x.n_slots) n += (cnt + TR - 1) / TR;
+    else if (report) status_or(x.status, MOE_STATUS_EXPERT_ABSENT);
+  }
+  int end = n;  // tiles up to and with this lane's experts
+#pragma unroll
+  for (int off = 1; off < kWave; off <<= 1) {
+    const int add = __shfl_up(end, off);
+    if (lane >= off) end += add;
+  }
+  const uint64_t mine = __ballot(m >= end - n && m < end);
+  if (mine == 0) return false;
+  int at = m - (end - n), row0 = 0, rows = 0, slot = 0;
+  for (int e = e0; e < e1; ++e) {
+    const int cnt = expert_rows(x, e, &lo);
+    if (cnt == 0) continue;
+    const int s = x.slot_of[e];
+    if (s < 0 || s >= x.n_slots) continue;
+    const int tiles = (cnt + TR - 1) / TR;
+    if (at >= 0 && at < tiles) {
+      row0 = lo + at * TR;
+      rows = min(TR, cnt - at * TR);
+      slot = s;
     }
+    at -= tiles;
   }
-  s[e] = n;
-  __syncthreads();
-  for (int off = 1; off < MOE_MAX_E; off <<= 1) {
-    const int32_t add = e >= off ? s[e - off] : 0;
-    __syncthreads();
-    s[e] += add;
-    __syncthreads();
-  }
-  const int first = s[e] - n;
-  for (int i = 0; i < n && first + i < tile_cap; ++i)
-    tiles[first + i] = Tile{e, lo + i * BM, min(BM, cnt - i * BM), slot};
-  if (e == 0) *n_tiles = min(s[MOE_MAX_E - 1], tile_cap);
+  const int owner = __builtin_ctzll(mine);
+  t->row0 = __builtin_amdgcn_readlane(row0, owner);
+  t->rows = __builtin_amdgcn_readlane(rows, owner);
+  t->slot = __builtin_amdgcn_readlane(slot, owner);
+  return true;
 }
 
 // dG, dU and h of one element, from g, u and dH.  exp2 and reciprocal are the hardware's (about 1
@@ -238,16 +254,14 @@ __device__ __forceinline__ int acc_row(int q) {
 }
 __device__ __forceinline__ int acc_col() { return (threadIdx.x / kWave & 1) * 32 + (threadIdx.x & 31); }
 
-// C[r][n] = sum_k A[r][k] B[k][n] for the rows of each tile; B of the tile's expert starts at
-// b_off of its block.
-__global__ __launch_bounds__(256) void rows_product_f32_kernel(
-    const float* __restrict__ A, int64_t lda, const char* __restrict__ wbase, int64_t expert_bytes,
-    int64_t b_off, int N, int K, const Tile* __restrict__ tiles, const int32_t* __restrict__ n_tiles,
-    float* __restrict__ C) {
-  __shared__ float lds[4 * kF32Lds];
-  if (static_cast<int>(blockIdx.x) >= *n_tiles) return;
-  const Tile t = tiles[blockIdx.x];
-  const int n0 = blockIdx.y * kBN;
+// C[r][n] = sum_k A[r][k] B[k][n] for tile m's rows and columns n0 .. n0 + 63; B of the tile's expert
+// starts at b_off of its block.
+__device__ __forceinline__ void rows_product_f32(const Experts& x, int m, int n0, bool report,
+                                                 const float* A, int64_t lda, const char* wbase,
+                                                 int64_t expert_bytes, int64_t b_off, int N, int K,
+                                                 float* C, float* lds) {
+  Tile t;
+  if (!find_tile<kBM>(x, m, report, &t)) return;
   const float* B = reinterpret_cast<const float*>(wbase + t.slot * expert_bytes + b_off);
   const floatx16 acc = tile_product_f32<false, true>(
       A + t.row0 * lda, lda, [&](int o) { return o < t.rows ? o : -1; }, B, N,
@@ -259,15 +273,22 @@ __global__ __launch_bounds__(256) void rows_product_f32_kernel(
     if (acc_row(q) < t.rows) C[static_cast<int64_t>(t.row0 + acc_row(q)) * N + c] = acc[q];
 }
 
+__global__ __launch_bounds__(256) void dh_f32_kernel(Experts x, const float* __restrict__ dy,
+                                                     const char* __restrict__ wbase, int64_t expert_bytes,
+                                                     int H, int I, float* __restrict__ dh) {
+  __shared__ float lds[4 * kF32Lds];
+  rows_product_f32(x, blockIdx.x, blockIdx.y * kBN, blockIdx.x == 0 && blockIdx.y == 0, dy, H, wbase,
+                   expert_bytes, 2 * static_cast<int64_t>(H) * I * 4, I, H, dh, lds);
+}
+
 // g and u for 32 columns, then dG, dU and h from dH.  Each wave's 32 tile columns are 16 of Wg and
 // the same 16 of Wu: lanes l and l ^ 16 hold g and u of one element.
 __global__ __launch_bounds__(256) void gate_up_backward_f32_kernel(
-    const float* __restrict__ x, const char* __restrict__ wbase, int64_t expert_bytes, int H, int I,
-    const Tile* __restrict__ tiles, const int32_t* __restrict__ n_tiles, const float* __restrict__ dh,
-    float* __restrict__ dgu, float* __restrict__ h) {
+    Experts ex, const float* __restrict__ x, const char* __restrict__ wbase, int64_t expert_bytes, int H,
+    int I, const float* __restrict__ dh, float* __restrict__ dgu, float* __restrict__ h) {
   __shared__ float lds[4 * kF32Lds];
-  if (static_cast<int>(blockIdx.x) >= *n_tiles) return;
-  const Tile t = tiles[blockIdx.x];
+  Tile t;
+  if (!find_tile<kBM>(ex, blockIdx.x, false, &t)) return;
   const int n0 = blockIdx.y * (kBN / 2);
   const float* W = reinterpret_cast<const float*>(wbase + t.slot * expert_bytes);
   const int c = n0 + (threadIdx.x / kWave & 1) * 16 + (threadIdx.x & 15);
@@ -300,19 +321,21 @@ __global__ __launch_bounds__(256) void gate_up_backward_f32_kernel(
   }
 }
 
-// C[m][n] = sum over the expert's rows r of A[r][m] B[r][n], written at c_off of the expert's
-// block of dw.  An expert without rows gets zeros, one outside the buffer nothing.
-__global__ __launch_bounds__(256) void weight_grad_f32_kernel(
-    const float* __restrict__ A, int M, const float* __restrict__ B, int N,
-    const int32_t* __restrict__ offsets, int R, const int32_t* __restrict__ slot_of, int n_slots,
-    int64_t expert_bytes, int64_t c_off, char* __restrict__ dw) {
-  __shared__ float lds[4 * kF32Lds];
-  const int e = blockIdx.z;
-  const int slot = slot_of[e];
-  if (slot < 0 || slot >= n_slots) return;
+// The third launch: dX, [dWg; dWu] and dWd.  Block ranges in this order, each possibly empty.
+struct Ranges {
+  int64_t dx, dwgu;  // blocks of dX, and of [dWg; dWu]
+  int per_gu, per_d;  // blocks of an expert in the second and third range
+};
+
+// C[m][n] = sum over expert e's rows r of A[r][m] B[r][n], written at c_off of the expert's block of
+// dw.  An expert without rows gets zeros, one outside the buffer nothing.
+__device__ __forceinline__ void weight_grad_f32(const Experts& x, int e, int m0, int n0, const float* A,
+                                                int M, const float* B, int N, int64_t expert_bytes,
+                                                int64_t c_off, char* dw, float* lds) {
+  const int slot = x.slot_of[e];
+  if (slot < 0 || slot >= x.n_slots) return;
   int lo;
-  const int K = expert_rows(offsets, e, R, &lo);
-  const int m0 = blockIdx.x * kBM, n0 = blockIdx.y * kBN;
+  const int K = expert_rows(x, e, &lo);
   const floatx16 acc = tile_product_f32<true, true>(
       A + static_cast<int64_t>(lo) * M, M, [&](int o) { return m0 + o < M ? m0 + o : -1; },
       B + static_cast<int64_t>(lo) * N, N, [&](int o) { return n0 + o < N ? n0 + o : -1; }, K, lds);
@@ -324,6 +347,30 @@ __global__ __launch_bounds__(256) void weight_grad_f32_kernel(
     if (m0 + acc_row(q) < M) C[static_cast<int64_t>(m0 + acc_row(q)) * N + c] = acc[q];
 }
 
+__global__ __launch_bounds__(256) void grads_f32_kernel(
+    Experts ex, const float* __restrict__ x, const float* __restrict__ dy, const float* __restrict__ dgu,
+    const float* __restrict__ h, const char* __restrict__ wbase, int64_t expert_bytes, int H, int I,
+    Ranges ranges, float* __restrict__ dx, char* __restrict__ dw) {
+  __shared__ float lds[4 * kF32Lds];
+  const int nh = (H + kBN - 1) / kBN, ni = (I + kBN - 1) / kBN;
+  int64_t b = blockIdx.x;
+  if (b < ranges.dx) {
+    rows_product_f32(ex, static_cast<int>(b / nh), static_cast<int>(b % nh) * kBN, false, dgu,
+                     2 * static_cast<int64_t>(I), wbase, expert_bytes, 0, H, 2 * I, dx, lds);
+    return;
+  }
+  b -= ranges.dx;
+  if (b < ranges.dwgu) {
+    const int e = static_cast<int>(b / ranges.per_gu), at = static_cast<int>(b % ranges.per_gu);
+    weight_grad_f32(ex, e, at / nh * kBM, at % nh * kBN, dgu, 2 * I, x, H, expert_bytes, 0, dw, lds);
+    return;
+  }
+  b -= ranges.dwgu;
+  const int e = static_cast<int>(b / ranges.per_d), at = static_cast<int>(b % ranges.per_d);
+  weight_grad_f32(ex, e, at / ni * kBM, at % ni * kBN, dy, H, h, I, expert_bytes,
+                  2 * static_cast<int64_t>(H) * I * 4, dw, lds);
+}
+
 // ---------------------------------------------------------------------------
 // bf16
 // ---------------------------------------------------------------------------
@@ -332,49 +379,37 @@ __global__ __launch_bounds__(256) void weight_grad_f32_kernel(
 // so the workgroups that run together on an XCD share gm row panels and gn column panels in its L2.
 struct Order {
   int gm, gn, n_gn;  // tiles of a unit; units across
+  int blocks;        // a multiple of 8
 };
 
-__device__ __forceinline__ void place(const Order& o, int* m, int* n) {
-  const int xcd = blockIdx.x % 8, local = blockIdx.x / 8;
+__device__ __forceinline__ void place(const Order& o, int block, int* m, int* n) {
+  const int xcd = block % 8, local = block / 8;
   const int per = o.gm * o.gn;
   const int unit = local / per * 8 + xcd, at = local % per;
   *m = unit / o.n_gn * o.gm + at % o.gm;
   *n = unit % o.n_gn * o.gn + at / o.gm;
 }
 
-Order make_order(int64_t mt, int64_t nt, int64_t* grid) {
-  // up to 4 x 8 tiles (32 CUs an XCD), the columns cut evenly, where that leaves every XCD a few
-  // units, else single tiles
-  Order o{4, static_cast<int>(ceil_div64(nt, ceil_div64(nt, 8))), 0};
-  if (ceil_div64(mt, o.gm) * ceil_div64(nt, o.gn) < 32) o.gm = o.gn = 1;
-  o.n_gn = static_cast<int>(ceil_div64(nt, o.gn));
-  const int64_t units = ceil_div64(mt, o.gm) * o.n_gn;
-  *grid = ceil_div64(units, 8) * 8 * o.gm * o.gn;
-  return o;
-}
-
-__device__ __forceinline__ Tile load_tile(const Tile* tiles, int m) {
-  const Tile t = tiles[m];
-  return Tile{__builtin_amdgcn_readfirstlane(t.expert), __builtin_amdgcn_readfirstlane(t.row0),
-              __builtin_amdgcn_readfirstlane(t.rows), __builtin_amdgcn_readfirstlane(t.slot)};
-}
-
 // Calls f with the smallest tile mode that holds `rows` rows.
-template <typename F>
+template <int TR, typename F>
 __device__ __forceinline__ void by_rows(int rows, F f) {
-  if (rows > 192) f(std::integral_constant<int, 0>{});
-  else if (rows > 128) f(std::integral_constant<int, 6>{});
-  else if (rows > 64) f(std::integral_constant<int, 4>{});
-  else if (rows > 32) f(std::integral_constant<int, 2>{});
-  else f(std::integral_constant<int, 1>{});
+  if constexpr (TR == 256) {
+    if (rows > 192) f(std::integral_constant<int, 0>{});
+    else if (rows > 128) f(std::integral_constant<int, 6>{});
+    else if (rows > 64) f(std::integral_constant<int, 4>{});
+    else if (rows > 32) f(std::integral_constant<int, 2>{});
+    else f(std::integral_constant<int, 1>{});
+  } else {
+    f(std::integral_constant<int, 0>{});
+  }
 }
 
 // A tile's accumulators to C (its first row and column), of which rows x cols exist.
-template <int MI>
+template <int TR, int MI>
 __device__ __forceinline__ void store_tile(
-    const floatx16 (&acc)[TileShape<MI, false>::MW][TileShape<MI, false>::NJ], lds_char* smem,
+    const floatx16 (&acc)[TileShape<TR, MI, false>::MW][TileShape<TR, MI, false>::NJ], lds_char* smem,
     uint16_t* C, int64_t ld, int rows, int cols) {
-  using S = TileShape<MI, false>;
+  using S = TileShape<TR, MI, false>;
 #pragma unroll
   for (int i = 0; i < S::MW; ++i) {
     const int r0 = S::first_row() + i * 32, c0 = S::first_col();
@@ -384,14 +419,14 @@ __device__ __forceinline__ void store_tile(
   }
 }
 
-template <int MI>
+template <int TR, int MI>
 __device__ __forceinline__ void store_tile(
-    const floatx16 (&acc)[TileShape<MI, false>::MW][TileShape<MI, false>::NJ], lds_char*, float* C,
+    const floatx16 (&acc)[TileShape<TR, MI, false>::MW][TileShape<TR, MI, false>::NJ], lds_char*, float* C,
     int64_t ld, int rows, int cols) {
-  using S = TileShape<MI, false>;
+  using S = TileShape<TR, MI, false>;
 #pragma unroll
   for (int i = 0; i < S::MW; ++i) {
-    const int r = lane_row<MI, false>(i);
+    const int r = lane_row<TR, MI, false>(i);
     if (r >= rows) continue;
 #pragma unroll
     for (int j = 0; j < S::NJ; ++j)
@@ -405,51 +440,62 @@ __device__ __forceinline__ void store_tile(
   }
 }
 
-// C[r][n] = sum_k A[r][k] B[k][n] for the rows of each tile; B of the tile's expert starts at
-// b_off of its block.
-template <int MI, typename O>
-__device__ __forceinline__ void rows_product(const Tile& t, int n0, const uint16_t* A, int lda,
-                                             const uint16_t* B, int N, int K, O* C, lds_char* smem) {
-  using S = TileShape<MI, false>;
+// C[r][n] = sum_k A[r][k] B[k][n] for the rows of a tile and columns n0 .. n0 + TN - 1.
+template <int TR, int MI, typename O>
+__device__ __forceinline__ void rows_tile(const Tile& t, int n0, const uint16_t* A, int lda,
+                                          const uint16_t* B, int N, int K, O* C, lds_char* smem) {
+  using S = TileShape<TR, MI, false>;
   Operand<false, S::ROWS> oa;
-  Operand<true, 256> ob;
+  Operand<true, S::TN> ob;
   oa.init(A + static_cast<int64_t>(t.row0) * lda, lda, K, [&](int r) { return r < t.rows ? r : -1; });
   ob.init(B + n0, N, K, [&](int c) { return n0 + c < N ? c : -1; });
   floatx16 acc[S::MW][S::NJ];
-  tile_product<MI, false, false, true>(oa, ob, K, smem, acc);
-  store_tile<MI>(acc, smem, C + static_cast<int64_t>(t.row0) * N + n0, N, t.rows, N - n0);
+  tile_product<TR, MI, false, false, true>(oa, ob, K, smem, acc);
+  store_tile<TR, MI>(acc, smem, C + static_cast<int64_t>(t.row0) * N + n0, N, t.rows, N - n0);
 }
 
-template <typename O>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void rows_product_kernel(
-    const uint16_t* __restrict__ A, int lda, const char* __restrict__ wbase, int64_t expert_bytes,
-    int64_t b_off, int N, int K, const Tile* __restrict__ tiles, const int32_t* __restrict__ n_tiles,
-    Order order, O* __restrict__ C) {
-  extern __shared__ __attribute__((aligned(1024))) char smem[];
-  int m, n;
-  place(order, &m, &n);
-  if (m >= *n_tiles || n * kTileN >= N) return;
-  const Tile t = load_tile(tiles, m);
+// The same for tile (m, n) of the list; B of the tile's expert starts at b_off of its block.
+template <int TR, typename O>
+__device__ __forceinline__ void rows_product(const Experts& x, int m, int n, bool report,
+                                             const uint16_t* A, int lda, const char* wbase,
+                                             int64_t expert_bytes, int64_t b_off, int N, int K, O* C,
+                                             lds_char* smem) {
+  const int n0 = n * tile_columns(TR, false);
+  Tile t;
+  if (n0 >= N || !find_tile<TR>(x, m, report, &t)) return;
   const uint16_t* B = reinterpret_cast<const uint16_t*>(wbase + t.slot * expert_bytes + b_off);
-  by_rows(t.rows, [&](auto mi) {
-    rows_product<decltype(mi)::value>(t, n * kTileN, A, lda, B, N, K, C, (lds_char*)smem);
+  by_rows<TR>(t.rows, [&](auto mi) {
+    rows_tile<TR, decltype(mi)::value>(t, n0, A, lda, B, N, K, C, smem);
   });
 }
 
-// g and u for 128 columns, then dG, dU and h from dH.
-template <int MI>
-__device__ __forceinline__ void gate_up_backward(const Tile& t, int n0, const uint16_t* x,
-                                                 const uint16_t* W, int H, int I, const float* dh,
-                                                 uint16_t* dgu, uint16_t* h, lds_char* smem) {
-  using S = TileShape<MI, true>;
+#define TILE_KERNEL \
+  __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(TR == 256 ? 1 : 2, TR == 256 ? 1 : 2))) void
+
+template <int TR>
+TILE_KERNEL dh_kernel(Experts ex, const uint16_t* __restrict__ dy, const char* __restrict__ wbase,
+                      int64_t expert_bytes, int H, int I, Order order, float* __restrict__ dh) {
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  int m, n;
+  place(order, blockIdx.x, &m, &n);
+  rows_product<TR>(ex, m, n, m == 0 && n == 0, dy, H, wbase, expert_bytes,
+                   2 * static_cast<int64_t>(H) * I * 2, I, H, dh, (lds_char*)smem);
+}
+
+// g and u for half a tile's columns, then dG, dU and h from dH.
+template <int TR, int MI>
+__device__ __forceinline__ void gate_up_tile(const Tile& t, int n0, const uint16_t* x,
+                                             const uint16_t* W, int H, int I, const float* dh,
+                                             uint16_t* dgu, uint16_t* h, lds_char* smem) {
+  using S = TileShape<TR, MI, true>;
+  constexpr int HALF = S::NJ / 2, COLS = HALF * 32, OUT = S::TN / 2;
   Operand<false, S::ROWS> oa;
-  Operand<false, 256> ob;
+  Operand<false, S::TN> ob;
   oa.init(x + static_cast<int64_t>(t.row0) * H, H, H, [&](int r) { return r < t.rows ? r : -1; });
   ob.init(W + static_cast<int64_t>(n0) * H, H, H,
-          [&](int r) { return n0 + (r & 127) < I ? (r & 127) + (r >> 7) * I : -1; });
+          [&](int r) { return n0 + r % OUT < I ? r % OUT + r / OUT * I : -1; });
   floatx16 acc[S::MW][S::NJ];
-  tile_product<MI, true, false, false>(oa, ob, H, smem, acc);
-  constexpr int HALF = S::NJ / 2, COLS = HALF * 32;
+  tile_product<TR, MI, true, false, false>(oa, ob, H, smem, acc);
   const int c0 = n0 + S::first_col(), cols = I - c0;
   if (cols <= 0) return;
 #pragma unroll
@@ -458,7 +504,7 @@ __device__ __forceinline__ void gate_up_backward(const Tile& t, int n0, const ui
     if (rows <= 0) return;
     // dH of the lane's row, all of it in flight at once; a lane past the tile or past I reads a
     // place inside and its values are not stored
-    const float* drow = dh + static_cast<int64_t>(t.row0 + min(lane_row<MI, true>(i), t.rows - 1)) * I;
+    const float* drow = dh + static_cast<int64_t>(t.row0 + min(lane_row<TR, MI, true>(i), t.rows - 1)) * I;
     floatx4 d[HALF][4];
 #pragma unroll
     for (int j = 0; j < HALF; ++j)
@@ -482,167 +528,186 @@ __device__ __forceinline__ void gate_up_backward(const Tile& t, int n0, const ui
   }
 }
 
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void
-gate_up_backward_kernel(const uint16_t* __restrict__ x, const char* __restrict__ wbase,
-                        int64_t expert_bytes, int H, int I, const Tile* __restrict__ tiles,
-                        const int32_t* __restrict__ n_tiles, Order order, const float* __restrict__ dh,
-                        uint16_t* __restrict__ dgu, uint16_t* __restrict__ h) {
+template <int TR>
+TILE_KERNEL gate_up_kernel(Experts ex, const uint16_t* __restrict__ x, const char* __restrict__ wbase,
+                           int64_t expert_bytes, int H, int I, Order order, const float* __restrict__ dh,
+                           uint16_t* __restrict__ dgu, uint16_t* __restrict__ h) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   int m, n;
-  place(order, &m, &n);
-  if (m >= *n_tiles || n * (kTileN / 2) >= I) return;
-  const Tile t = load_tile(tiles, m);
+  place(order, blockIdx.x, &m, &n);
+  const int n0 = n * (tile_columns(TR, true) / 2);
+  Tile t;
+  if (n0 >= I || !find_tile<TR>(ex, m, false, &t)) return;
   const uint16_t* W = reinterpret_cast<const uint16_t*>(wbase + t.slot * expert_bytes);
-  by_rows(t.rows, [&](auto mi) {
-    gate_up_backward<decltype(mi)::value>(t, n * (kTileN / 2), x, W, H, I, dh, dgu, h, (lds_char*)smem);
+  by_rows<TR>(t.rows, [&](auto mi) {
+    gate_up_tile<TR, decltype(mi)::value>(t, n0, x, W, H, I, dh, dgu, h, (lds_char*)smem);
   });
 }
 
-// C[m][n] = sum over the expert's rows r of A[r][m] B[r][n], written at c_off of the expert's
-// block of dw.  An expert without rows gets zeros, one outside the buffer nothing.
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void weight_grad_kernel(
-    const uint16_t* __restrict__ A, int M, const uint16_t* __restrict__ B, int N,
-    const int32_t* __restrict__ offsets, int R, const int32_t* __restrict__ slot_of, int n_slots,
-    int64_t expert_bytes, int64_t c_off, Order order, char* __restrict__ dw) {
-  extern __shared__ __attribute__((aligned(1024))) char smem[];
-  using S = TileShape<0, false>;
-  int m, n;
-  place(order, &m, &n);
-  const int e = blockIdx.y;
-  const int m0 = m * kRowTile, n0 = n * kTileN;
+// C[m][n] = sum over expert e's rows r of A[r][m] B[r][n], written at c_off of the expert's block of
+// dw.  An expert without rows gets zeros, one outside the buffer nothing.
+template <int TR>
+__device__ __forceinline__ void weight_grad(const Experts& x, int e, int m, int n, const uint16_t* A, int M,
+                                            const uint16_t* B, int N, int64_t expert_bytes,
+                                            int64_t c_off, char* dw, lds_char* smem) {
+  using S = TileShape<TR, 0, false>;
+  const int m0 = m * TR, n0 = n * S::TN;
   if (m0 >= M || n0 >= N) return;
-  const int slot = __builtin_amdgcn_readfirstlane(slot_of[e]);
-  if (slot < 0 || slot >= n_slots) return;
+  const int slot = __builtin_amdgcn_readfirstlane(x.slot_of[e]);
+  if (slot < 0 || slot >= x.n_slots) return;
   int lo;
-  const int K = __builtin_amdgcn_readfirstlane(expert_rows(offsets, e, R, &lo));
+  const int K = __builtin_amdgcn_readfirstlane(expert_rows(x, e, &lo));
   lo = __builtin_amdgcn_readfirstlane(lo);
-  Operand<true, 256> oa, ob;
+  Operand<true, TR> oa;
+  Operand<true, S::TN> ob;
   oa.init(A + static_cast<int64_t>(lo) * M + m0, M, K, [&](int c) { return m0 + c < M ? c : -1; });
   ob.init(B + static_cast<int64_t>(lo) * N + n0, N, K, [&](int c) { return n0 + c < N ? c : -1; });
   floatx16 acc[S::MW][S::NJ];
-  tile_product<0, false, true, true>(oa, ob, K, (lds_char*)smem, acc);
+  tile_product<TR, 0, false, true, true>(oa, ob, K, smem, acc);
   uint16_t* C = reinterpret_cast<uint16_t*>(dw + slot * expert_bytes + c_off);
-  store_tile<0>(acc, (lds_char*)smem, C + static_cast<int64_t>(m0) * N + n0, N, M - m0, N - n0);
+  store_tile<TR, 0>(acc, smem, C + static_cast<int64_t>(m0) * N + n0, N, M - m0, N - n0);
+}
+
+struct GradsOrder {
+  Order dx, gu, d;  // of dX; of an expert's [dWg; dWu] and dWd
+};
+
+template <int TR>
+TILE_KERNEL grads_kernel(Experts ex, const uint16_t* __restrict__ x, const uint16_t* __restrict__ dy,
+                         const uint16_t* __restrict__ dgu, const uint16_t* __restrict__ h,
+                         const char* __restrict__ wbase, int64_t expert_bytes, int H, int I,
+                         Ranges ranges, GradsOrder order, uint16_t* __restrict__ dx,
+                         char* __restrict__ dw) {
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  lds_char* lds = (lds_char*)smem;
+  int m, n;
+  int64_t b = blockIdx.x;
+  if (b < ranges.dx) {
+    place(order.dx, static_cast<int>(b), &m, &n);
+    rows_product<TR>(ex, m, n, false, dgu, 2 * I, wbase, expert_bytes, 0, H, 2 * I, dx, lds);
+    return;
+  }
+  b -= ranges.dx;
+  const bool gu = b < ranges.dwgu;
+  if (!gu) b -= ranges.dwgu;
+  const int per = gu ? ranges.per_gu : ranges.per_d;
+  const int e = static_cast<int>(b / per);
+  place(gu ? order.gu : order.d, static_cast<int>(b % per), &m, &n);
+  weight_grad<TR>(ex, e, m, n, gu ? dgu : dy, gu ? 2 * I : H, gu ? x : h, gu ? H : I, expert_bytes,
+                  gu ? 0 : 2 * static_cast<int64_t>(H) * I * 2, dw, lds);
 }
 
 struct Call {
-  const int32_t* offsets;
-  int R, E, H, I;
-  const moe_wbuf* w;
+  Experts ex;
+  int H, I;
+  const char* wbase;
+  int64_t expert_bytes;
   char* ws;
   BackwardWs L;
   void* dx_perm;
   char* dw;
-  int32_t* status;
   hipStream_t s;
 };
 
-int launch_plan(const Call& c, moe_dtype dt, Tile** tiles, int32_t** n_tiles, int64_t* cap) {
-  *tiles = reinterpret_cast<Tile*>(c.ws + c.L.tiles_off);
-  *n_tiles = reinterpret_cast<int32_t*>(c.ws + c.L.count_off);
-  *cap = max_tiles(c.R, c.E, dt);
-  hipLaunchKernelGGL(backward_plan_kernel, dim3(1), dim3(MOE_MAX_E), 0, c.s, c.offsets, c.R, c.E,
-                     tile_rows(dt), c.w->slot_of, c.w->n_slots, static_cast<int>(*cap), *tiles, *n_tiles,
-                     c.status);
-  MOE_LAUNCH_CHECK("moe_grouped_swiglu_backward: plan");
-  return MOE_OK;
-}
-
 int run_f32(const Call& c, const float* x, const float* dy) {
-  const int E = c.E, H = c.H, I = c.I;
+  const int E = c.ex.E, H = c.H, I = c.I;
   float* dh = reinterpret_cast<float*>(c.ws + c.L.dh_off);
   float* dgu = reinterpret_cast<float*>(c.ws + c.L.dgu_off);
   float* h = reinterpret_cast<float*>(c.ws + c.L.h_off);
-  const char* wbase = static_cast<const char*>(c.w->base);
-  const int64_t eb = c.w->expert_bytes, HI = static_cast<int64_t>(H) * I * sizeof(float);
-  if (c.R > 0) {
-    Tile* tiles;
-    int32_t* n_tiles;
-    int64_t cap64;
-    const int rc = launch_plan(c, MOE_F32, &tiles, &n_tiles, &cap64);
-    if (rc) return rc;
-    const unsigned cap = static_cast<unsigned>(cap64);
-    hipLaunchKernelGGL(rows_product_f32_kernel, dim3(cap, ceil_div(I, kBN)), dim3(256), 0, c.s, dy,
-                       static_cast<int64_t>(H), wbase, eb, 2 * HI, I, H, tiles, n_tiles, dh);
+  const unsigned cap = static_cast<unsigned>(max_tiles(c.ex.R, E, kBM));
+  if (c.ex.R > 0) {
+    hipLaunchKernelGGL(dh_f32_kernel, dim3(cap, ceil_div(I, kBN)), dim3(256), 0, c.s, c.ex, dy, c.wbase,
+                       c.expert_bytes, H, I, dh);
     MOE_LAUNCH_CHECK("moe_grouped_swiglu_backward: dh");
-    hipLaunchKernelGGL(gate_up_backward_f32_kernel, dim3(cap, ceil_div(I, kBN / 2)), dim3(256), 0, c.s, x,
-                       wbase, eb, H, I, tiles, n_tiles, dh, dgu, h);
+    hipLaunchKernelGGL(gate_up_backward_f32_kernel, dim3(cap, ceil_div(I, kBN / 2)), dim3(256), 0, c.s,
+                       c.ex, x, c.wbase, c.expert_bytes, H, I, dh, dgu, h);
     MOE_LAUNCH_CHECK("moe_grouped_swiglu_backward: gate/up");
-    if (c.dx_perm) {
-      hipLaunchKernelGGL(rows_product_f32_kernel, dim3(cap, ceil_div(H, kBN)), dim3(256), 0, c.s, dgu,
-                         2 * static_cast<int64_t>(I), wbase, eb, int64_t{0}, H, 2 * I, tiles, n_tiles,
-                         static_cast<float*>(c.dx_perm));
-      MOE_LAUNCH_CHECK("moe_grouped_swiglu_backward: dx");
-    }
   }
-  if (c.dw) {
-    hipLaunchKernelGGL(weight_grad_f32_kernel, dim3(ceil_div(2 * I, kBM), ceil_div(H, kBN), E), dim3(256),
-                       0, c.s, dgu, 2 * I, x, H, c.offsets, c.R, c.w->slot_of, c.w->n_slots, eb,
-                       int64_t{0}, c.dw);
-    MOE_LAUNCH_CHECK("moe_grouped_swiglu_backward: gate/up weights");
-    hipLaunchKernelGGL(weight_grad_f32_kernel, dim3(ceil_div(H, kBM), ceil_div(I, kBN), E), dim3(256), 0,
-                       c.s, dy, H, h, I, c.offsets, c.R, c.w->slot_of, c.w->n_slots, eb, 2 * HI, c.dw);
-    MOE_LAUNCH_CHECK("moe_grouped_swiglu_backward: down weights");
-  }
+  Ranges r;
+  r.dx = c.dx_perm ? static_cast<int64_t>(cap) * ceil_div(H, kBN) : 0;
+  r.per_gu = ceil_div(2 * I, kBM) * ceil_div(H, kBN);
+  r.per_d = ceil_div(H, kBM) * ceil_div(I, kBN);
+  r.dwgu = c.dw ? static_cast<int64_t>(E) * r.per_gu : 0;
+  const int64_t blocks = r.dx + r.dwgu + (c.dw ? static_cast<int64_t>(E) * r.per_d : 0);
+  if (blocks > INT32_MAX)
+    return fail(MOE_ERR_UNSUPPORTED, "moe_grouped_swiglu_backward: %lld blocks", static_cast<long long>(blocks));
+  if (blocks == 0) return MOE_OK;
+  hipLaunchKernelGGL(grads_f32_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, c.s, c.ex, x, dy,
+                     dgu, h, c.wbase, c.expert_bytes, H, I, r, static_cast<float*>(c.dx_perm), c.dw);
+  MOE_LAUNCH_CHECK("moe_grouped_swiglu_backward: gradients");
   return MOE_OK;
 }
 
-// Enqueue a tile kernel: its 128 KB of LDS are above the default limit of a launch.
+Order make_order(int tr, int64_t mt, int64_t nt, int64_t* blocks) {
+  // large tiles: up to 4 x 8 (32 CUs an XCD), the columns cut evenly, where that leaves every XCD a
+  // few units, else single tiles
+  Order o{4, static_cast<int>(ceil_div64(nt, ceil_div64(nt, 8))), 0, 0};
+  if (tr != 256 || ceil_div64(mt, o.gm) * ceil_div64(nt, o.gn) < 32) o.gm = o.gn = 1;
+  o.n_gn = static_cast<int>(ceil_div64(nt, o.gn));
+  const int64_t units = ceil_div64(mt, o.gm) * o.n_gn;
+  *blocks = ceil_div64(units, 8) * 8 * o.gm * o.gn;
+  o.blocks = static_cast<int>(*blocks);
+  return o;
+}
+
+// Large tiles when dH and dX together have one for every CU, else small ones, of which there are 16
+// times as many.  Measured, large against small: 954 tokens x 3 of 3 experts, 840 x 120 (75 large
+// tiles) 91 / 46 us; 239 x 3 of 42, 88 x 120 (90) 34 / 17 us; 136 x 3 of 20, 3984 x 72 (357) 95 / 96 us;
+// 1623 x 7 of 16, 984 x 616 (427) 234 / 390 us; 18 x 8 of 42, 1848 x 1296 (602) 416 / 573 us.
+bool large_tiles(int R, int E, int H, int I) {
+  return max_tiles(R, E, 256) * (ceil_div(H, 256) + ceil_div(I, 256)) >= 256;
+}
+
+// Enqueue a tile kernel: its LDS is above the default limit of a launch.
 template <typename K, typename... A>
-int launch_tiles(const char* what, K kernel, dim3 grid, hipStream_t s, A... args) {
+int launch_tiles(const char* what, K kernel, int64_t blocks, int lds, hipStream_t s, A... args) {
+  if (blocks > INT32_MAX)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: %lld blocks", what, static_cast<long long>(blocks));
   MOE_HIP_CHECK(hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                    hipFuncAttributeMaxDynamicSharedMemorySize, kTileLds));
-  hipLaunchKernelGGL(kernel, grid, dim3(256), kTileLds, s, args...);
+                                    hipFuncAttributeMaxDynamicSharedMemorySize, lds));
+  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), lds, s, args...);
   MOE_LAUNCH_CHECK(what);
   return MOE_OK;
 }
 
+template <int TR>
 int run_bf16(const Call& c, const uint16_t* x, const uint16_t* dy) {
-  const int H = c.H, I = c.I;
+  const int E = c.ex.E, H = c.H, I = c.I;
+  constexpr int TN = tile_columns(TR, false);
   float* dh = reinterpret_cast<float*>(c.ws + c.L.dh_off);
   uint16_t* dgu = reinterpret_cast<uint16_t*>(c.ws + c.L.dgu_off);
   uint16_t* h = reinterpret_cast<uint16_t*>(c.ws + c.L.h_off);
-  const char* wbase = static_cast<const char*>(c.w->base);
-  const int64_t eb = c.w->expert_bytes, HI = static_cast<int64_t>(H) * I * 2;
-  int64_t grid;
-  int rc;
-  if (c.R > 0) {
-    Tile* tiles;
-    int32_t* n_tiles;
-    int64_t cap;
-    rc = launch_plan(c, MOE_BF16, &tiles, &n_tiles, &cap);
+  const int64_t cap = max_tiles(c.ex.R, E, TR);
+  int64_t n;
+  if (c.ex.R > 0) {
+    Order o = make_order(TR, cap, ceil_div(I, TN), &n);
+    int rc = launch_tiles("moe_grouped_swiglu_backward: dh", dh_kernel<TR>, n, tile_lds(TR, false), c.s,
+                          c.ex, dy, c.wbase, c.expert_bytes, H, I, o, dh);
     if (rc) return rc;
-    Order o = make_order(cap, ceil_div(I, kTileN), &grid);
-    rc = launch_tiles("moe_grouped_swiglu_backward: dh", rows_product_kernel<float>,
-                      dim3(static_cast<unsigned>(grid)), c.s, dy, H, wbase, eb, 2 * HI, I, H, tiles,
-                      n_tiles, o, dh);
+    o = make_order(TR, cap, ceil_div(I, tile_columns(TR, true) / 2), &n);
+    rc = launch_tiles("moe_grouped_swiglu_backward: gate/up", gate_up_kernel<TR>, n, tile_lds(TR, true),
+                      c.s, c.ex, x, c.wbase, c.expert_bytes, H, I, o, dh, dgu, h);
     if (rc) return rc;
-    o = make_order(cap, ceil_div(I, kTileN / 2), &grid);
-    rc = launch_tiles("moe_grouped_swiglu_backward: gate/up", gate_up_backward_kernel,
-                      dim3(static_cast<unsigned>(grid)), c.s, x, wbase, eb, H, I, tiles, n_tiles, o, dh,
-                      dgu, h);
-    if (rc) return rc;
-    if (c.dx_perm) {
-      o = make_order(cap, ceil_div(H, kTileN), &grid);
-      rc = launch_tiles("moe_grouped_swiglu_backward: dx", rows_product_kernel<uint16_t>,
-                        dim3(static_cast<unsigned>(grid)), c.s, dgu, 2 * I, wbase, eb, int64_t{0}, H,
-                        2 * I, tiles, n_tiles, o, static_cast<uint16_t*>(c.dx_perm));
-      if (rc) return rc;
-    }
+  }
+  GradsOrder o{};
+  Ranges r{0, 0, 1, 1};
+  int64_t blocks = 0;
+  if (c.dx_perm && c.ex.R > 0) {
+    o.dx = make_order(TR, cap, ceil_div(H, TN), &n);
+    blocks = r.dx = n;
   }
   if (c.dw) {
-    Order o = make_order(ceil_div(2 * I, kRowTile), ceil_div(H, kTileN), &grid);
-    rc = launch_tiles("moe_grouped_swiglu_backward: gate/up weights", weight_grad_kernel,
-                      dim3(static_cast<unsigned>(grid), c.E), c.s, dgu, 2 * I, x, H, c.offsets, c.R,
-                      c.w->slot_of, c.w->n_slots, eb, int64_t{0}, o, c.dw);
-    if (rc) return rc;
-    o = make_order(ceil_div(H, kRowTile), ceil_div(I, kTileN), &grid);
-    rc = launch_tiles("moe_grouped_swiglu_backward: down weights", weight_grad_kernel,
-                      dim3(static_cast<unsigned>(grid), c.E), c.s, dy, H, h, I, c.offsets, c.R,
-                      c.w->slot_of, c.w->n_slots, eb, 2 * HI, o, c.dw);
-    if (rc) return rc;
+    o.gu = make_order(TR, ceil_div(2 * I, TR), ceil_div(H, TN), &n);
+    r.per_gu = static_cast<int>(n);
+    o.d = make_order(TR, ceil_div(H, TR), ceil_div(I, TN), &n);
+    r.per_d = static_cast<int>(n);
+    r.dwgu = static_cast<int64_t>(E) * r.per_gu;
+    blocks += r.dwgu + static_cast<int64_t>(E) * r.per_d;
   }
-  return MOE_OK;
+  if (blocks == 0) return MOE_OK;
+  return launch_tiles("moe_grouped_swiglu_backward: gradients", grads_kernel<TR>, blocks,
+                      tile_lds(TR, false), c.s, c.ex, x, dy, dgu, h, c.wbase, c.expert_bytes, H, I, r, o,
+                      static_cast<uint16_t*>(c.dx_perm), c.dw);
 }
 
 }  // namespace
@@ -653,7 +718,7 @@ extern "C" int moe_grouped_swiglu_backward_workspace_size(int R, int E, int H, i
   using namespace moe;
   if (!bytes || R < 0 || E < 1 || H < 1 || I < 1 || (dtype != MOE_F32 && dtype != MOE_BF16))
     return fail(MOE_ERR_ARG, "moe_grouped_swiglu_backward_workspace_size: bad arguments");
-  *bytes = backward_ws(R, E, I, dtype).total;
+  *bytes = backward_ws(R, I, dtype).total;
   return MOE_OK;
 }
 
@@ -683,14 +748,21 @@ extern "C" int moe_grouped_swiglu_backward(const void* x_perm, const void* dy_pe
   if (all % (dtype == MOE_BF16 ? 16 : 4) != 0)
     return fail(MOE_ERR_UNSUPPORTED, "%s: a pointer is not aligned to %d bytes", who,
                 dtype == MOE_BF16 ? 16 : 4);
-  const BackwardWs L = backward_ws(R, E, I, dtype);
+  const BackwardWs L = backward_ws(R, I, dtype);
   if (!ws || ws_bytes < L.total)
     return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", who, ws_bytes, L.total);
   if (R > 0 && (!x_perm || !dy_perm)) return fail(MOE_ERR_ARG, "%s: null pointer", who);
   hipStream_t s = as_stream(stream);
-  const Call c{offsets, R, E, H, I, w, static_cast<char*>(ws), L, dx_perm, static_cast<char*>(dw), status, s};
-  const int rc = dtype == MOE_F32
-                     ? run_f32(c, static_cast<const float*>(x_perm), static_cast<const float*>(dy_perm))
-                     : run_bf16(c, static_cast<const uint16_t*>(x_perm), static_cast<const uint16_t*>(dy_perm));
+  const Call c{Experts{offsets, w->slot_of, R, E, w->n_slots, status}, H, I,
+               static_cast<const char*>(w->base), eb, static_cast<char*>(ws), L, dx_perm,
+               static_cast<char*>(dw), s};
+  int rc;
+  if (dtype == MOE_F32) {
+    rc = run_f32(c, static_cast<const float*>(x_perm), static_cast<const float*>(dy_perm));
+  } else {
+    const uint16_t* x = static_cast<const uint16_t*>(x_perm);
+    const uint16_t* dy = static_cast<const uint16_t*>(dy_perm);
+    rc = large_tiles(R, E, H, I) ? run_bf16<256>(c, x, dy) : run_bf16<64>(c, x, dy);
+  }
   return debug_check(rc, who, s, status);
 }
