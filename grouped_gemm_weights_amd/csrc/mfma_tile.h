@@ -357,8 +357,10 @@ __device__ __forceinline__ int lane_col(int v) {
 
 // 32 rows x COLS columns of bf16 from this wave's accumulators to memory.  put(j, v) gives the
 // four values of column block j, elements 4 v .. 4 v + 3, as packed bf16.  The LDS rows are padded
-// by 16 bytes, which spreads the 16 rows of a write over all banks.  out: the block's first row
-// and column; rows, cols: how many exist (cols a multiple of 8).
+// by 16 bytes, which spreads the 16 rows of a write over all banks.  The stores are non-temporal: a
+// round of tiles writes as much as all of L2 holds, and would push out the panels that the next
+// reads (weight gradients of 384 rows an expert: 450 -> 420 us).  out: the block's first row and
+// column; rows, cols: how many exist (cols a multiple of 8).
 template <int COLS, typename Put>
 __device__ __forceinline__ void store_block(lds_char* smem, uint16_t* out, int64_t ld, int rows,
                                             int cols, Put put) {
@@ -381,7 +383,7 @@ __device__ __forceinline__ void store_block(lds_char* smem, uint16_t* out, int64
   for (int i = 0; i < 32 / PER; ++i) {
     const int r = i * PER + lane / LANES;
     const u32x4 d = *reinterpret_cast<lds_u32x4*>(mine + r * PITCH + c * 2);
-    if (r < rows && c < cols) *reinterpret_cast<u32x4*>(out + r * ld + c) = d;
+    if (r < rows && c < cols) __builtin_nontemporal_store(d, reinterpret_cast<u32x4*>(out + r * ld + c));
   }
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
   __builtin_amdgcn_wave_barrier();
