@@ -42,7 +42,8 @@ def test_layer_norm_backward(B):
     A, U, W = B.MOE_ERR_ARG, B.MOE_ERR_UNSUPPORTED, B.MOE_ERR_WORKSPACE
     f = B.moe_layer_norm_backward
     need = B.moe_layer_norm_backward_workspace_size(4, 100)
-    assert need >= 4 * 2 * 100 * 4 and B.moe_layer_norm_backward_workspace_size(0, 100) == 0
+    # one partial row of dgamma and dbeta per workgroup, and at least one workgroup
+    assert need >= 2 * 100 * 4 and B.moe_layer_norm_backward_workspace_size(0, 100) == 0
     # T and H far past any partial count: the workspace stays bounded
     assert B.moe_layer_norm_backward_workspace_size(1 << 30, 64) <= 4096 * 2 * 64 * 4
     ok = (P, P, P, P, P, 4, 100, B.MOE_F32, P, P, P, P, need)
