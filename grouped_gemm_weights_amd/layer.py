@@ -88,8 +88,7 @@ class MoELayer:
         self.x = torch.empty((T, H), dtype=tdt, device=d)
         f32 = dict(dtype=torch.float32, device=d)
         self.pre_norm, self.eps, self.training = pre_norm, eps, training
-        # what the router and the experts see: x, or its norm
-        self.xn = torch.empty_like(self.x) if pre_norm else self.x
+        self._xn = torch.empty_like(self.x) if pre_norm else None
         if pre_norm:
             self.gamma, self.beta = torch.ones((H,), **f32), torch.zeros((H,), **f32)
             self.mean, self.rstd = torch.empty((T,), **f32), torch.empty((T,), **f32)
@@ -197,6 +196,12 @@ class MoELayer:
         """The pool block of expert e (device or host tensor view)."""
         n_local = self.cfg.n_local
         return self._local_t[e] if e < n_local else self._remote_t[e - n_local]
+
+    @property
+    def xn(self) -> torch.Tensor:
+        """What the router and the experts see: the norm of x, or, without pre_norm, whatever x is
+        at the time (a caller may put another tensor in its place)."""
+        return self._xn if self.pre_norm else self.x
 
     # ------------------------------------------------------------------ steps
     def norm(self) -> None:

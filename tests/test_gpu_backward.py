@@ -632,6 +632,28 @@ def test_layer_router_reads_the_normed_rows():
         L.close()
 
 
+@pytest.mark.parametrize("fused_gather", [False, True])
+def test_layer_reads_the_x_that_is_there(fused_gather):
+    """Without pre_norm the step reads the layer's x at the time of the step, also another tensor
+    that a caller has put in its place."""
+    cfg = synth.MoEConfig("other_x", T=50, H=64, I=32, E=8, k=2, dtype="bf16", n_local=4, seed=3)
+    L = build_layer(cfg, fused_gather=fused_gather)
+    try:
+        L.forward(remote="all")
+        L.synchronize()
+        y = L.y.clone()
+        other = L.x.clone()
+        L.x.zero_()
+        L.x = other
+        L.y.fill_(float("nan"))
+        torch.cuda.synchronize()
+        L.forward(remote="all")
+        L.synchronize()
+        assert torch.equal(L.y, y)
+    finally:
+        L.close()
+
+
 def test_layer_training_refusals():
     cfg, L, dy = layer_case("bf16", False)
     try:
