@@ -190,8 +190,8 @@ extern "C" int moe_combine_backward(const void* dy, moe_dtype dy_dtype, const fl
     return fail(MOE_ERR_ARG, "moe_combine_backward: bad sizes T=%d k=%d H=%d or dtype", T, k, H);
   if (k > MOE_MAX_K)
     return fail(MOE_ERR_UNSUPPORTED, "moe_combine_backward: k=%d above %d", k, MOE_MAX_K);
-  if (static_cast<int64_t>(T) * k > INT32_MAX || H > kMaxRow)
-    return fail(MOE_ERR_UNSUPPORTED, "moe_combine_backward: T*k or H=%d too large", H);
+  if (static_cast<int64_t>(T) * k > INT32_MAX || H > kMaxRow || too_many(T, 256))
+    return fail(MOE_ERR_UNSUPPORTED, "moe_combine_backward: T=%d, T*k or H=%d too large", T, H);
   if (T == 0) return MOE_OK;
   if (!dy || !row_of || !topk_w || !dy_perm || (dtopk_w && !y_perm))
     return fail(MOE_ERR_ARG, "moe_combine_backward: null pointer");

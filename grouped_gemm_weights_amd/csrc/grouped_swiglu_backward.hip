@@ -21,6 +21,7 @@
 #include <type_traits>
 
 #include "mfma_tile.h"
+#include "rows.h"
 
 namespace moe {
 namespace {
@@ -629,8 +630,6 @@ int run_f32(const Call& c, const float* x, const float* dy) {
   r.per_d = ceil_div(H, kBM) * ceil_div(I, kBN);
   r.dwgu = c.dw ? static_cast<int64_t>(E) * r.per_gu : 0;
   const int64_t blocks = r.dx + r.dwgu + (c.dw ? static_cast<int64_t>(E) * r.per_d : 0);
-  if (blocks > INT32_MAX)
-    return fail(MOE_ERR_UNSUPPORTED, "moe_grouped_swiglu_backward: %lld blocks", static_cast<long long>(blocks));
   if (blocks == 0) return MOE_OK;
   hipLaunchKernelGGL(grads_f32_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, c.s, c.ex, x, dy,
                      dgu, h, c.wbase, c.expert_bytes, H, I, r, static_cast<float*>(c.dx_perm), c.dw);
@@ -661,8 +660,6 @@ bool large_tiles(int R, int E, int H, int I) {
 // Enqueue a tile kernel: its LDS is above the default limit of a launch.
 template <typename K, typename... A>
 int launch_tiles(const char* what, K kernel, int64_t blocks, int lds, hipStream_t s, A... args) {
-  if (blocks > INT32_MAX)
-    return fail(MOE_ERR_UNSUPPORTED, "%s: %lld blocks", what, static_cast<long long>(blocks));
   MOE_HIP_CHECK(hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                     hipFuncAttributeMaxDynamicSharedMemorySize, lds));
   hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), lds, s, args...);
@@ -742,6 +739,10 @@ extern "C" int moe_grouped_swiglu_backward(const void* x_perm, const void* dy_pe
     return fail(MOE_ERR_UNSUPPORTED, "%s: H=%d or I=%d above %d, or H*I 2^29 or more", who, H, I, kMaxSide);
   if (dtype == MOE_BF16 && (H % 8 != 0 || I % 8 != 0))
     return fail(MOE_ERR_UNSUPPORTED, "%s: H=%d and I=%d must be multiples of 8", who, H, I);
+  // the largest launch: small tiles of dX and of every expert's weight gradients
+  const int64_t nh = ceil_div(H, 64), ni = ceil_div(I, 64);
+  if (too_many((max_tiles(R, E, 64) + 8) * std::max(nh, 2 * ni) + E * (3 * nh * ni + 24), 256))
+    return fail(MOE_ERR_UNSUPPORTED, "%s: R=%d rows of H=%d, I=%d are more than a launch takes", who, R, H, I);
   const uintptr_t all = reinterpret_cast<uintptr_t>(x_perm) | reinterpret_cast<uintptr_t>(dy_perm) |
                         reinterpret_cast<uintptr_t>(w->base) | reinterpret_cast<uintptr_t>(dx_perm) |
                         reinterpret_cast<uintptr_t>(dw) | reinterpret_cast<uintptr_t>(ws);

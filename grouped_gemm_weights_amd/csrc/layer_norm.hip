@@ -470,7 +470,8 @@ extern "C" int moe_layer_norm(const void* x, const float* gamma, const float* be
   using namespace moe;
   if (T < 0 || H < 1 || !(eps >= 0.f) || (dtype != MOE_F32 && dtype != MOE_BF16))
     return fail(MOE_ERR_ARG, "moe_layer_norm: bad sizes T=%d H=%d, eps or dtype", T, H);
-  if (H > kMaxRow) return fail(MOE_ERR_UNSUPPORTED, "moe_layer_norm: H=%d above %d", H, kMaxRow);
+  if (H > kMaxRow || (H > kMaxH && too_many(T, 1024)))
+    return fail(MOE_ERR_UNSUPPORTED, "moe_layer_norm: H=%d above %d, or T=%d too large for it", H, kMaxRow, T);
   if (T == 0) return MOE_OK;
   if (!x || !gamma || !y) return fail(MOE_ERR_ARG, "moe_layer_norm: null pointer");
   hipStream_t s = as_stream(stream);
@@ -494,8 +495,9 @@ extern "C" int moe_layer_norm_backward(const void* dy, const void* x, const floa
   using namespace moe;
   if (T < 0 || H < 1 || (dtype != MOE_F32 && dtype != MOE_BF16))
     return fail(MOE_ERR_ARG, "moe_layer_norm_backward: bad sizes T=%d H=%d or dtype", T, H);
-  if (H > kMaxRow)
-    return fail(MOE_ERR_UNSUPPORTED, "moe_layer_norm_backward: H=%d above %d", H, kMaxRow);
+  if (H > kMaxRow || (H > kMaxBackwardH && too_many(T, 1024)))
+    return fail(MOE_ERR_UNSUPPORTED, "moe_layer_norm_backward: H=%d above %d, or T=%d too large for it", H,
+                kMaxRow, T);
   const bool sums = dgamma || dbeta;
   if (T > 0 && (!dy || !x || !gamma || !mean || !rstd || !dx))
     return fail(MOE_ERR_ARG, "moe_layer_norm_backward: null pointer");

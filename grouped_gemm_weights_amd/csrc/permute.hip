@@ -401,9 +401,6 @@ extern "C" int moe_permute_backward(const void* dx_perm, const int32_t* row_of, 
     return fail(MOE_ERR_ARG, "moe_permute_backward: bad sizes T=%d k=%d H=%d or dtype", T, k, H);
   if (static_cast<int64_t>(T) * k > INT32_MAX || H > kMaxRow)
     return fail(MOE_ERR_UNSUPPORTED, "moe_permute_backward: T=%d k=%d H=%d too large", T, k, H);
-  if (T == 0) return MOE_OK;
-  if (!dx_perm || !row_of || !dx) return fail(MOE_ERR_ARG, "moe_permute_backward: null pointer");
-  hipStream_t s = as_stream(stream);
   const int pieces = ceil_div(H, kVec);
   const bool tail = H % kVec != 0;
   // short rows: 256 threads hold several tokens; long ones: the row's waves in blocks of up to 8
@@ -411,6 +408,11 @@ extern "C" int moe_permute_backward(const void* dx_perm, const int32_t* row_of, 
   const int waves = ceil_div(pieces, kWave), across = ceil_div(waves, 8);
   const dim3 grid(ceil_div(T, tokens), tokens > 1 ? 1 : across);
   const dim3 block(tokens > 1 ? 256 : ceil_div(waves, across) * kWave);
+  if (too_many(grid.x, block.x))
+    return fail(MOE_ERR_UNSUPPORTED, "moe_permute_backward: T=%d too large at H=%d", T, H);
+  if (T == 0) return MOE_OK;
+  if (!dx_perm || !row_of || !dx) return fail(MOE_ERR_ARG, "moe_permute_backward: null pointer");
+  hipStream_t s = as_stream(stream);
   if (dtype == MOE_F32) {
     auto kernel = tail ? permute_backward_kernel<float, true> : permute_backward_kernel<float, false>;
     hipLaunchKernelGGL(kernel, grid, block, 0, s, static_cast<const float*>(dx_perm), row_of, T, k, H,

@@ -182,6 +182,8 @@ extern "C" int moe_route_backward(const int32_t* topk_idx, const float* topk_w, 
     return fail(MOE_ERR_ARG, "moe_route_backward: bad sizes T=%d E=%d k=%d", T, E, k);
   if (E > MOE_MAX_E || k > MOE_MAX_K)
     return fail(MOE_ERR_UNSUPPORTED, "moe_route_backward: E=%d or k=%d above the limits", E, k);
+  if (too_many(ceil_div(T, kRouteWaves), kRouteWaves * kWave))
+    return fail(MOE_ERR_UNSUPPORTED, "moe_route_backward: T=%d too large", T);
   if (T == 0) return MOE_OK;
   if (!topk_idx || !topk_w || !dtopk_w || !dlogits)
     return fail(MOE_ERR_ARG, "moe_route_backward: null pointer");

@@ -7,6 +7,9 @@
 
 namespace moe {
 
+// Whether a grid of `blocks` workgroups of `threads` is more than one launch takes (2^32 threads).
+inline bool too_many(int64_t blocks, int threads) { return blocks * threads > UINT32_MAX; }
+
 // Rows start at any element (H need not be a multiple of anything), so the vector types claim
 // the alignment of one element only.  gfx950 loads and stores 16 bytes at any such address in
 // one instruction.

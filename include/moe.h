@@ -368,7 +368,8 @@ int moe_combine(const float* y_perm, const int32_t* row_of, const float* topk_w,
  * rstd).  Sums and statistics are f32; outputs are rounded once.  No call uses atomics on its
  * outputs: the same inputs give the same bits.  dtype is that of x, x_perm and the weights.
  * Every call may be captured into a HIP graph; captured calls that may run at the same time
- * need workspaces of their own.  Outputs must not alias inputs.
+ * need workspaces of their own.  Outputs must not alias inputs.  Sizes whose launch would pass
+ * 2^32 threads (more than about 8 million tokens or rows) are MOE_ERR_UNSUPPORTED.
  */
 
 /*
@@ -462,8 +463,8 @@ int moe_grouped_swiglu_backward_workspace_size(int R, int E, int H, int I, moe_d
  *   dx_perm device [R][H] dtype; may be NULL (only the weights are trained)
  *   dw      device, n_slots expert blocks laid out as w's: the gradient of the expert in slot s
  *           is written (not added) at dw + s * expert_bytes, zeros for an expert without rows;
- *           blocks of slots that no expert maps to keep what they held.  May be NULL (frozen
- *           experts).  Not both dx_perm and dw NULL.
+ *           blocks of slots that no expert maps to keep what they held.  No two experts may
+ *           share a slot.  May be NULL (frozen experts).  Not both dx_perm and dw NULL.
  *   status  device i32, may be NULL (MOE_STATUS_EXPERT_ABSENT when an expert with rows has no
  *           slot in [0, n_slots): its rows of dx_perm are left unwritten)
  * Rows of dx_perm at or past offsets[E] are left as they were.  With R = 0 only dw is written.

@@ -33,7 +33,8 @@ def test_layer_norm(B):
             (A, (P, P, P, 2, 8, -1e-5, B.MOE_F32, P)), (A, (P, P, P, 2, 8, float("nan"), B.MOE_F32, P)),
             (A, (P, P, P, 2, 8, 1e-5, 7, P)), (A, (None, P, P, 2, 8, 1e-5, B.MOE_F32, P)),
             (A, (P, None, P, 2, 8, 1e-5, B.MOE_F32, P)), (A, (P, P, P, 2, 8, 1e-5, B.MOE_F32, None)),
-            (U, (P, P, P, 2, (1 << 28) + 1, 1e-5, B.MOE_F32, P))]:
+            (U, (P, P, P, 2, (1 << 28) + 1, 1e-5, B.MOE_F32, P)),
+            (U, (P, P, P, 1 << 23, 1 << 16, 1e-5, B.MOE_F32, P))]:      # 2^33 threads
         refused(B, code, f, *args)
     f(None, None, None, 0, 8, 1e-5, B.MOE_BF16, None)      # no rows: nothing to do
 
@@ -78,6 +79,7 @@ def test_combine_and_permute_backward(B):
     refused(B, U, f, *but(6, 65))
     refused(B, U, f, *but(5, 1 << 30))
     refused(B, U, f, *but(7, (1 << 28) + 1))
+    refused(B, U, f, *but(5, 1 << 25))                                  # 2^33 threads
     f(*but(5, 0))
     g = B.moe_permute_backward
     ok = (P, P, 4, 2, 8, B.MOE_BF16, P)
@@ -87,6 +89,7 @@ def test_combine_and_permute_backward(B):
         refused(B, A, g, *but(at, value))
     refused(B, U, g, *but(2, 1 << 30))
     refused(B, U, g, *but(4, (1 << 28) + 1))
+    refused(B, U, g, P, P, 1 << 25, 2, 4096, B.MOE_BF16, P)             # 2^34 threads
     g(*but(2, 0))
 
 
@@ -104,6 +107,7 @@ def test_route_backward(B):
         refused(B, A, f, *but(at, value))
     refused(B, U, f, *but(4, 1025))
     refused(B, U, f, P, P, P, 4, 128, 65, P)
+    refused(B, U, f, *but(3, 1 << 27))                                  # 2^33 threads
     f(*but(3, 0))
 
 
@@ -139,6 +143,7 @@ def test_grouped_swiglu_backward(B):
     refused(B, U, f, *but((5, side), (6, side), (8, B.wbuf(P, 6 * side * side, 4, E, P))))
     side = (1 << 20) + 8
     refused(B, U, f, *but((5, side), (8, B.wbuf(P, 6 * side * I, 4, E, P))))
+    refused(B, U, f, *but((3, 1 << 30), (10, 1 << 62)))                 # more than 2^32 threads
     for at in (0, 1, 9, 11, 12):
         refused(B, U, f, *but((at, P + 8)))                             # alignment
     refused(B, W, f, *but((10, need - 1)))
