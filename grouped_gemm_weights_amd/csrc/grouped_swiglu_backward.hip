@@ -130,74 +130,65 @@ __device__ __forceinline__ void swiglu_grad(float g, float u, float d, float* dg
 // latency.  A stage is 32 of depth; the next two stages' loads are in flight while this one's
 // MFMAs run, LDS is double-buffered and an even and an odd accumulator keep two MFMAs independent.
 
-typedef float f32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
-
-// This thread's 8 elements of a stage of an operand: 64 "outer" indices by 32 of depth, zero outside
-// the operand.  KMAJOR: element (o, k) is at p[k * ld + o], else at p[o * ld + k]; either way four
-// elements that lie together in memory are one load where all four exist.  Two pieces alternate,
-// each a stage ahead of the other.  at(o) maps a tile's outer index to the operand's, or to -1;
-// four from a multiple of 4 stay together (KMAJOR).
+// How the stages of an operand are loaded: 64 "outer" indices by 32 of depth, 8 elements a thread,
+// each load of a wave one or two runs that lie together in memory.  A lane outside the operand has
+// an offset past the buffer's range, for which the hardware returns zero: no load is behind a
+// branch, so none has to arrive before the branch ends.  KMAJOR: element (o, k) is at
+// p[k * ld + o], else at p[o * ld + k].
 template <bool KMAJOR>
-struct Piece {
-  const float* p[2];  // this thread's elements of the stage to load next
-  int n[2];           // how many of the four exist (KMAJOR: columns; else 4 or 0)
-  int64_t step;       // two stages on
-  int k;              // depth of the first of them within the operand
-  float v[2][4];
+struct OperandF32 {
+  uint64_t base;     // wave-uniform: where the stage to load next starts
+  uint32_t step;     // bytes from a stage to the next
+  int left;          // steps of depth from there on
+  int k;             // depth of this thread's element 0 within a stage
+  uint32_t voff[8];  // kOutside for what does not exist
 
+  // at(o) maps a tile's outer index to the operand's, or to -1
   template <typename At>
-  __device__ __forceinline__ void init(const float* base, int64_t ld, int k0, At at) {
+  __device__ __forceinline__ void init(const float* p, int64_t ld, int K, At at) {
     const int tid = threadIdx.x;
-    k = k0 + (KMAJOR ? tid >> 4 : (tid & 7) * 4);
-    step = 2 * kBK * (KMAJOR ? ld : 1);
+    const uint64_t u = reinterpret_cast<uint64_t>(p);
+    base = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(u))) |
+           static_cast<uint64_t>(static_cast<uint32_t>(
+               __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(u >> 32)))) << 32;
+    step = static_cast<uint32_t>(kBK * (KMAJOR ? ld : 1) * 4);
+    left = K;
+    k = KMAJOR ? tid >> 6 : tid & 31;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int o = KMAJOR ? (tid & 15) * 4 : (tid >> 3) + i * 32;
-      n[i] = 0;
-      if (KMAJOR) {
-        while (n[i] < 4 && at(o + n[i]) >= 0) ++n[i];
-      } else if (at(o) >= 0) {
-        n[i] = 4;
-      }
-      const int src = n[i] ? at(o) : 0;
-      p[i] = base + (KMAJOR ? static_cast<int64_t>(k + 16 * i) * ld + src : static_cast<int64_t>(src) * ld + k);
+    for (int i = 0; i < 8; ++i) {
+      const int src = at(outer(i));
+      voff[i] = src < 0 ? kOutside
+                        : static_cast<uint32_t>(KMAJOR ? (k + 4 * i) * ld + src : src * ld + k) * 4u;
+    }
+    bound();
+  }
+  __device__ __forceinline__ int outer(int i) const {
+    return KMAJOR ? threadIdx.x & 63 : (threadIdx.x >> 5) + 8 * i;
+  }
+  // The last stage may be short and the ones after it are empty.
+  __device__ __forceinline__ void bound() {
+    if (left < kBK) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (k + (KMAJOR ? 4 * i : 0) >= left) voff[i] = kOutside;
     }
   }
-
-  __device__ __forceinline__ void load(int K) {
+  // The next stage's elements of this thread.
+  __device__ __forceinline__ void load(float (&v)[8]) {
+    const __amdgpu_buffer_rsrc_t r =
+        __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(base), 0, kOutside, 0x00020000);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      // of the four, those inside the depth too
-      const int left = K - k;
-      const int m = KMAJOR ? (left > 16 * i ? n[i] : 0) : min(n[i], left);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[i][j] = 0.f;
-      if (m == 4) {
-        const f32x4_a4 q = *reinterpret_cast<const f32x4_a4*>(p[i]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[i][j] = q[j];
-      } else if (m > 0) {
-#pragma unroll
-        for (int j = 0; j < 3; ++j)
-          if (j < m) v[i][j] = p[i][j];
-      }
-      p[i] += step;
-    }
-    k += 2 * kBK;
+    for (int i = 0; i < 8; ++i)
+      v[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, voff[i], 0, 0));
+    base += step;
+    left -= kBK;
+    bound();
   }
-
-  // To LDS as [depth][outer], rows of 97 floats: the transposing writes of a row operand and the
-  // fragment reads (two depths of 32) spread over the banks.
-  __device__ __forceinline__ void store(float* __restrict__ lds) const {
-    const int tid = threadIdx.x;
+  // To LDS as [depth][outer], rows of 97 floats: these writes and the fragment reads (two depths of
+  // 32) spread over the banks.
+  __device__ __forceinline__ void store(const float (&v)[8], float* lds) const {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int o = KMAJOR ? (tid & 15) * 4 + j : (tid >> 3) + i * 32;
-        const int k = KMAJOR ? (tid >> 4) + i * 16 : (tid & 7) * 4 + j;
-        lds[k * kLd + o] = v[i][j];
-      }
+    for (int i = 0; i < 8; ++i) lds[(k + (KMAJOR ? 4 * i : 0)) * kLd + outer(i)] = v[i];
   }
 };
 
@@ -215,32 +206,31 @@ __device__ __forceinline__ floatx16 tile_product_f32(const float* __restrict__ A
   floatx16 even, odd;
 #pragma unroll
   for (int q = 0; q < 16; ++q) even[q] = odd[q] = 0.f;
-  Piece<A_KMAJOR> pa[2];
-  Piece<B_KMAJOR> pb[2];
-  auto load = [&](int i) {
-    pa[i].load(K);
-    pb[i].load(K);
-  };
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    pa[i].init(A, lda, i * kBK, at_a);
-    pb[i].init(B, ldb, i * kBK, at_b);
-    load(i);
-  }
-  // stage i & 1, from its registers and into its LDS.  The barrier of the next stage orders these
-  // reads before the same buffer is written again.
+  OperandF32<A_KMAJOR> oa;
+  OperandF32<B_KMAJOR> ob;
+  oa.init(A, lda, K, at_a);
+  ob.init(B, ldb, K, at_b);
+  float va[2][8], vb[2][8];
+  // stage i & 1, from its registers and into its LDS; then its registers take the stage two ahead.
+  // The barrier of the next stage orders these reads before the same buffer is written again.
   auto stage = [&](int i) {
     float* cur = lds + i * 2 * kF32Lds;
-    pa[i].store(cur);
-    pb[i].store(cur + kF32Lds);
+    oa.store(va[i], cur);
+    ob.store(vb[i], cur + kF32Lds);
     __syncthreads();
-    load(i);
+    oa.load(va[i]);
+    ob.load(vb[i]);
 #pragma unroll
     for (int k = 0; k < kBK; k += 4) {
       even = __builtin_amdgcn_mfma_f32_32x32x2f32(cur[k * kLd + ra], cur[k * kLd + rb], even, 0, 0, 0);
       odd = __builtin_amdgcn_mfma_f32_32x32x2f32(cur[(k + 2) * kLd + ra], cur[(k + 2) * kLd + rb], odd, 0, 0, 0);
     }
   };
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    oa.load(va[i]);
+    ob.load(vb[i]);
+  }
   for (int k0 = 0; k0 < K; k0 += 2 * kBK) {
     stage(0);
     if (k0 + kBK < K) stage(1);
@@ -735,8 +725,9 @@ extern "C" int moe_grouped_swiglu_backward(const void* x_perm, const void* dy_pe
   if (w->expert_bytes != eb || w->n_experts != E)
     return fail(MOE_ERR_ARG, "%s: merged buffer holds %lld-byte blocks for E=%d, expected %lld for E=%d",
                 who, static_cast<long long>(w->expert_bytes), w->n_experts, static_cast<long long>(eb), E);
-  if (static_cast<int64_t>(H) * I >= (int64_t{1} << 29) || H > kMaxSide || I > kMaxSide)
-    return fail(MOE_ERR_UNSUPPORTED, "%s: H=%d or I=%d above %d, or H*I 2^29 or more", who, H, I, kMaxSide);
+  if (eb / 3 >= (int64_t{1} << 30) || H > kMaxSide || I > kMaxSide)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: H=%d or I=%d above %d, or a matrix of 2^30 bytes or more", who, H,
+                I, kMaxSide);
   if (dtype == MOE_BF16 && (H % 8 != 0 || I % 8 != 0))
     return fail(MOE_ERR_UNSUPPORTED, "%s: H=%d and I=%d must be multiples of 8", who, H, I);
   // the largest launch: small tiles of dX and of every expert's weight gradients
