@@ -27,8 +27,6 @@ namespace moe {
 namespace {
 
 constexpr int kMaxSide = 1 << 20;  // largest H and I: bounds the grids
-constexpr int kBM = 64, kBN = 64, kBK = 32;  // f32 tile
-constexpr int kLd = kBM + 33;                // LDS row (one k) of an f32 operand tile
 
 struct BackwardWs {
   size_t dh_off, dgu_off, h_off, total;
@@ -125,182 +123,247 @@ __device__ __forceinline__ void swiglu_grad(float g, float u, float d, float* dg
 // f32
 // ---------------------------------------------------------------------------
 
-// Tiles of 64 x 64, four waves of one 32 x 32 block each: small enough that the few rows of an
-// expert still make blocks for every CU, several of which share a CU and hide one another's
-// latency.  A stage is 32 of depth; the next two stages' loads are in flight while this one's
-// MFMAs run, LDS is double-buffered and an even and an odd accumulator keep two MFMAs independent.
+// Tiles of TR x TR, four waves:
+//   64  a wave a 32 x 32 block, stages of 32 of depth
+//   32  every wave the whole tile and a quarter of each stage's depth (64); the four sums are
+//       added in LDS in wave order.  For calls too small to fill the CUs with large tiles: four
+//       times as many blocks, and half as many stages of depth, each of which takes at least the
+//       latency of its loads.
+// The next two stages' loads are in flight while this one's MFMAs run, LDS is double-buffered and an
+// even and an odd accumulator keep two MFMAs independent.
+template <int TR>
+struct TileF32 {
+  static constexpr int K = TR == 64 ? 32 : 64;   // depth of a stage
+  static constexpr int N = TR * K / 256;         // elements of an operand's stage per thread
+  static constexpr int LD = TR + 1;              // LDS row (one k): writes along k spread over the banks
+  static constexpr int STAGE = K * LD;           // floats of one operand's stage
+  static constexpr int LDS = 4 * STAGE;          // two stages of two operands
+  static constexpr int AHEAD = 2;  // stages of loads in flight
+  static constexpr int NQ = TR == 64 ? 16 : 4;   // elements of C per lane
+  // row and column within the tile of this lane's element q
+  static __device__ __forceinline__ int row(int q) {
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    return TR == 64 ? (wave >> 1) * 32 + (q >> 2) * 8 + (lane >> 5) * 4 + (q & 3)
+                    : wave * 8 + (lane >> 5) * 4 + q;
+  }
+  static __device__ __forceinline__ int block_col() { return TR == 64 ? threadIdx.x / kWave & 1 : 0; }
+  static __device__ __forceinline__ int col() { return block_col() * 32 + (threadIdx.x & 31); }
+};
 
-// How the stages of an operand are loaded: 64 "outer" indices by 32 of depth, 8 elements a thread,
-// each load of a wave one or two runs that lie together in memory.  A lane outside the operand has
-// an offset past the buffer's range, for which the hardware returns zero: no load is behind a
-// branch, so none has to arrive before the branch ends.  KMAJOR: element (o, k) is at
-// p[k * ld + o], else at p[o * ld + k].
-template <bool KMAJOR>
+// How the stages of an operand are loaded: TR "outer" indices by K of depth, each load of a wave one
+// or two runs that lie together in memory.  A lane outside the operand has an offset past the
+// buffer's range, for which the hardware returns zero: no load is behind a branch, so none has to
+// arrive before the branch ends.  KMAJOR: element (o, k) is at p[k * ld + o], else at p[o * ld + k].
+template <int TR, bool KMAJOR>
 struct OperandF32 {
-  uint64_t base;     // wave-uniform: where the stage to load next starts
-  uint32_t step;     // bytes from a stage to the next
-  int left;          // steps of depth from there on
-  int k;             // depth of this thread's element 0 within a stage
-  uint32_t voff[8];  // kOutside for what does not exist
+  using T = TileF32<TR>;
+  static constexpr int STEP = 256 / (KMAJOR ? TR : T::K);  // k's (outer indices) from element to element
+  uint64_t base;        // wave-uniform: where the stage to load next starts
+  uint32_t step;        // bytes from a stage to the next
+  int left;             // steps of depth from there on
+  int k;                // depth of this thread's element 0 within a stage
+  uint32_t voff[T::N];  // kOutside for what does not exist
 
   // at(o) maps a tile's outer index to the operand's, or to -1
   template <typename At>
-  __device__ __forceinline__ void init(const float* p, int64_t ld, int K, At at) {
-    const int tid = threadIdx.x;
+  __device__ __forceinline__ void init(const float* p, int64_t ld, int depth, At at) {
     const uint64_t u = reinterpret_cast<uint64_t>(p);
     base = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(u))) |
            static_cast<uint64_t>(static_cast<uint32_t>(
                __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(u >> 32)))) << 32;
-    step = static_cast<uint32_t>(kBK * (KMAJOR ? ld : 1) * 4);
-    left = K;
-    k = KMAJOR ? tid >> 6 : tid & 31;
+    step = static_cast<uint32_t>(T::K * (KMAJOR ? ld : 1) * 4);
+    left = depth;
+    k = KMAJOR ? threadIdx.x / TR : threadIdx.x % T::K;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < T::N; ++i) {
       const int src = at(outer(i));
       voff[i] = src < 0 ? kOutside
-                        : static_cast<uint32_t>(KMAJOR ? (k + 4 * i) * ld + src : src * ld + k) * 4u;
+                        : static_cast<uint32_t>(KMAJOR ? (k + STEP * i) * ld + src : src * ld + k) * 4u;
     }
-    bound();
   }
   __device__ __forceinline__ int outer(int i) const {
-    return KMAJOR ? threadIdx.x & 63 : (threadIdx.x >> 5) + 8 * i;
+    return KMAJOR ? threadIdx.x % TR : threadIdx.x / T::K + STEP * i;
   }
-  // The last stage may be short and the ones after it are empty.
-  __device__ __forceinline__ void bound() {
-    if (left < kBK) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (k + (KMAJOR ? 4 * i : 0) >= left) voff[i] = kOutside;
-    }
-  }
-  // The next stage's elements of this thread.
-  __device__ __forceinline__ void load(float (&v)[8]) {
+  // Element I of the next stage (the depth past the operand reads zeros: no branch, which would end
+  // the compiler's block).
+  template <int I>
+  __device__ __forceinline__ void load(float (&v)[T::N]) const {
     const __amdgpu_buffer_rsrc_t r =
         __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(base), 0, kOutside, 0x00020000);
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      v[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, voff[i], 0, 0));
-    base += step;
-    left -= kBK;
-    bound();
+    const uint32_t at = k + (KMAJOR ? STEP * I : 0) < left ? voff[I] : kOutside;
+    v[I] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0));
   }
-  // To LDS as [depth][outer], rows of 97 floats: these writes and the fragment reads (two depths of
-  // 32) spread over the banks.
-  __device__ __forceinline__ void store(const float (&v)[8], float* lds) const {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) lds[(k + (KMAJOR ? 4 * i : 0)) * kLd + outer(i)] = v[i];
+  __device__ __forceinline__ void next_stage() {
+    base += step;
+    left -= T::K;
+  }
+  // Element I to LDS as [depth][outer].
+  template <int I>
+  __device__ __forceinline__ void store(const float (&v)[T::N], float* lds) const {
+    lds[(k + (KMAJOR ? STEP * I : 0)) * T::LD + outer(I)] = v[I];
   }
 };
 
-constexpr int kF32Lds = kBK * kLd;  // floats of one operand's stage
-
-// The wave's 32 x 32 block (rows 32 (wave / 2), tile columns 32 (wave % 2)) of A B over depth
-// [0, K).  lds: two stages of two operands.
-template <bool A_KMAJOR, bool B_KMAJOR, typename AtA, typename AtB>
-__device__ __forceinline__ floatx16 tile_product_f32(const float* __restrict__ A, int64_t lda, AtA at_a,
-                                                     const float* __restrict__ B, int64_t ldb, AtB at_b,
-                                                     int K, float* lds) {
+// This lane's elements of the tile of A B over depth [0, K).  lds: TileF32<TR>::LDS floats.
+template <int TR, bool A_KMAJOR, bool B_KMAJOR, typename AtA, typename AtB>
+__device__ __forceinline__ void tile_product_f32(const float* __restrict__ A, int64_t lda, AtA at_a,
+                                                 const float* __restrict__ B, int64_t ldb, AtB at_b, int K,
+                                                 float* lds, float (&c)[TileF32<TR>::NQ]) {
+  using T = TileF32<TR>;
+  constexpr int KW = TR == 64 ? T::K : T::K / 4;  // a wave's depth of a stage
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-  const int ra = (lane >> 5) * kLd + (wave >> 1) * 32 + (lane & 31);
-  const int rb = (lane >> 5) * kLd + (wave & 1) * 32 + (lane & 31) + kF32Lds;
+  const int k_lane = (lane >> 5) + (TR == 64 ? 0 : wave * KW);
+  const int ra = k_lane * T::LD + (TR == 64 ? (wave >> 1) * 32 : 0) + (lane & 31);
+  const int rb = k_lane * T::LD + T::col() + T::STAGE;
   floatx16 even, odd;
 #pragma unroll
   for (int q = 0; q < 16; ++q) even[q] = odd[q] = 0.f;
-  OperandF32<A_KMAJOR> oa;
-  OperandF32<B_KMAJOR> ob;
+  OperandF32<TR, A_KMAJOR> oa;
+  OperandF32<TR, B_KMAJOR> ob;
   oa.init(A, lda, K, at_a);
   ob.init(B, ldb, K, at_b);
-  float va[2][8], vb[2][8];
-  // stage i & 1, from its registers and into its LDS; then its registers take the stage two ahead.
-  // The barrier of the next stage orders these reads before the same buffer is written again.
-  auto stage = [&](int i) {
-    float* cur = lds + i * 2 * kF32Lds;
-    oa.store(va[i], cur);
-    ob.store(vb[i], cur + kF32Lds);
-    __syncthreads();
-    oa.load(va[i]);
-    ob.load(vb[i]);
-#pragma unroll
-    for (int k = 0; k < kBK; k += 4) {
-      even = __builtin_amdgcn_mfma_f32_32x32x2f32(cur[k * kLd + ra], cur[k * kLd + rb], even, 0, 0, 0);
-      odd = __builtin_amdgcn_mfma_f32_32x32x2f32(cur[(k + 2) * kLd + ra], cur[(k + 2) * kLd + rb], odd, 0, 0, 0);
-    }
+  float va[T::AHEAD][T::N], vb[T::AHEAD][T::N];
+  constexpr int NM = KW / 2, NP = NM / 4;  // MFMAs of a stage; fragments read a stage early
+  float fa[2][NM], fb[2][NM];
+  auto read = [&](auto i, auto t, const float* from) {
+    constexpr int I = decltype(i)::value, P = decltype(t)::value;
+    fa[I][P] = from[2 * P * T::LD + ra];
+    fb[I][P] = from[2 * P * T::LD + rb];
   };
+  // Stage i (mod AHEAD), its first fragments read.  With one wave a SIMD every instruction between two
+  // MFMAs counts, so each goes with an MFMA: first this stage's other fragments and the loads of
+  // the stage AHEAD, then the next stage's elements to LDS, and past the barrier (which the reads
+  // of this buffer precede) the next stage's first fragments.
+  auto stage = [&](auto ic) {
+    constexpr int I = decltype(ic)::value, B = I % 2, NEXT = (I + 1) % T::AHEAD;
+    const float* cur = lds + B * 2 * T::STAGE;
+    float* next = lds + (1 - B) * 2 * T::STAGE;
+    each<0, NM>([&](auto tc) {
+      constexpr int t = decltype(tc)::value;
+      if constexpr (t == NM - NP) __syncthreads();
+      floatx16& acc = t % 2 ? odd : even;
+      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(fa[B][t], fb[B][t], acc, 0, 0, 0);
+      each<0, NM>([&](auto f) {
+        constexpr int F = decltype(f)::value;
+        if constexpr (F >= NP && (F - NP) * (NM / 2) / (NM - NP) == t) read(std::integral_constant<int, B>{}, f, cur);
+        if constexpr (F < NP && t == NM - NP + F) read(std::integral_constant<int, 1 - B>{}, f, next);
+      });
+      each<0, T::N>([&](auto e) {
+        constexpr int X = decltype(e)::value;
+        if constexpr (X * (NM / 2) / T::N == t) {
+          oa.template load<X>(va[I]);
+          ob.template load<X>(vb[I]);
+        }
+        if constexpr (NM / 4 + X * (NM / 2) / T::N == t) {
+          oa.template store<X>(va[NEXT], next);
+          ob.template store<X>(vb[NEXT], next + T::STAGE);
+        }
+      });
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    oa.next_stage();
+    ob.next_stage();
+  };
+  each<0, T::AHEAD>([&](auto i) {
+    each<0, T::N>([&](auto e) {
+      oa.template load<decltype(e)::value>(va[decltype(i)::value]);
+      ob.template load<decltype(e)::value>(vb[decltype(i)::value]);
+    });
+    oa.next_stage();
+    ob.next_stage();
+  });
+  each<0, T::N>([&](auto e) {
+    oa.template store<decltype(e)::value>(va[0], lds);
+    ob.template store<decltype(e)::value>(vb[0], lds + T::STAGE);
+  });
+  __syncthreads();
+  each<0, NP>([&](auto t) { read(std::integral_constant<int, 0>{}, t, lds); });
+  int stages = (K + T::K - 1) / T::K;
+  for (; stages >= T::AHEAD; stages -= T::AHEAD) each<0, T::AHEAD>(stage);
+  if (stages > 0) stage(std::integral_constant<int, 0>{});
+  if constexpr (T::AHEAD == 4) {
+    if (stages > 1) stage(std::integral_constant<int, 1>{});
+    if (stages > 2) stage(std::integral_constant<int, 2>{});
+  }
+  const floatx16 sum = even + odd;
+  if constexpr (TR == 64) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    oa.load(va[i]);
-    ob.load(vb[i]);
+    for (int q = 0; q < 16; ++q) c[q] = sum[q];
+  } else {
+    __syncthreads();  // the stages' reads are done
+#pragma unroll
+    for (int q = 0; q < 16; ++q) lds[(wave * 16 + q) * kWave + lane] = sum[q];
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float* p = lds + (wave * 4 + q) * kWave + lane;
+      c[q] = p[0] + p[16 * kWave] + p[32 * kWave] + p[48 * kWave];
+    }
   }
-  for (int k0 = 0; k0 < K; k0 += 2 * kBK) {
-    stage(0);
-    if (k0 + kBK < K) stage(1);
-  }
-  return even + odd;
 }
 
-// Row within the tile of element q of this lane's block; its tile column is 32 (wave % 2) + lane % 32.
-__device__ __forceinline__ int acc_row(int q) {
-  const int lane = threadIdx.x & (kWave - 1);
-  return (threadIdx.x / kWave >> 1) * 32 + (q >> 2) * 8 + (lane >> 5) * 4 + (q & 3);
-}
-__device__ __forceinline__ int acc_col() { return (threadIdx.x / kWave & 1) * 32 + (threadIdx.x & 31); }
-
-// C[r][n] = sum_k A[r][k] B[k][n] for tile m's rows and columns n0 .. n0 + 63; B of the tile's expert
-// starts at b_off of its block.
+// C[r][n] = sum_k A[r][k] B[k][n] for tile m's rows and columns n0 .. n0 + TR - 1; B of the tile's
+// expert starts at b_off of its block.
+template <int TR>
 __device__ __forceinline__ void rows_product_f32(const Experts& x, int m, int n0, bool report,
                                                  const float* A, int64_t lda, const char* wbase,
                                                  int64_t expert_bytes, int64_t b_off, int N, int K,
                                                  float* C, float* lds) {
   Tile t;
-  if (!find_tile<kBM>(x, m, report, &t)) return;
+  if (!find_tile<TR>(x, m, report, &t)) return;
+  using S = TileF32<TR>;
   const float* B = reinterpret_cast<const float*>(wbase + t.slot * expert_bytes + b_off);
-  const floatx16 acc = tile_product_f32<false, true>(
+  float acc[S::NQ];
+  tile_product_f32<TR, false, true>(
       A + t.row0 * lda, lda, [&](int o) { return o < t.rows ? o : -1; }, B, N,
-      [&](int o) { return n0 + o < N ? n0 + o : -1; }, K, lds);
-  const int c = n0 + acc_col();
+      [&](int o) { return n0 + o < N ? n0 + o : -1; }, K, lds, acc);
+  const int c = n0 + S::col();
   if (c >= N) return;
 #pragma unroll
-  for (int q = 0; q < 16; ++q)
-    if (acc_row(q) < t.rows) C[static_cast<int64_t>(t.row0 + acc_row(q)) * N + c] = acc[q];
+  for (int q = 0; q < S::NQ; ++q)
+    if (S::row(q) < t.rows) C[static_cast<int64_t>(t.row0 + S::row(q)) * N + c] = acc[q];
 }
 
+template <int TR>
 __global__ __launch_bounds__(256) void dh_f32_kernel(Experts x, const float* __restrict__ dy,
                                                      const char* __restrict__ wbase, int64_t expert_bytes,
                                                      int H, int I, float* __restrict__ dh) {
-  __shared__ float lds[4 * kF32Lds];
-  rows_product_f32(x, blockIdx.x, blockIdx.y * kBN, blockIdx.x == 0 && blockIdx.y == 0, dy, H, wbase,
-                   expert_bytes, 2 * static_cast<int64_t>(H) * I * 4, I, H, dh, lds);
+  __shared__ float lds[TileF32<TR>::LDS];
+  rows_product_f32<TR>(x, blockIdx.x, blockIdx.y * TR, blockIdx.x == 0 && blockIdx.y == 0, dy, H, wbase,
+                       expert_bytes, 2 * static_cast<int64_t>(H) * I * 4, I, H, dh, lds);
 }
 
-// g and u for 32 columns, then dG, dU and h from dH.  Each wave's 32 tile columns are 16 of Wg and
-// the same 16 of Wu: lanes l and l ^ 16 hold g and u of one element.
+// g and u for TR / 2 columns, then dG, dU and h from dH.  Each 32 tile columns are 16 of Wg and the
+// same 16 of Wu: lanes l and l ^ 16 hold g and u of one element.
+template <int TR>
 __global__ __launch_bounds__(256) void gate_up_backward_f32_kernel(
     Experts ex, const float* __restrict__ x, const char* __restrict__ wbase, int64_t expert_bytes, int H,
     int I, const float* __restrict__ dh, float* __restrict__ dgu, float* __restrict__ h) {
-  __shared__ float lds[4 * kF32Lds];
+  using S = TileF32<TR>;
+  __shared__ float lds[S::LDS];
   Tile t;
-  if (!find_tile<kBM>(ex, blockIdx.x, false, &t)) return;
-  const int n0 = blockIdx.y * (kBN / 2);
+  if (!find_tile<TR>(ex, blockIdx.x, false, &t)) return;
+  const int n0 = blockIdx.y * (TR / 2);
   const float* W = reinterpret_cast<const float*>(wbase + t.slot * expert_bytes);
-  const int c = n0 + (threadIdx.x / kWave & 1) * 16 + (threadIdx.x & 15);
+  const int c = n0 + S::block_col() * 16 + (threadIdx.x & 15);
   const bool up = threadIdx.x & 16;
   // dH arrives while the products run; a lane past the tile or past I reads a place inside
-  float d[16];
+  float d[S::NQ], acc[S::NQ];
 #pragma unroll
-  for (int q = 0; q < 16; ++q)
-    d[q] = dh[static_cast<int64_t>(t.row0 + min(acc_row(q), t.rows - 1)) * I + min(c, I - 1)];
-  const floatx16 acc = tile_product_f32<false, false>(
+  for (int q = 0; q < S::NQ; ++q)
+    d[q] = dh[static_cast<int64_t>(t.row0 + min(S::row(q), t.rows - 1)) * I + min(c, I - 1)];
+  tile_product_f32<TR, false, false>(
       x + static_cast<int64_t>(t.row0) * H, H, [&](int o) { return o < t.rows ? o : -1; }, W, H,
       [&](int o) {
         const int c = n0 + (o >> 5) * 16 + (o & 15);
         return c < I ? c + (o >> 4 & 1) * I : -1;
       },
-      H, lds);
+      H, lds, acc);
 #pragma unroll
-  for (int q = 0; q < 16; ++q) {
+  for (int q = 0; q < S::NQ; ++q) {
     const float mate = __shfl_xor(acc[q], 16);
-    if (acc_row(q) >= t.rows || c >= I) continue;
-    const int64_t row = t.row0 + acc_row(q);
+    if (S::row(q) >= t.rows || c >= I) continue;
+    const int64_t row = t.row0 + S::row(q);
     float dg, du, hv;
     swiglu_grad(up ? mate : acc[q], up ? acc[q] : mate, d[q], &dg, &du, &hv);
     if (up) {
@@ -320,6 +383,7 @@ struct Ranges {
 
 // C[m][n] = sum over expert e's rows r of A[r][m] B[r][n], written at c_off of the expert's block of
 // dw.  An expert without rows gets zeros, one outside the buffer nothing.
+template <int TR>
 __device__ __forceinline__ void weight_grad_f32(const Experts& x, int e, int m0, int n0, const float* A,
                                                 int M, const float* B, int N, int64_t expert_bytes,
                                                 int64_t c_off, char* dw, float* lds) {
@@ -327,38 +391,43 @@ __device__ __forceinline__ void weight_grad_f32(const Experts& x, int e, int m0,
   if (slot < 0 || slot >= x.n_slots) return;
   int lo;
   const int K = expert_rows(x, e, &lo);
-  const floatx16 acc = tile_product_f32<true, true>(
+  using S = TileF32<TR>;
+  float acc[S::NQ];
+  tile_product_f32<TR, true, true>(
       A + static_cast<int64_t>(lo) * M, M, [&](int o) { return m0 + o < M ? m0 + o : -1; },
-      B + static_cast<int64_t>(lo) * N, N, [&](int o) { return n0 + o < N ? n0 + o : -1; }, K, lds);
+      B + static_cast<int64_t>(lo) * N, N, [&](int o) { return n0 + o < N ? n0 + o : -1; }, K, lds, acc);
   float* C = reinterpret_cast<float*>(dw + slot * expert_bytes + c_off);
-  const int c = n0 + acc_col();
+  const int c = n0 + S::col();
   if (c >= N) return;
 #pragma unroll
-  for (int q = 0; q < 16; ++q)
-    if (m0 + acc_row(q) < M) C[static_cast<int64_t>(m0 + acc_row(q)) * N + c] = acc[q];
+  for (int q = 0; q < S::NQ; ++q)
+    if (m0 + S::row(q) < M) C[static_cast<int64_t>(m0 + S::row(q)) * N + c] = acc[q];
 }
 
+// DX and DW: the tiles of dX and of the weight gradients.
+template <int DX, int DW>
 __global__ __launch_bounds__(256) void grads_f32_kernel(
     Experts ex, const float* __restrict__ x, const float* __restrict__ dy, const float* __restrict__ dgu,
     const float* __restrict__ h, const char* __restrict__ wbase, int64_t expert_bytes, int H, int I,
     Ranges ranges, float* __restrict__ dx, char* __restrict__ dw) {
-  __shared__ float lds[4 * kF32Lds];
-  const int nh = (H + kBN - 1) / kBN, ni = (I + kBN - 1) / kBN;
+  __shared__ float lds[std::max(TileF32<DX>::LDS, TileF32<DW>::LDS)];
   int64_t b = blockIdx.x;
   if (b < ranges.dx) {
-    rows_product_f32(ex, static_cast<int>(b / nh), static_cast<int>(b % nh) * kBN, false, dgu,
+    const int nh = (H + DX - 1) / DX;
+    rows_product_f32<DX>(ex, static_cast<int>(b / nh), static_cast<int>(b % nh) * DX, false, dgu,
                      2 * static_cast<int64_t>(I), wbase, expert_bytes, 0, H, 2 * I, dx, lds);
     return;
   }
   b -= ranges.dx;
+  const int nh = (H + DW - 1) / DW, ni = (I + DW - 1) / DW;
   if (b < ranges.dwgu) {
     const int e = static_cast<int>(b / ranges.per_gu), at = static_cast<int>(b % ranges.per_gu);
-    weight_grad_f32(ex, e, at / nh * kBM, at % nh * kBN, dgu, 2 * I, x, H, expert_bytes, 0, dw, lds);
+    weight_grad_f32<DW>(ex, e, at / nh * DW, at % nh * DW, dgu, 2 * I, x, H, expert_bytes, 0, dw, lds);
     return;
   }
   b -= ranges.dwgu;
   const int e = static_cast<int>(b / ranges.per_d), at = static_cast<int>(b % ranges.per_d);
-  weight_grad_f32(ex, e, at / ni * kBM, at % ni * kBN, dy, H, h, I, expert_bytes,
+  weight_grad_f32<DW>(ex, e, at / ni * DW, at % ni * DW, dy, H, h, I, expert_bytes,
                   2 * static_cast<int64_t>(H) * I * 4, dw, lds);
 }
 
@@ -600,31 +669,54 @@ struct Call {
   hipStream_t s;
 };
 
+// Small tiles for a product with fewer than two large ones a CU.  Measured, large against small: dH
+// of 128 rows, depth 1024 (144 large tiles) 25 / 15 us; 1024 rows, depth 256 (192) 10.4 / 9.1; 2048
+// rows, depth 512 (320) 24 / 21; 4096 rows, depth 512 (576) 33 / 34; 8192 rows, depth 1023 (2176)
+// 175 / 227.
+bool small_tiles_f32(int64_t large) { return large < 2 * kCus; }
+
+template <int DX, int DW>
+int launch_grads_f32(const Call& c, const float* x, const float* dy, const float* dgu, const float* h) {
+  const int E = c.ex.E, H = c.H, I = c.I;
+  Ranges r;
+  r.dx = c.dx_perm ? max_tiles(c.ex.R, E, DX) * ceil_div(H, DX) : 0;
+  r.per_gu = ceil_div(2 * I, DW) * ceil_div(H, DW);
+  r.per_d = ceil_div(H, DW) * ceil_div(I, DW);
+  r.dwgu = c.dw ? static_cast<int64_t>(E) * r.per_gu : 0;
+  const int64_t blocks = r.dx + r.dwgu + (c.dw ? static_cast<int64_t>(E) * r.per_d : 0);
+  if (blocks == 0) return MOE_OK;
+  hipLaunchKernelGGL((grads_f32_kernel<DX, DW>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, c.s, c.ex,
+                     x, dy, dgu, h, c.wbase, c.expert_bytes, H, I, r, static_cast<float*>(c.dx_perm), c.dw);
+  MOE_LAUNCH_CHECK("moe_grouped_swiglu_backward: gradients");
+  return MOE_OK;
+}
+
 int run_f32(const Call& c, const float* x, const float* dy) {
   const int E = c.ex.E, H = c.H, I = c.I;
   float* dh = reinterpret_cast<float*>(c.ws + c.L.dh_off);
   float* dgu = reinterpret_cast<float*>(c.ws + c.L.dgu_off);
   float* h = reinterpret_cast<float*>(c.ws + c.L.h_off);
-  const unsigned cap = static_cast<unsigned>(max_tiles(c.ex.R, E, kBM));
+  const int64_t large = max_tiles(c.ex.R, E, 64);
   if (c.ex.R > 0) {
-    hipLaunchKernelGGL(dh_f32_kernel, dim3(cap, ceil_div(I, kBN)), dim3(256), 0, c.s, c.ex, dy, c.wbase,
-                       c.expert_bytes, H, I, dh);
+    bool small = small_tiles_f32(large * ceil_div(I, 64));
+    int tr = small ? 32 : 64;
+    hipLaunchKernelGGL(small ? dh_f32_kernel<32> : dh_f32_kernel<64>,
+                       dim3(static_cast<unsigned>(max_tiles(c.ex.R, E, tr)), ceil_div(I, tr)), dim3(256), 0,
+                       c.s, c.ex, dy, c.wbase, c.expert_bytes, H, I, dh);
     MOE_LAUNCH_CHECK("moe_grouped_swiglu_backward: dh");
-    hipLaunchKernelGGL(gate_up_backward_f32_kernel, dim3(cap, ceil_div(I, kBN / 2)), dim3(256), 0, c.s,
-                       c.ex, x, c.wbase, c.expert_bytes, H, I, dh, dgu, h);
+    small = small_tiles_f32(large * ceil_div(I, 32));
+    tr = small ? 32 : 64;
+    hipLaunchKernelGGL(small ? gate_up_backward_f32_kernel<32> : gate_up_backward_f32_kernel<64>,
+                       dim3(static_cast<unsigned>(max_tiles(c.ex.R, E, tr)), ceil_div(I, tr / 2)), dim3(256), 0,
+                       c.s, c.ex, x, c.wbase, c.expert_bytes, H, I, dh, dgu, h);
     MOE_LAUNCH_CHECK("moe_grouped_swiglu_backward: gate/up");
   }
-  Ranges r;
-  r.dx = c.dx_perm ? static_cast<int64_t>(cap) * ceil_div(H, kBN) : 0;
-  r.per_gu = ceil_div(2 * I, kBM) * ceil_div(H, kBN);
-  r.per_d = ceil_div(H, kBM) * ceil_div(I, kBN);
-  r.dwgu = c.dw ? static_cast<int64_t>(E) * r.per_gu : 0;
-  const int64_t blocks = r.dx + r.dwgu + (c.dw ? static_cast<int64_t>(E) * r.per_d : 0);
-  if (blocks == 0) return MOE_OK;
-  hipLaunchKernelGGL(grads_f32_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, c.s, c.ex, x, dy,
-                     dgu, h, c.wbase, c.expert_bytes, H, I, r, static_cast<float*>(c.dx_perm), c.dw);
-  MOE_LAUNCH_CHECK("moe_grouped_swiglu_backward: gradients");
-  return MOE_OK;
+  const int64_t nh = ceil_div(H, 64), ni = ceil_div(I, 64);
+  const bool small_dx = small_tiles_f32(large * nh);
+  const bool small_dw = small_tiles_f32(E * nh * (ceil_div(2 * I, 64) + ni));
+  auto launch = small_dx ? (small_dw ? launch_grads_f32<32, 32> : launch_grads_f32<32, 64>)
+                         : (small_dw ? launch_grads_f32<64, 32> : launch_grads_f32<64, 64>);
+  return launch(c, x, dy, dgu, h);
 }
 
 Order make_order(int tr, int64_t mt, int64_t nt, int64_t* blocks) {
@@ -750,7 +842,9 @@ extern "C" int moe_grouped_swiglu_backward(const void* x_perm, const void* dy_pe
                static_cast<char*>(dw), s};
   int rc;
   if (dtype == MOE_F32) {
-    rc = run_f32(c, static_cast<const float*>(x_perm), static_cast<const float*>(dy_perm));
+    const float* x = static_cast<const float*>(x_perm);
+    const float* dy = static_cast<const float*>(dy_perm);
+    rc = run_f32(c, x, dy);
   } else {
     const uint16_t* x = static_cast<const uint16_t*>(x_perm);
     const uint16_t* dy = static_cast<const uint16_t*>(dy_perm);

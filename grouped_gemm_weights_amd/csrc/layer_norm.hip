@@ -369,7 +369,6 @@ __global__ __launch_bounds__(kSumWaves* kWave) void norm_sum_kernel(
 
 constexpr int kMaxH = kMaxWaves * kWave * 4 * kVec;          // 32768: the longest row norm_kernel holds
 constexpr int kMaxBackwardH = kMaxWaves * kWave * 2 * kVec;  // 16384: the longest of the backward kernel
-constexpr int kCus = 256;
 constexpr int kPartials = kCus;                              // most blocks of the backward pass
 constexpr int kJoinBytes = kMaxWaves * kWave * kVec * 2 * sizeof(float);  // 64 KB: 16 waves' sums
 

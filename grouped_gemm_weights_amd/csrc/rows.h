@@ -16,6 +16,7 @@ inline bool too_many(int64_t blocks, int threads) { return blocks * threads > UI
 typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
 typedef float f32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
 
+constexpr int kCus = 256;
 constexpr int kVec = 8;             // elements per lane and step
 constexpr int kMaxRow = 1 << 26;    // longest row: grids and column indices stay in range
 
@@ -167,8 +168,8 @@ __device__ __forceinline__ void store8(float* row, int64_t v, int n, const float
 }
 
 // Sum over the wave, the same in every lane: four adds of lanes 1, 2, 4 and 8 to the left within
-// rows of 16 lanes, then row 0's (2's) total into row 1 (3) and the lower half's into the upper, on
-// the data path between lanes (a sixth of the latency of six LDS permutes).
+// rows of 16 lanes, then row 0's (2's) total into row 1 (3) and the lower half's into the upper, all on
+// the data path between lanes and not through LDS.
 __device__ __forceinline__ float wave_sum(float v) {
 #define ADD(CTRL, ROWS)                                                                       \
   v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xf, true))
