@@ -416,6 +416,17 @@ def test_grouped_swiglu_backward(counts, H, I, dtype):
     assert torch.equal(first[0], dx) and torch.equal(first[1], dw)
 
 
+# f32: each pair of tile sizes (large, small) that dX and the weight gradients can have
+@pytest.mark.parametrize("counts,H,I", [((700, 1, 899, 500), 1030, 901), ((3500,), 645, 130),
+                                        ((5, 7, 0, 1, 33, 2, 3, 4, 5, 6, 7, 8), 330, 261),
+                                        ((31, 33, 0, 65), 97, 63)])
+def test_grouped_swiglu_backward_f32_tiles(counts, H, I):
+    log(f"case experts backward rows={counts} H={H} I={I} f32")
+    inp, dx, dw, status = run_experts(counts, H, I, "f32", 90 + H + I)
+    assert status == 0
+    check_experts(counts, H, I, "f32", inp, dx, dw)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("seed", range(8))
 def test_grouped_swiglu_backward_random(seed, dtype):
