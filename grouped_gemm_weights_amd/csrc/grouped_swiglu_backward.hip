@@ -76,35 +76,30 @@ __device__ __forceinline__ bool find_tile(const Experts& x, int m, bool report, 
   const int lane = threadIdx.x & (kWave - 1);
   const int per = (x.E + kWave - 1) / kWave;  // experts of a lane
   const int e0 = min(lane * per, x.E), e1 = min(e0 + per, x.E);
-  int n = 0, lo;
+  int n = 0, cnt = 0, lo = 0, slot = 0;
   for (int e = e0; e < e1; ++e) {
-    const int cnt = expert_rows(x, e, &lo);
-    if (cnt == 0) continue;
-    const int slot = x.slot_of[e];
+    cnt = expert_rows(x, e, &lo);
+    slot = x.slot_of[e];  // unconditional: it is on its way together with the offsets
     if (slot >= 0 && slot < x.n_slots) n += (cnt + TR - 1) / TR;
-    else if (report) status_or(x.status, MOE_STATUS_EXPERT_ABSENT);
+    else if (report && cnt > 0) status_or(x.status, MOE_STATUS_EXPERT_ABSENT);
   }
-  int end = n;  // tiles up to and with this lane's experts
-#pragma unroll
-  for (int off = 1; off < kWave; off <<= 1) {
-    const int add = __shfl_up(end, off);
-    if (lane >= off) end += add;
-  }
+  const int end = wave_scan(n);  // tiles up to and with this lane's experts
   const uint64_t mine = __ballot(m >= end - n && m < end);
   if (mine == 0) return false;
-  int at = m - (end - n), row0 = 0, rows = 0, slot = 0;
-  for (int e = e0; e < e1; ++e) {
-    const int cnt = expert_rows(x, e, &lo);
-    if (cnt == 0) continue;
-    const int s = x.slot_of[e];
-    if (s < 0 || s >= x.n_slots) continue;
-    const int tiles = (cnt + TR - 1) / TR;
-    if (at >= 0 && at < tiles) {
-      row0 = lo + at * TR;
-      rows = min(TR, cnt - at * TR);
-      slot = s;
+  int left = m - (end - n), row0 = lo + left * TR, rows = min(TR, cnt - left * TR);
+  if (per > 1) {
+    for (int e = e0; e < e1; ++e) {
+      cnt = expert_rows(x, e, &lo);
+      const int s = x.slot_of[e];
+      if (s < 0 || s >= x.n_slots) continue;
+      const int tiles = (cnt + TR - 1) / TR;
+      if (left >= 0 && left < tiles) {
+        row0 = lo + left * TR;
+        rows = min(TR, cnt - left * TR);
+        slot = s;
+      }
+      left -= tiles;
     }
-    at -= tiles;
   }
   const int owner = __builtin_ctzll(mine);
   t->row0 = __builtin_amdgcn_readlane(row0, owner);
@@ -387,10 +382,9 @@ template <int TR>
 __device__ __forceinline__ void weight_grad_f32(const Experts& x, int e, int m0, int n0, const float* A,
                                                 int M, const float* B, int N, int64_t expert_bytes,
                                                 int64_t c_off, char* dw, float* lds) {
-  const int slot = x.slot_of[e];
-  if (slot < 0 || slot >= x.n_slots) return;
   int lo;
-  const int K = expert_rows(x, e, &lo);
+  const int K = expert_rows(x, e, &lo), slot = x.slot_of[e];
+  if (slot < 0 || slot >= x.n_slots) return;
   using S = TileF32<TR>;
   float acc[S::NQ];
   tile_product_f32<TR, true, true>(
@@ -613,11 +607,11 @@ __device__ __forceinline__ void weight_grad(const Experts& x, int e, int m, int 
   using S = TileShape<TR, 0, false>;
   const int m0 = m * TR, n0 = n * S::TN;
   if (m0 >= M || n0 >= N) return;
-  const int slot = __builtin_amdgcn_readfirstlane(x.slot_of[e]);
-  if (slot < 0 || slot >= x.n_slots) return;
   int lo;
   const int K = __builtin_amdgcn_readfirstlane(expert_rows(x, e, &lo));
+  const int slot = __builtin_amdgcn_readfirstlane(x.slot_of[e]);
   lo = __builtin_amdgcn_readfirstlane(lo);
+  if (slot < 0 || slot >= x.n_slots) return;
   Operand<true, TR> oa;
   Operand<true, S::TN> ob;
   oa.init(A + static_cast<int64_t>(lo) * M + m0, M, K, [&](int c) { return m0 + c < M ? c : -1; });

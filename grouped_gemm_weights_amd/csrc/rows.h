@@ -167,12 +167,23 @@ __device__ __forceinline__ void store8(float* row, int64_t v, int n, const float
   }
 }
 
-// Sum over the wave, the same in every lane: four adds of lanes 1, 2, 4 and 8 to the left within
-// rows of 16 lanes, then row 0's (2's) total into row 1 (3) and the lower half's into the upper, all on
-// the data path between lanes and not through LDS.
+// Inclusive prefix sum over the wave: four adds of lanes 1, 2, 4 and 8 to the left within rows of 16
+// lanes, then row 0's (2's) total into row 1 (3) and the lower half's into the upper, all on the data
+// path between lanes and not through LDS.
+#define DPP(v, CTRL, ROWS) __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, true)
+__device__ __forceinline__ int wave_scan(int v) {
+  v += DPP(v, 0x111, 0xf);
+  v += DPP(v, 0x112, 0xf);
+  v += DPP(v, 0x114, 0xf);
+  v += DPP(v, 0x118, 0xf);
+  v += DPP(v, 0x142, 0xa);
+  v += DPP(v, 0x143, 0xc);
+  return v;
+}
+
+// Sum over the wave, the same in every lane: the scan's last lane.
 __device__ __forceinline__ float wave_sum(float v) {
-#define ADD(CTRL, ROWS)                                                                       \
-  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xf, true))
+#define ADD(CTRL, ROWS) v += __int_as_float(DPP(__float_as_int(v), CTRL, ROWS))
   ADD(0x111, 0xf);
   ADD(0x112, 0xf);
   ADD(0x114, 0xf);
@@ -182,5 +193,6 @@ __device__ __forceinline__ float wave_sum(float v) {
 #undef ADD
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
+#undef DPP
 
 }  // namespace moe

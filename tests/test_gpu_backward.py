@@ -665,6 +665,24 @@ def test_layer_reads_the_x_that_is_there(fused_gather):
         L.close()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_layer_training_step_without_tokens(dtype):
+    """An empty batch: every gradient of a parameter that the half holds is zero."""
+    cfg, L, dy = layer_case(dtype, True, T=0)
+    try:
+        for t in (L.dw, L.dgamma, L.dbeta):
+            t.fill_(float("nan"))
+        torch.cuda.synchronize()
+        L.forward(half=0, remote="all")
+        L.backward(dy, half=0)
+        assert L.read_status() == 0
+        assert not L.dgamma.any() and not L.dbeta.any()
+        assert not L.dw[L.slot_maps[0].long()].any()
+        assert L.dx.shape == (0, cfg.H) and L.dlogits.shape == (0, cfg.E)
+    finally:
+        L.close()
+
+
 def test_layer_training_refusals():
     cfg, L, dy = layer_case("bf16", False)
     try:
