@@ -13,7 +13,7 @@
 //      dW: [dWg; dWu] = [dG dU]^T X and dWd = dY^T h, one block per expert and output tile.  The
 //      three are independent, so the blocks of one fill the CUs that the last of another leave.
 // A block finds its tile of rows from offsets by itself (find_tile: a scan over the experts in
-// each wave, about 1 us of a block's time, against 4-5 us for a launch that lists the tiles).
+// each wave, under 1 us of a block's time, against 4-5 us for a launch that lists the tiles).
 // Measured, bf16, 65536 rows of 32 experts of 7168 x 2048: 1.69 + 3.6 + 8.15 ms (1140, 1070 and 1180
 // TFLOP/s; the chip holds 1.7-1.9 GHz), so 1150 in all against 1400-1500 of one large library
 // product.  24576 rows of 64 experts of 2048 x 1408, skewed: 0.20 + 0.39 + 0.95 ms, where a weight
@@ -130,7 +130,7 @@ __device__ __forceinline__ void swiglu_grad(float g, float u, float d, float* dg
 // The loads of a stage are issued two stages ahead, LDS is double-buffered and an even and an odd
 // accumulator keep two MFMAs independent.  Measured: 8192 rows of 8 experts of 1023 x 1001 1.29 ms
 // (104 of the fp32 MFMA's 140 TFLOP/s that a large library product reaches), 1024 rows of 8
-// experts of 256 x 512 52 us, one token x 3 of 280 x 273 21 us (launches and depth loops).
+// experts of 256 x 512 51 us, one token x 3 of 280 x 273 19 us (launches and depth loops).
 template <int TR>
 struct TileF32 {
   static constexpr int K = TR == 64 ? 32 : 64;   // depth of a stage
