@@ -330,8 +330,8 @@ class MoELayer:
         read-back, nothing waits on the host) or 'all' (fetch the whole remote share).
         chunks > 0 (not with 'device') splits the remote fetch into that many chunks with one
         ready event each, and the grouped GEMM runs per chunk as its weights land (the local
-        experts first, while the copies run)."""
-        self.route_permute()
+        experts first, while the copies run).  normed: as route_permute takes it."""
+        self.route_permute(normed)
         if remote == "device":
             if chunks > 0:
                 raise ValueError("the device-routed pull is not chunked")
