@@ -42,6 +42,7 @@ EXPORTS = (
     "moe_layer_norm", "moe_layer_norm_backward_workspace_size", "moe_layer_norm_backward",
     "moe_combine_backward", "moe_permute_backward", "moe_route_backward",
     "moe_grouped_swiglu_backward_workspace_size", "moe_grouped_swiglu_backward",
+    "moe_clear_unmapped",
 )
 
 
@@ -106,6 +107,7 @@ def _load() -> ctypes.CDLL:
         "moe_grouped_swiglu_backward_workspace_size": [I, I, I, I, I, PSZ],
         "moe_grouped_swiglu_backward": [P, P, P, I, I, I, I, I, ctypes.POINTER(MoeWbuf), P, SZ, P, P,
                                         P, P],
+        "moe_clear_unmapped": [ctypes.POINTER(MoeWbuf), P, P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -308,6 +310,10 @@ def moe_grouped_swiglu_backward(x_perm, dy_perm, offsets, R, E, H, I, dtype, w: 
            lib.moe_grouped_swiglu_backward(ptr(x_perm), ptr(dy_perm), ptr(offsets), R, E, H, I, dtype,
                                            ctypes.byref(w), ptr(ws), ws_bytes, ptr(dx_perm), ptr(dw),
                                            ptr(status), stream_handle(stream)))
+
+
+def moe_clear_unmapped(w: MoeWbuf, dw, stream=None):
+    _check("moe_clear_unmapped", lib.moe_clear_unmapped(ctypes.byref(w), ptr(dw), stream_handle(stream)))
 
 
 def moe_dense_gemm(x, w, M, N, K, out, stream=None):

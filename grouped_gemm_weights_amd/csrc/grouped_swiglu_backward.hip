@@ -21,6 +21,8 @@
 //
 // bf16: the tile product of mfma_tile.h; dH and dX read the weights transposed, dW both operands.
 // f32: 64 x 64 tiles of the fp32 MFMA (32x32x2), staged through registers.
+//
+// moe_clear_unmapped: zeros for the blocks of dw that belong to no expert.
 #include <algorithm>
 #include <type_traits>
 
@@ -783,8 +785,54 @@ int run_bf16(const Call& c, const uint16_t* x, const uint16_t* dy) {
                       static_cast<uint16_t*>(c.dx_perm), c.dw);
 }
 
+// Zeros for the blocks of dw whose slot no expert maps to.  `parts` workgroups a slot, each of which
+// looks the slot up in slot_of (4 KB at most, from L2) and leaves if an expert has it, so the cost is
+// a launch and the bytes that have to be zero.
+constexpr int64_t kClearBytes = 1 << 20;  // of a workgroup
+
+__global__ __launch_bounds__(256) void clear_unmapped_kernel(const int32_t* __restrict__ slot_of, int E,
+                                                             int parts, int64_t words,
+                                                             uint32_t* __restrict__ dw) {
+  typedef uint32_t u32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
+  const int slot = blockIdx.x / parts, part = blockIdx.x % parts;
+  int mapped = 0;
+  for (int e = threadIdx.x; e < E; e += 256) mapped |= slot_of[e] == slot;
+  if (__syncthreads_or(mapped)) return;
+  uint32_t* p = dw + slot * words;
+  const int64_t begin = part * (kClearBytes / 4), end = min(begin + kClearBytes / 4, words);
+  for (int64_t i = begin + threadIdx.x * 4; i < end; i += 1024) {
+    if (i + 4 <= end) {
+      __builtin_nontemporal_store(u32x4_a4{0, 0, 0, 0}, reinterpret_cast<u32x4_a4*>(p + i));
+    } else {
+      for (int64_t j = i; j < end; ++j) p[j] = 0;
+    }
+  }
+}
+
 }  // namespace
 }  // namespace moe
+
+extern "C" int moe_clear_unmapped(const moe_wbuf* w, void* dw, moe_stream_t stream) {
+  using namespace moe;
+  const char* who = "moe_clear_unmapped";
+  if (!w || !w->slot_of || w->n_experts < 1 || w->n_slots < 0 || w->expert_bytes < 4 || w->expert_bytes % 4 != 0)
+    return fail(MOE_ERR_ARG, "%s: bad merged buffer", who);
+  if (w->n_experts > MOE_MAX_E) return fail(MOE_ERR_UNSUPPORTED, "%s: E=%d above %d", who, w->n_experts, MOE_MAX_E);
+  const int64_t parts = (w->expert_bytes - 1) / kClearBytes + 1;  // no sum or product here can pass 64 bits
+  if (parts > UINT32_MAX / 256 || too_many(parts * w->n_slots, 256))
+    return fail(MOE_ERR_UNSUPPORTED, "%s: %d slots of %lld bytes are more than a launch takes", who, w->n_slots,
+                static_cast<long long>(w->expert_bytes));
+  if (w->n_slots == 0) return MOE_OK;
+  if (!dw) return fail(MOE_ERR_ARG, "%s: null pointer", who);
+  if (reinterpret_cast<uintptr_t>(dw) % 4 != 0)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: a pointer is not aligned to 4 bytes", who);
+  hipStream_t s = as_stream(stream);
+  hipLaunchKernelGGL(clear_unmapped_kernel, dim3(static_cast<unsigned>(parts * w->n_slots)), dim3(256), 0, s,
+                     w->slot_of, w->n_experts, static_cast<int>(parts), w->expert_bytes / 4,
+                     static_cast<uint32_t*>(dw));
+  MOE_LAUNCH_CHECK("moe_clear_unmapped: launch");
+  return debug_check(MOE_OK, who, s, nullptr);
+}
 
 extern "C" int moe_grouped_swiglu_backward_workspace_size(int R, int E, int H, int I, moe_dtype dtype,
                                                           size_t* bytes) {

@@ -20,7 +20,7 @@ The backward pass runs on the compute stream, on the buffers of the step it
 follows:
 
     moe_combine_backward -> moe_route_backward -> moe_grouped_swiglu_backward
-    -> moe_permute_backward (-> moe_layer_norm_backward)
+    -> moe_clear_unmapped -> moe_permute_backward (-> moe_layer_norm_backward)
 
 Every step of the arithmetic runs in the library's HIP kernels.
 """
@@ -388,9 +388,10 @@ class MoELayer:
 
     def backward_experts(self, dy: torch.Tensor, half: int = 0) -> None:
         """Compute stream: from dy (the gradient of y, [T, H] f32 or bf16, written on the compute
-        stream) the gradients of the logits (``dlogits``), of the experts' weights (``dw``: slot by
-        slot as the half holds the experts) and of the rows they saw (``dxn``; that is ``dx``
-        without pre_norm), for the forward step that last ran.  The half must still hold that
+        stream) the gradients of the logits (``dlogits``), of the experts' weights (``dw``: expert
+        e's in block ``slot_maps[half][e]``; an expert without a slot had no tokens, and its gradient
+        is zero; a block whose slot no expert has holds zeros) and of the rows they saw (``dxn``; that is
+        ``dx`` without pre_norm), for the forward step that last ran.  The half must still hold that
         step's experts; it is released again when the weights have been read."""
         cfg, cs = self.cfg, self.compute_stream
         if not self.training:
@@ -407,6 +408,8 @@ class MoELayer:
         B.moe_grouped_swiglu_backward(self.x_perm, self.dy_perm, self.offsets, self.R, cfg.E, cfg.H,
                                       cfg.I, self.dt, self.wbufs[half], self.ws_backward,
                                       self.ws_backward.numel(), self.dx_perm, self.dw, self.status, cs)
+        # before the half is released: the next fill writes the slot map
+        B.moe_clear_unmapped(self.wbufs[half], self.dw, cs)
         B.moe_event_record(self.free[half], cs)
         B.moe_permute_backward(self.dx_perm, self.row_of, cfg.T, cfg.k, cfg.H, self.dt, self.dxn, cs)
 

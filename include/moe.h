@@ -463,7 +463,8 @@ int moe_grouped_swiglu_backward_workspace_size(int R, int E, int H, int I, moe_d
  *   dx_perm device [R][H] dtype; may be NULL (only the weights are trained)
  *   dw      device, n_slots expert blocks laid out as w's: the gradient of the expert in slot s
  *           is written (not added) at dw + s * expert_bytes, zeros for an expert without rows;
- *           blocks of slots that no expert maps to keep what they held.  No two experts may
+ *           blocks of slots that no expert maps to keep what they held (moe_clear_unmapped
+ *           clears them).  No two experts may
  *           share a slot.  May be NULL (frozen experts).  Not both dx_perm and dw NULL.
  *   status  device i32, may be NULL (MOE_STATUS_EXPERT_ABSENT when an expert with rows has no
  *           slot in [0, n_slots): its rows of dx_perm are left unwritten)
@@ -477,6 +478,16 @@ int moe_grouped_swiglu_backward(const void* x_perm, const void* dy_perm, const i
                                 int R, int E, int H, int I, moe_dtype dtype, const moe_wbuf* w,
                                 void* ws, size_t ws_bytes, void* dx_perm, void* dw,
                                 int32_t* status, moe_stream_t stream);
+
+/*
+ * moe_clear_unmapped -- zeros for the expert blocks of dw (n_slots blocks laid out as w's) whose slot
+ * no expert of w->slot_of maps to.  After moe_grouped_swiglu_backward on the same w and dw every
+ * block then holds the gradient of what its slot holds, whichever experts earlier steps had there.
+ *   w   merged buffer (base is not read; expert_bytes a multiple of 4); dw device, aligned to 4
+ * Errors: MOE_ERR_ARG for null pointers or a bad buffer; MOE_ERR_UNSUPPORTED for more than MOE_MAX_E
+ * experts, an unaligned dw, or sizes whose launch would pass 2^32 threads.
+ */
+int moe_clear_unmapped(const moe_wbuf* w, void* dw, moe_stream_t stream);
 
 /*
  * Multi-layer pipeline helpers (the block between two MoE layers).  The

@@ -149,3 +149,16 @@ def test_grouped_swiglu_backward(B):
     refused(B, W, f, *but((10, need - 1)))
     refused(B, W, f, *but((9, None)))
     refused(B, A, B.moe_grouped_swiglu_backward_workspace_size, 8, 0, 16, 8, B.MOE_BF16)
+
+
+def test_clear_unmapped(B):
+    A, U = B.MOE_ERR_ARG, B.MOE_ERR_UNSUPPORTED
+    f = B.moe_clear_unmapped
+    for code, buf, dw in [
+            (A, (P, 96, 4, 4, None), P), (A, (P, 96, 4, 4, P), None), (A, (P, 0, 4, 4, P), P),
+            (A, (P, 98, 4, 4, P), P), (A, (P, 96, -1, 4, P), P), (A, (P, 96, 4, 0, P), P),
+            (U, (P, 96, 4, 1025, P), P), (U, (P, 96, 4, 4, P), P + 2),
+            (U, (P, 96, 1 << 25, 4, P), P), (U, (P, 1 << 45, 4, 4, P), P),       # over 2^32 threads
+            (U, (P, (1 << 63) - 4, (1 << 31) - 1, 4, P), P)]:
+        refused(B, code, f, B.wbuf(*buf), dw)
+    f(B.wbuf(None, 96, 0, 4, P), None)                                           # no slots
