@@ -385,7 +385,7 @@ BackwardShape backward_shape(int T, int H) {
   b.nv = H <= kMaxBackwardH / 2 ? 1 : 2;
   b.waves = ceil_div(H, b.nv * kWave * kVec);
   b.groups = std::max(1, kMaxWaves / b.waves);
-  b.blocks = std::min(kPartials, ceil_div(T, b.groups));
+  b.blocks = static_cast<int>(std::min<int64_t>(kPartials, ceil_div64(T, b.groups)));
   return b;
 }
 
@@ -399,13 +399,13 @@ int launch_norm(const void* x, const float* gamma, const float* beta, int T, int
   const int waves = ceil_div(H, NV * kWave * kVec), rows = waves == 1 ? 4 : 1;
   // as many blocks as the CUs hold at once (16 waves a CU at the registers of KEEP); when that is
   // every row, KEEP has nothing to keep for, and its registers only take waves from the CU
-  const int all = ceil_div(T, rows), most = kCus * std::max(1, 16 / (waves * rows));
+  const int64_t all = ceil_div64(T, rows), most = kCus * std::max(1, 16 / (waves * rows));
   const bool keep = NV <= 2 && all > 2 * most;
-  const int blocks = keep ? std::min(all, most) : all;
+  const int64_t blocks = keep ? most : all;
   auto kernel = H % kVec == 0
                     ? (keep ? norm_kernel<E, NV, NV <= 2, false> : norm_kernel<E, NV, false, false>)
                     : (keep ? norm_kernel<E, NV, NV <= 2, true> : norm_kernel<E, NV, false, true>);
-  hipLaunchKernelGGL(kernel, dim3(blocks), dim3(waves * rows * kWave), 0, s,
+  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(blocks)), dim3(waves * rows * kWave), 0, s,
                      static_cast<const E*>(x), gamma, beta, T, H, waves, eps, static_cast<E*>(y), mean,
                      rstd);
   MOE_LAUNCH_CHECK("moe_layer_norm: launch");

@@ -407,10 +407,11 @@ extern "C" int moe_permute_backward(const void* dx_perm, const int32_t* row_of, 
   // short rows: 256 threads hold several tokens; long ones: the row's waves in blocks of up to 8
   const int tokens = pieces < kWave ? 256 / pieces : 1;
   const int waves = ceil_div(pieces, kWave), across = ceil_div(waves, 8);
-  const dim3 grid(ceil_div(T, tokens), tokens > 1 ? 1 : across);
   const dim3 block(tokens > 1 ? 256 : ceil_div(waves, across) * kWave);
-  if (too_many(grid.x, block.x))
+  const int64_t blocks = ceil_div64(T, tokens);
+  if (too_many(blocks, block.x))
     return fail(MOE_ERR_UNSUPPORTED, "moe_permute_backward: T=%d too large at H=%d", T, H);
+  const dim3 grid(static_cast<unsigned>(blocks), tokens > 1 ? 1 : across);
   if (T == 0) return MOE_OK;
   if (!dx_perm || !row_of || !dx) return fail(MOE_ERR_ARG, "moe_permute_backward: null pointer");
   hipStream_t s = as_stream(stream);

@@ -183,7 +183,8 @@ extern "C" int moe_route_backward(const int32_t* topk_idx, const float* topk_w, 
     return fail(MOE_ERR_ARG, "moe_route_backward: bad sizes T=%d E=%d k=%d", T, E, k);
   if (E > MOE_MAX_E || k > MOE_MAX_K)
     return fail(MOE_ERR_UNSUPPORTED, "moe_route_backward: E=%d or k=%d above the limits", E, k);
-  if (too_many(ceil_div(T, kRouteWaves), kRouteWaves * kWave))
+  const int64_t blocks = ceil_div64(T, kRouteWaves);
+  if (too_many(blocks, kRouteWaves * kWave))
     return fail(MOE_ERR_UNSUPPORTED, "moe_route_backward: T=%d too large", T);
   if (T == 0) return MOE_OK;
   if (!topk_idx || !topk_w || !dtopk_w || !dlogits)
@@ -191,7 +192,7 @@ extern "C" int moe_route_backward(const int32_t* topk_idx, const float* topk_w, 
   hipStream_t s = as_stream(stream);
   const bool wide = E % 4 == 0 && reinterpret_cast<uintptr_t>(dlogits) % 16 == 0;
   hipLaunchKernelGGL(wide ? route_backward_kernel<true> : route_backward_kernel<false>,
-                     dim3(ceil_div(T, kRouteWaves)), dim3(kRouteWaves * kWave),
+                     dim3(static_cast<unsigned>(blocks)), dim3(kRouteWaves * kWave),
                      kRouteWaves * E * sizeof(float), s, topk_idx, topk_w, dtopk_w, T, E, k, dlogits,
                      status);
   MOE_LAUNCH_CHECK("moe_route_backward: launch");

@@ -151,6 +151,20 @@ def test_grouped_swiglu_backward(B):
     refused(B, A, B.moe_grouped_swiglu_backward_workspace_size, 8, 0, 16, 8, B.MOE_BF16)
 
 
+def test_sizes_up_to_the_largest_int(B):
+    """Counts of workgroups stay exact up to T = 2^31 - 1."""
+    U, last = B.MOE_ERR_UNSUPPORTED, (1 << 31) - 1
+    for T in (last, last - 14):
+        # the partial rows of as many workgroups as smaller sizes have
+        for H in (1, 64, 8192, 16385):
+            assert B.moe_layer_norm_backward_workspace_size(T, H) == \
+                B.moe_layer_norm_backward_workspace_size(1 << 30, H)
+        for H in (9, 72, 4096):                                         # 2^32 threads and more
+            refused(B, U, B.moe_permute_backward, P, P, T, 1, H, B.MOE_BF16, P)
+        refused(B, U, B.moe_route_backward, P, P, P, T, 16, 1, P)
+        refused(B, U, B.moe_combine_backward, P, B.MOE_F32, P, P, P, T, 1, 8, B.MOE_F32, P, P)
+
+
 def test_clear_unmapped(B):
     A, U = B.MOE_ERR_ARG, B.MOE_ERR_UNSUPPORTED
     f = B.moe_clear_unmapped
