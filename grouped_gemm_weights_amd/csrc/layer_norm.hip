@@ -402,6 +402,8 @@ int launch_norm(const void* x, const float* gamma, const float* beta, int T, int
   const int64_t all = ceil_div64(T, rows), most = kCus * std::max(1, 16 / (waves * rows));
   const bool keep = NV <= 2 && all > 2 * most;
   const int64_t blocks = keep ? most : all;
+  if (too_many(blocks, waves * rows * kWave))
+    return fail(MOE_ERR_UNSUPPORTED, "moe_layer_norm: T=%d too large at H=%d", T, H);
   auto kernel = H % kVec == 0
                     ? (keep ? norm_kernel<E, NV, NV <= 2, false> : norm_kernel<E, NV, false, false>)
                     : (keep ? norm_kernel<E, NV, NV <= 2, true> : norm_kernel<E, NV, false, true>);

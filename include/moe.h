@@ -369,7 +369,8 @@ int moe_combine(const float* y_perm, const int32_t* row_of, const float* topk_w,
  * outputs: the same inputs give the same bits.  dtype is that of x, x_perm and the weights.
  * Every call may be captured into a HIP graph; captured calls that may run at the same time
  * need workspaces of their own.  Outputs must not alias inputs.  Sizes whose launch would pass
- * 2^32 threads (more than about 8 million tokens or rows) are MOE_ERR_UNSUPPORTED.
+ * 2^32 threads are MOE_ERR_UNSUPPORTED; no call has that limit below 4 million tokens or rows, except
+ * moe_grouped_swiglu_backward, whose launch also grows with H, I and E.
  */
 
 /*
@@ -379,7 +380,7 @@ int moe_combine(const float* y_perm, const int32_t* row_of, const float* topk_w,
  *   gamma, beta device f32[H]; beta may be NULL (no shift)
  *   mean, rstd  device f32[T] (written; what the backward pass reads); either may be NULL
  * Errors: MOE_ERR_ARG for null pointers, bad sizes or eps negative or NaN; MOE_ERR_UNSUPPORTED
- * for H > 2^26.  T = 0 is a no-op.
+ * for H > 2^26, or rows of more than 16384 elements by the millions (2^32 threads).  T = 0 is a no-op.
  */
 int moe_layer_norm(const void* x, const float* gamma, const float* beta, int T, int H, float eps,
                    moe_dtype dtype, void* y, float* mean, float* rstd, moe_stream_t stream);

@@ -165,6 +165,14 @@ def test_sizes_up_to_the_largest_int(B):
         refused(B, U, B.moe_combine_backward, P, B.MOE_F32, P, P, P, T, 1, 8, B.MOE_F32, P, P)
 
 
+def test_layer_norm_launches_of_long_rows(B):
+    """Rows of 16385 to 32768 elements have a workgroup of 9 to 16 waves each: 2^32 threads are
+    passed at T = 2^32 / 1024 and more."""
+    for T, H in ((1 << 22, 32768), ((1 << 32) // 576 + 1, 16385), ((1 << 31) - 1, 20000)):
+        for dtype in (B.MOE_F32, B.MOE_BF16):
+            refused(B, B.MOE_ERR_UNSUPPORTED, B.moe_layer_norm, P, P, P, T, H, 1e-5, dtype, P)
+
+
 def test_clear_unmapped(B):
     A, U = B.MOE_ERR_ARG, B.MOE_ERR_UNSUPPORTED
     f = B.moe_clear_unmapped
