@@ -73,6 +73,14 @@ __device__ __forceinline__ uint16_t f32_to_bf16(float f) {
   return __builtin_bit_cast(uint16_t, h);
 }
 
+// Between a wave's writes to LDS and its other lanes' reads of them (and before they are written
+// again): the compiler keeps the two in order.
+__device__ __forceinline__ void wave_lds_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 __device__ __forceinline__ void status_or(int32_t* status, int32_t bits) {
   if (status) atomicOr(status, bits);
 }

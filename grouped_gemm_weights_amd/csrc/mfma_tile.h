@@ -375,9 +375,7 @@ __device__ __forceinline__ void store_block(lds_char* smem, uint16_t* out, int64
     for (int v = 0; v < 4; ++v) {
       *reinterpret_cast<lds_u32x2*>(mine + (lane & 31) * PITCH + (j * 32 + lane_col(v)) * 2) = put(j, v);
     }
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  wave_lds_sync();
   const int c = (lane % LANES) * 8;
 #pragma unroll
   for (int i = 0; i < 32 / PER; ++i) {
@@ -385,9 +383,7 @@ __device__ __forceinline__ void store_block(lds_char* smem, uint16_t* out, int64
     const u32x4 d = *reinterpret_cast<lds_u32x4*>(mine + r * PITCH + c * 2);
     if (r < rows && c < cols) __builtin_nontemporal_store(d, reinterpret_cast<u32x4*>(out + r * ld + c));
   }
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  wave_lds_sync();
 }
 
 __device__ __forceinline__ u32x2 pack4(float a, float b, float c, float d) {

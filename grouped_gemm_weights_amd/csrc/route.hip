@@ -142,9 +142,9 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_backward_kernel(
   } else {
     for (int e = lane; e < E; e += kWave) row[e] = 0.f;
   }
-  __builtin_amdgcn_wave_barrier();
+  wave_lds_sync();
   if (first) row[id] = g;
-  __builtin_amdgcn_wave_barrier();
+  wave_lds_sync();
   if (WIDE) {
     for (int e = lane * 4; e < E; e += kWave * 4)
       __builtin_nontemporal_store(*reinterpret_cast<const f32x4*>(row + e), reinterpret_cast<f32x4*>(out + e));
