@@ -435,7 +435,6 @@ __global__ __launch_bounds__(256) void grads_f32_kernel(
 // so the workgroups that run together on an XCD share gm row panels and gn column panels in its L2.
 struct Order {
   int gm, gn, n_gn;  // tiles of a unit; units across
-  int blocks;        // a multiple of 8
 };
 
 __device__ __forceinline__ void place(const Order& o, int block, int* m, int* n) {
@@ -715,15 +714,15 @@ int run_f32(const Call& c, const float* x, const float* dy) {
   return launch(c, x, dy, dgu, h);
 }
 
+// blocks: a multiple of 8.
 Order make_order(int tr, int64_t mt, int64_t nt, int64_t* blocks) {
   // large tiles: up to 4 x 8 (32 CUs an XCD), the columns cut evenly, where that leaves every XCD a
   // few units, else single tiles
-  Order o{4, static_cast<int>(ceil_div64(nt, ceil_div64(nt, 8))), 0, 0};
+  Order o{4, static_cast<int>(ceil_div64(nt, ceil_div64(nt, 8))), 0};
   if (tr != 256 || ceil_div64(mt, o.gm) * ceil_div64(nt, o.gn) < 32) o.gm = o.gn = 1;
   o.n_gn = static_cast<int>(ceil_div64(nt, o.gn));
   const int64_t units = ceil_div64(mt, o.gm) * o.n_gn;
   *blocks = ceil_div64(units, 8) * 8 * o.gm * o.gn;
-  o.blocks = static_cast<int>(*blocks);
   return o;
 }
 
