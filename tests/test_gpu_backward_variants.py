@@ -34,16 +34,19 @@ def mixed(E, seed):
 
 EDGES = (1, 32, 33, 0, 64, 65, 128, 129, 192, 193, 255, 256, 257, 31, 300)
 FEW = tuple(int(c) for c in np.random.default_rng(2).integers(0, 6, 130))
+MANY = tuple(int(c) for c in np.random.default_rng(4).integers(0, 4, 1024))
 LARGE = [
     (EDGES, 1544, 1032),             # every row mode; depths that end inside a stage, ragged columns
     (mixed(90, 1), 264, 136),        # many experts, two column tiles and one
     (FEW, 520, 264),                 # a few rows each: units of 4 row tiles, the last of them ragged
     (mixed(64, 3), 2312, 72),        # ten column tiles: two units across, of five
     ((1025,), 8200, 4104),           # a weight gradient of several units each way
+    (FEW, 8, 24),                    # the narrowest rows
+    (MANY, 72, 40),                  # sixteen experts a lane in the tile search
 ]
 
 
-@pytest.mark.parametrize("counts,H,I", LARGE, ids=["edges", "mixed", "few", "wide", "one"])
+@pytest.mark.parametrize("counts,H,I", LARGE, ids=["edges", "mixed", "few", "wide", "one", "narrow", "many"])
 def test_grouped_swiglu_backward_large_tiles(counts, H, I):
     assert takes_large_tiles(counts, H, I)
     log(f"case experts backward {len(counts)} experts, {sum(counts)} rows, H={H} I={I} bf16, large tiles")

@@ -1,5 +1,5 @@
-"""The layer's training step on the GPU where the caller takes part in it, and where its
-expert set changes from step to step."""
+"""The layer's training step on the GPU where the caller takes part in it, where its
+expert set changes from step to step, and from halves stitched out of pages."""
 import pytest
 
 import test_gpu_backward as base
@@ -114,3 +114,31 @@ def test_clear_unmapped(words, E, slots, n_slots):
     for s in set(range(n_slots)) - set(slots):
         want[s * words:(s + 1) * words] = 0
     assert torch.equal(dw, want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("remote,chunks", [("all", 0), ("all", 3), ("device", 0), ("routed", 0),
+                                           ("routed", 3)])
+def test_training_step_from_stitched_halves(dtype, remote, chunks):
+    """Halves stitched from pages hold the same bytes as copied ones: the step and every gradient
+    agree bit for bit, block by expert, over several steps on both halves."""
+    size = dict(T=40, H=1024, I=1024)                    # whole pages: blocks of 6 and 12 MiB
+    cfg, L, dy = base.layer_case(dtype, True, stitched=True, **size)
+    cfg, M, _ = base.layer_case(dtype, True, **size)
+    log(f"case stitched training step {dtype} remote={remote} chunks={chunks}")
+    try:
+        for turn in range(3):
+            half = turn % 2
+            for step, how, n in ((L, remote, chunks), (M, "all", 0)):
+                step.set_inputs(synth.activations(cfg, turn), synth.logits(cfg, turn))
+                step.forward(half=half, remote=how, chunks=n)
+                step.backward(dy, half=half)
+                assert step.read_status() == 0
+            for name in ("y", "dx", "dlogits", "dgamma", "dbeta"):
+                assert torch.equal(getattr(L, name), getattr(M, name)), (turn, name)
+            assert torch.isfinite(L.dx).all() and L.dx.any()
+            for e, s in enumerate(L.slot_maps[half].tolist()):
+                assert torch.equal(L.dw[s], M.dw[e]) if s >= 0 else not M.dw[e].any(), (turn, e)
+    finally:
+        L.close()
+        M.close()
