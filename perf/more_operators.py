@@ -7,7 +7,7 @@ by expert (``moe_grouped_gemm``, its backward, and ``moe_grouped_gemm_mx`` on 8-
 dropout in front of the residual (``moe_dropout_add`` and its backward).
 
 8-bit rows are e4m3 values with one power-of-two scale for each 32 of them (a byte, the exponent
-plus 127); a row's scales are padded with zero bytes to whole words of four.
+plus 127); a row's scales are padded with zero bytes to a multiple of 16.
 
 ``listed()`` and ``draw()`` give cases, ``prepare()`` the inputs a program has in hand, ``run()``
 one pass through the operator: with ``own`` false its plain form in elementary torch operations,
@@ -107,8 +107,8 @@ def _dtype(name):
 
 
 def _pitch(cols):
-    """Bytes of a row's scales: one for each block, padded to whole words."""
-    return 4 * -(-cols // (4 * BLOCK))
+    """Bytes of a row's scales: one for each block, padded to a multiple of 16."""
+    return 16 * -(-cols // (16 * BLOCK))
 
 
 def _power(e, dtype=torch.float32):
@@ -201,11 +201,11 @@ def prepare(case, seed):
             q, s["xs"] = _to_8_bits(x)
             s["x"] = q.view(torch.uint8)
             # an expert's block: its matrix, then the matrix's scales
-            s["w"] = torch.zeros(E, -(-N * (K + _pitch(K)) // 16) * 16, dtype=torch.uint8, device="cuda")
+            s["w"] = torch.empty(E, N * (K + _pitch(K)), dtype=torch.uint8, device="cuda")
             for e in range(E):
                 q, ws = _to_8_bits(normal(N, K, scale=K ** -0.5))
                 s["w"][e, :N * K] = q.view(torch.uint8).view(-1)
-                s["w"][e, N * K:N * K + ws.numel()] = ws.view(-1)
+                s["w"][e, N * K:] = ws.view(-1)
         else:
             s["x"] = x
             s["w"] = torch.empty(E, N * K, dtype=_dtype(dt), device="cuda")
@@ -296,7 +296,7 @@ def _plain_product(s):
     if s["dtype"] == "mx":
         x = _from_8_bits(s["x"], s["xs"])[from_row]
         w = _from_8_bits(s["w"][:, :N * K].view(E, N, K),
-                         s["w"][:, N * K:N * (K + _pitch(K))].view(E, N, _pitch(K)))
+                         s["w"][:, N * K:].view(E, N, _pitch(K)))
     else:
         x, w = s["x"][from_row].float(), s["w"].float().view(E, N, K)
     x = x * keep
@@ -500,7 +500,7 @@ def exact(case, seed):
         if case["dtype"] == "mx":
             block = s["w"][e]
             x = _from_8_bits(s["x"][at], s["xs"][at], torch.float64)
-            w = _from_8_bits(block[:N * K].view(N, K), block[N * K:N * (K + _pitch(K))].view(N, -1),
+            w = _from_8_bits(block[:N * K].view(N, K), block[N * K:].view(N, -1),
                              torch.float64)
         else:
             x, w = d["x"][at], s["w"][e].double().view(N, K)
