@@ -43,6 +43,9 @@ EXPORTS = (
     "moe_combine_backward", "moe_permute_backward", "moe_route_backward",
     "moe_grouped_swiglu_backward_workspace_size", "moe_grouped_swiglu_backward",
     "moe_clear_unmapped",
+    "moe_mx_scale_pitch", "moe_mx_quantize", "moe_rms_norm", "moe_rms_norm_backward_workspace_size",
+    "moe_rms_norm_backward", "moe_grouped_gemm", "moe_grouped_gemm_backward", "moe_grouped_gemm_mx",
+    "moe_dropout_add", "moe_dropout_add_backward",
 )
 
 
@@ -68,7 +71,7 @@ def _load() -> ctypes.CDLL:
         raise ImportError(f"{LIB_PATH} is not built; run `python -m grouped_gemm_weights_amd.build`")
     lib = ctypes.CDLL(LIB_PATH)
     P, I, I64, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
-    F = ctypes.c_float
+    F, D = ctypes.c_float, ctypes.c_double
     PSZ = ctypes.POINTER(ctypes.c_size_t)
     sig = {
         "moe_route": [P, I, I, I, P, P, P, P],
@@ -108,6 +111,16 @@ def _load() -> ctypes.CDLL:
         "moe_grouped_swiglu_backward": [P, P, P, I, I, I, I, I, ctypes.POINTER(MoeWbuf), P, SZ, P, P,
                                         P, P],
         "moe_clear_unmapped": [ctypes.POINTER(MoeWbuf), P, P],
+        "moe_mx_scale_pitch": [I, PSZ],
+        "moe_mx_quantize": [P, I, I, I, I, P, P, P],
+        "moe_rms_norm": [P, P, P, I, I, F, I, P, P, P, P, P, P],
+        "moe_rms_norm_backward_workspace_size": [I, I, PSZ],
+        "moe_rms_norm_backward": [P, P, P, P, P, I, I, I, P, P, P, SZ, P],
+        "moe_grouped_gemm": [P, P, I, P, I, I, I, I, I, ctypes.POINTER(MoeWbuf), I64, I, P, P, P],
+        "moe_grouped_gemm_backward": [P, P, P, I, I, I, I, I, ctypes.POINTER(MoeWbuf), I64, P, P, P, P],
+        "moe_grouped_gemm_mx": [P, P, P, I, P, I, I, I, I, ctypes.POINTER(MoeWbuf), I64, I64, I, P, P, P],
+        "moe_dropout_add": [P, I, P, I64, D, P, I, P, P],
+        "moe_dropout_add_backward": [P, I, I64, D, P, I, P, P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -314,6 +327,69 @@ def moe_grouped_swiglu_backward(x_perm, dy_perm, offsets, R, E, H, I, dtype, w: 
 
 def moe_clear_unmapped(w: MoeWbuf, dw, stream=None):
     _check("moe_clear_unmapped", lib.moe_clear_unmapped(ctypes.byref(w), ptr(dw), stream_handle(stream)))
+
+
+def moe_mx_scale_pitch(cols) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_mx_scale_pitch", lib.moe_mx_scale_pitch(cols, ctypes.byref(n)))
+    return n.value
+
+
+def moe_mx_quantize(x, rows, cols, dtype, swiglu, q, scales, stream=None):
+    _check("moe_mx_quantize", lib.moe_mx_quantize(ptr(x), rows, cols, dtype, swiglu, ptr(q), ptr(scales),
+                                                  stream_handle(stream)))
+
+
+def moe_rms_norm(x, residual, gamma, T, H, eps, dtype, sum=None, y=None, q=None, scales=None, rstd=None,
+                 stream=None):
+    _check("moe_rms_norm", lib.moe_rms_norm(ptr(x), ptr(residual), ptr(gamma), T, H, eps, dtype, ptr(sum),
+                                            ptr(y), ptr(q), ptr(scales), ptr(rstd), stream_handle(stream)))
+
+
+def moe_rms_norm_backward_workspace_size(T, H) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_rms_norm_backward_workspace_size",
+           lib.moe_rms_norm_backward_workspace_size(T, H, ctypes.byref(n)))
+    return n.value
+
+
+def moe_rms_norm_backward(dy, dsum, s, gamma, rstd, T, H, dtype, dx, dgamma, ws, ws_bytes, stream=None):
+    _check("moe_rms_norm_backward",
+           lib.moe_rms_norm_backward(ptr(dy), ptr(dsum), ptr(s), ptr(gamma), ptr(rstd), T, H, dtype, ptr(dx),
+                                     ptr(dgamma), ptr(ws), ws_bytes, stream_handle(stream)))
+
+
+def moe_grouped_gemm(x, src_of, top_k, offsets, R, E, K, N, dtype, w: MoeWbuf, w_off, y_dtype, y, status=None,
+                     stream=None):
+    _check("moe_grouped_gemm",
+           lib.moe_grouped_gemm(ptr(x), ptr(src_of), top_k, ptr(offsets), R, E, K, N, dtype, ctypes.byref(w),
+                                w_off, y_dtype, ptr(y), ptr(status), stream_handle(stream)))
+
+
+def moe_grouped_gemm_backward(x, dy, offsets, R, E, K, N, dtype, w: MoeWbuf, w_off, dx, dw, status=None,
+                              stream=None):
+    _check("moe_grouped_gemm_backward",
+           lib.moe_grouped_gemm_backward(ptr(x), ptr(dy), ptr(offsets), R, E, K, N, dtype, ctypes.byref(w),
+                                         w_off, ptr(dx), ptr(dw), ptr(status), stream_handle(stream)))
+
+
+def moe_grouped_gemm_mx(x, x_scales, src_of, top_k, offsets, R, E, K, N, w: MoeWbuf, w_off, s_off, y_dtype, y,
+                        status=None, stream=None):
+    _check("moe_grouped_gemm_mx",
+           lib.moe_grouped_gemm_mx(ptr(x), ptr(x_scales), ptr(src_of), top_k, ptr(offsets), R, E, K, N,
+                                   ctypes.byref(w), w_off, s_off, y_dtype, ptr(y), ptr(status),
+                                   stream_handle(stream)))
+
+
+def moe_dropout_add(x, x_dtype, residual, n, p, rng, dtype, out, stream=None):
+    _check("moe_dropout_add", lib.moe_dropout_add(ptr(x), x_dtype, ptr(residual), n, p, ptr(rng), dtype, ptr(out),
+                                                  stream_handle(stream)))
+
+
+def moe_dropout_add_backward(dout, dtype, n, p, rng, x_dtype, dx, stream=None):
+    _check("moe_dropout_add_backward",
+           lib.moe_dropout_add_backward(ptr(dout), dtype, n, p, ptr(rng), x_dtype, ptr(dx),
+                                        stream_handle(stream)))
 
 
 def moe_dense_gemm(x, w, M, N, K, out, stream=None):

@@ -1,0 +1,127 @@
+// moe_dropout_add and its gradient: dropout with a mask that is computed from a counter and never
+// stored, and the residual's addition.
+//
+//   out_i = residual_i + keep_i x_i / (1 - p),     dx_i = keep_i dout_i / (1 - p)
+//
+// keep_i: Philox4x32-10 (Salmon, Moraes, Dror and Shaw, "Parallel random numbers: as easy as 1, 2, 3",
+// SC 2011) with the seed as its 64-bit key and (i / 4, step) as its 128-bit counter gives four 32-bit
+// words; element i takes word i % 4 and is kept where it is at least p 2^32.  Every element's word
+// depends on its index alone, so the mask is the same whatever the launch and in the backward pass.
+//
+// Bound by HBM; the ten rounds are 20 products of 32 by 32 bits for four elements, beside the loads of
+// the other waves.
+#include "mx.h"
+#include "rows.h"
+
+namespace moe {
+namespace {
+
+struct Words {
+  uint32_t w[4];
+};
+
+__device__ __forceinline__ Words philox(uint64_t seed, uint64_t step, uint64_t at) {
+  uint32_t c0 = static_cast<uint32_t>(at), c1 = static_cast<uint32_t>(at >> 32);
+  uint32_t c2 = static_cast<uint32_t>(step), c3 = static_cast<uint32_t>(step >> 32);
+  uint32_t k0 = static_cast<uint32_t>(seed), k1 = static_cast<uint32_t>(seed >> 32);
+#pragma unroll
+  for (int i = 0; i < 10; ++i) {
+    const uint64_t a = static_cast<uint64_t>(c0) * 0xD2511F53u, b = static_cast<uint64_t>(c2) * 0xCD9E8D57u;
+    c0 = static_cast<uint32_t>(b >> 32) ^ c1 ^ k0;
+    c1 = static_cast<uint32_t>(b);
+    c2 = static_cast<uint32_t>(a >> 32) ^ c3 ^ k1;
+    c3 = static_cast<uint32_t>(a);
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  return Words{{c0, c1, c2, c3}};
+}
+
+__device__ __forceinline__ float one(const uint16_t* p) { return bf16_to_f32(*p); }
+__device__ __forceinline__ float one(const float* p) { return *p; }
+__device__ __forceinline__ void put(uint16_t* p, float v) { *p = f32_to_bf16(v); }
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+
+// Eight elements a thread and turn.  out may be x or the residual itself: a thread has read its
+// elements before it writes them.
+template <typename X, typename O>
+__global__ __launch_bounds__(256) void dropout_kernel(const X* x, const O* res, int64_t n, uint32_t drop,
+                                                      float scale, const uint64_t* __restrict__ rng, O* out) {
+  const uint64_t seed = rng[0], step = rng[1];
+  const int64_t all = static_cast<int64_t>(gridDim.x) * 256;
+  for (int64_t u = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; u * kVec < n; u += all) {
+    const int64_t at = u * kVec;
+    const bool whole = at + kVec <= n;
+    Raw8<X> rx;
+    Raw8<O> rr;
+    float v[kVec], b[kVec];
+    if (whole) {
+      load_raw<true, false>(x + at, 0, kVec, rx);
+      load_raw<true, false>(res + (res ? at : 0), 0, res ? kVec : 0, rr);
+    }
+    const Words w[2] = {philox(seed, step, 2 * u), philox(seed, step, 2 * u + 1)};
+    if (whole) {
+      unpack<false>(rx, 0, kVec, v);
+      unpack<false>(rr, 0, kVec, b);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        v[i] = at + i < n ? one(x + at + i) : 0.f;
+        b[i] = res && at + i < n ? one(res + at + i) : 0.f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      // a dropped value counts for nothing, also where it is not finite
+      const float kept = w[i / 4].w[i % 4] >= drop ? v[i] * scale : 0.f;
+      v[i] = res ? kept + b[i] : kept;
+    }
+    if (whole) {
+      store8<true, false>(out + at, 0, kVec, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i)
+        if (at + i < n) put(out + at + i, v[i]);
+    }
+  }
+}
+
+template <typename X, typename O>
+void launch(const void* x, const void* res, int64_t n, double p, const uint64_t* rng, void* out, hipStream_t s) {
+  const int64_t blocks = std::min<int64_t>(ceil_div64(n, 256 * kVec), kCus * 64);
+  hipLaunchKernelGGL((dropout_kernel<X, O>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s,
+                     static_cast<const X*>(x), static_cast<const O*>(res), n,
+                     static_cast<uint32_t>(p * 4294967296.0), static_cast<float>(1.0 / (1.0 - p)), rng,
+                     static_cast<O*>(out));
+}
+
+int dropout(const char* who, const void* x, moe_dtype x_dtype, const void* res, int64_t n, double p,
+            const uint64_t* rng, moe_dtype dtype, void* out, moe_stream_t stream) {
+  if (n < 0 || !(p >= 0.0 && p < 1.0) || !is_dtype(x_dtype) || !is_dtype(dtype))
+    return fail(MOE_ERR_ARG, "%s: bad size n=%lld, p=%g or dtype", who, static_cast<long long>(n), p);
+  if (n == 0) return MOE_OK;
+  if (!x || !rng || !out) return fail(MOE_ERR_ARG, "%s: null pointer", who);
+  hipStream_t s = as_stream(stream);
+  if (x_dtype == MOE_F32) {
+    if (dtype == MOE_F32) launch<float, float>(x, res, n, p, rng, out, s);
+    else launch<float, uint16_t>(x, res, n, p, rng, out, s);
+  } else {
+    if (dtype == MOE_F32) launch<uint16_t, float>(x, res, n, p, rng, out, s);
+    else launch<uint16_t, uint16_t>(x, res, n, p, rng, out, s);
+  }
+  MOE_LAUNCH_CHECK(who);
+  return debug_check(MOE_OK, who, s, nullptr);
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" int moe_dropout_add(const void* x, moe_dtype x_dtype, const void* residual, int64_t n, double p,
+                               const uint64_t* rng, moe_dtype dtype, void* out, moe_stream_t stream) {
+  return moe::dropout("moe_dropout_add", x, x_dtype, residual, n, p, rng, dtype, out, stream);
+}
+
+extern "C" int moe_dropout_add_backward(const void* dout, moe_dtype dtype, int64_t n, double p,
+                                        const uint64_t* rng, moe_dtype x_dtype, void* dx, moe_stream_t stream) {
+  return moe::dropout("moe_dropout_add_backward", dout, dtype, nullptr, n, p, rng, x_dtype, dx, stream);
+}

@@ -16,30 +16,6 @@
 namespace moe {
 namespace {
 
-constexpr int kMaxWaves = 16;
-
-// The sum of 16 floats of LDS, in order: an entry per wave, zeros where there are fewer.
-__device__ __forceinline__ float sum16(const float* part) {
-  typedef float f32x4 __attribute__((ext_vector_type(4)));
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < kMaxWaves / 4; ++i) {
-    const f32x4 v = reinterpret_cast<const f32x4*>(part)[i];
-    s += (v[0] + v[1]) + (v[2] + v[3]);
-  }
-  return s;
-}
-
-// Sum of one value over the waves of a block that share a row.  `part` is 16 floats of LDS that no
-// other sum of the same barrier interval uses, zero past the block's waves.
-__device__ __forceinline__ float row_sum(float v, int waves, float* part) {
-  v = wave_sum(v);
-  if (waves == 1) return v;
-  if ((threadIdx.x & (kWave - 1)) == 0) part[threadIdx.x / kWave] = v;
-  __syncthreads();
-  return sum16(part);
-}
-
 // `waves` waves per row, each lane NV vectors of 8 elements: H <= waves * 64 * NV * 8.  Rows of one
 // wave go four to a block, each wave on its own.  A block (wave) takes every `step`-th row.  KEEP:
 // gamma and beta stay in registers from row to row (as fp32 they are twice a bf16 row and would

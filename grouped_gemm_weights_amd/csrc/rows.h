@@ -195,4 +195,28 @@ __device__ __forceinline__ float wave_sum(float v) {
 }
 #undef DPP
 
+constexpr int kMaxWaves = 16;
+
+// The sum of 16 floats of LDS, in order: an entry per wave, zeros where there are fewer.
+__device__ __forceinline__ float sum16(const float* part) {
+  typedef float f32x4 __attribute__((ext_vector_type(4)));
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMaxWaves / 4; ++i) {
+    const f32x4 v = reinterpret_cast<const f32x4*>(part)[i];
+    s += (v[0] + v[1]) + (v[2] + v[3]);
+  }
+  return s;
+}
+
+// Sum of one value over the waves of a block that share a row.  `part` is 16 floats of LDS that no
+// other sum of the same barrier interval uses, zero past the block's waves.
+__device__ __forceinline__ float row_sum(float v, int waves, float* part) {
+  v = wave_sum(v);
+  if (waves == 1) return v;
+  if ((threadIdx.x & (kWave - 1)) == 0) part[threadIdx.x / kWave] = v;
+  __syncthreads();
+  return sum16(part);
+}
+
 }  // namespace moe

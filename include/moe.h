@@ -491,6 +491,164 @@ int moe_grouped_swiglu_backward(const void* x_perm, const void* dy_perm, const i
 int moe_clear_unmapped(const moe_wbuf* w, void* dw, moe_stream_t stream);
 
 /*
+ * The block in 8 bits, products by expert, and what stands around the block.
+ *
+ * 8-bit rows ("mx") are the OCP microscaling format MXFP8 with e4m3 elements: 32 consecutive values
+ * of a row share a scale 2^s, kept as the byte s + 127, and are held as e4m3(v / 2^s).  A matrix of
+ * rows x cols is
+ *   q       uint8 [rows][cols], cols a multiple of 32
+ *   scales  uint8 [rows][pitch], pitch = moe_mx_scale_pitch(cols) = 16 * ceil(cols / 512): the bytes
+ *           of the row's blocks, then zeros (whoever fills scales by other means writes the zeros too)
+ * The quantisers here take the smallest s with max |v| <= 448 * 2^s, so that no value saturates; a
+ * block of zeros has scale byte 0.  A value that is not finite becomes NaN; its block's scale is that
+ * of the finite ones.  A decode step of an 8-bit block is
+ *   moe_rms_norm         x + residual -> sum, y (for the router), q and scales
+ *   moe_route, moe_permute (x_perm = NULL)
+ *   moe_grouped_gemm_mx  gathered by src_of: gate and up as one matrix of 2 I rows -> [R][2 I]
+ *   moe_mx_quantize      with swiglu -> q and scales [R][I]
+ *   moe_grouped_gemm_mx  down -> y_perm f32
+ *   moe_combine
+ * Statistics and sums are f32, outputs are rounded once, no call uses atomics on its outputs and the
+ * same inputs give the same bits.  Every call only enqueues and may be captured into a HIP graph;
+ * captured calls that may run at the same time need workspaces of their own.  Unless a call says
+ * otherwise, outputs must not overlap inputs.  Sizes whose launch would pass 2^32 threads are
+ * MOE_ERR_UNSUPPORTED.
+ */
+
+/* Bytes of the scales of a row of `cols` values. */
+int moe_mx_scale_pitch(int cols, size_t* bytes);
+
+/*
+ * moe_mx_quantize -- rows to 8 bits: v = x[r], or with swiglu = 1 (x has 2 cols columns, gate then up)
+ * v = silu(x[r][:cols]) * x[r][cols:].
+ *   x       device [rows][cols] dtype ([rows][2 cols] with swiglu); any alignment of one element
+ *   q, scales device, aligned to 16 bytes
+ * Errors: MOE_ERR_ARG for null pointers, bad sizes or swiglu not 0 or 1; MOE_ERR_UNSUPPORTED for cols not
+ * a multiple of 32 or above 2^26, an unaligned output, or about 2^32 units of 512 columns.  rows = 0 is
+ * a no-op.
+ */
+int moe_mx_quantize(const void* x, int rows, int cols, moe_dtype dtype, int swiglu, uint8_t* q,
+                    uint8_t* scales, moe_stream_t stream);
+
+/*
+ * moe_rms_norm -- the root-mean-square norm with the residual's addition: s[t] = x[t] + residual[t],
+ * rounded to dtype (s = x without a residual), rstd_t = 1 / sqrt(mean s[t]^2 + eps),
+ * y[t] = s[t] * rstd_t * gamma, and the same in 8 bits (from f32, not from y's rounding).
+ *   x, residual device [T][H] dtype; residual may be NULL
+ *   gamma     device f32[H]
+ *   sum       device [T][H] dtype (s: the stream after the addition); may be NULL, has to be without a
+ *             residual; may be x or the residual itself (the addition in place)
+ *   y         device [T][H] dtype; may be NULL when q is given
+ *   q, scales device, 8-bit rows of H (H a multiple of 32), aligned to 16 bytes; both or neither
+ *   rstd      device f32[T] (what the backward pass reads); may be NULL
+ * Errors: MOE_ERR_ARG for null pointers, bad sizes, eps negative or NaN, a sum without a residual, or one
+ * of q and scales; MOE_ERR_UNSUPPORTED for H > 2^26, q with H not a multiple of 32, or unaligned.
+ * T = 0 is a no-op.
+ */
+int moe_rms_norm(const void* x, const void* residual, const float* gamma, int T, int H, float eps,
+                 moe_dtype dtype, void* sum, void* y, uint8_t* q, uint8_t* scales, float* rstd,
+                 moe_stream_t stream);
+
+/* Workspace bytes moe_rms_norm_backward needs for dgamma (none without it). */
+int moe_rms_norm_backward_workspace_size(int T, int H, size_t* bytes);
+
+/*
+ * moe_rms_norm_backward -- the gradient of moe_rms_norm with respect to x (and to the residual, which is
+ * the same): with xh = s * rstd and a = dy * gamma,
+ *   dx = dsum + rstd * (a - xh * mean_h(a xh)),   dgamma = sum_t dy * xh.
+ *   dy      device [T][H] dtype, the gradient of y
+ *   dsum    device [T][H] dtype, what reaches s past the norm; may be NULL (none); dx may be dsum itself
+ *   s       device [T][H] dtype: the sum that moe_rms_norm wrote (x without a residual)
+ *   dx      device [T][H] dtype
+ *   dgamma  device f32[H] (overwritten; zeros for T = 0); may be NULL
+ *   ws      device workspace of moe_rms_norm_backward_workspace_size() bytes; may be NULL when dgamma is
+ * Errors: as moe_rms_norm, plus MOE_ERR_WORKSPACE when ws_bytes is too small.
+ */
+int moe_rms_norm_backward(const void* dy, const void* dsum, const void* s, const float* gamma,
+                          const float* rstd, int T, int H, moe_dtype dtype, void* dx, float* dgamma,
+                          void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * moe_grouped_gemm -- one product per expert over ragged rows: y[r] = x[r] W_e^T for the rows r of
+ * expert e (offsets[e] <= r < offsets[e + 1]), accumulated in f32 (MFMA).
+ *   x       device [R][K] dtype; or, with src_of (device i32[R], from moe_permute) not NULL, [ceil(R / top_k)][K]:
+ *           row r is x[src_of[r] / top_k] (zeros where that is no row of x)
+ *   offsets device i32[E+1] (from moe_permute)
+ *   w       merged buffer; W_e [N][K] dtype is read at w_off bytes of expert e's block, so a block may hold
+ *           other matrices too
+ *   y       device [R][N] y_dtype (MOE_F32 for MOE_F32 operands)
+ *   status  device i32, may be NULL (MOE_STATUS_EXPERT_ABSENT when an expert with rows has no slot in
+ *           [0, n_slots): its rows of y are left unwritten)
+ * Rows of y at or past offsets[E] are left as they were.
+ * Errors: MOE_ERR_ARG for null pointers or sizes that disagree with w; MOE_ERR_UNSUPPORTED for E > MOE_MAX_E,
+ * K or N > 2^20, a matrix of 2^30 bytes or more, a gathered x of 2^31 bytes or more, (MOE_BF16) K or N
+ * not a multiple of 8, or pointers, w_off or expert_bytes not aligned to 16 bytes (MOE_F32: to 4).
+ * R = 0 is a no-op.
+ */
+int moe_grouped_gemm(const void* x, const int32_t* src_of, int top_k, const int32_t* offsets, int R,
+                     int E, int K, int N, moe_dtype dtype, const moe_wbuf* w, int64_t w_off,
+                     moe_dtype y_dtype, void* y, int32_t* status, moe_stream_t stream);
+
+/*
+ * moe_grouped_gemm_backward -- its gradient, for x that is not gathered (moe_permute_backward gathers
+ * dx back to the tokens): dx[r] = dy[r] W_e,  dW_e = sum_r dy[r]^T x[r].
+ *   x, dy   device [R][K] and [R][N] dtype
+ *   dx      device [R][K] dtype; may be NULL (only the weights are trained)
+ *   dw      device, n_slots expert blocks laid out as w's: dW_e is written (not added) at w_off of
+ *           the block of its expert's slot, zeros for an expert without rows; the rest of a block, and
+ *           blocks that no expert maps to, keep what they held (moe_clear_unmapped).  No two experts may
+ *           share a slot.  May be NULL (frozen experts).  Not both dx and dw NULL.
+ *   status  as moe_grouped_gemm
+ * Errors: as moe_grouped_gemm.  With R = 0 only dw is written.
+ */
+int moe_grouped_gemm_backward(const void* x, const void* dy, const int32_t* offsets, int R, int E, int K,
+                              int N, moe_dtype dtype, const moe_wbuf* w, int64_t w_off, void* dx,
+                              void* dw, int32_t* status, moe_stream_t stream);
+
+/*
+ * moe_grouped_gemm_mx -- moe_grouped_gemm on 8-bit rows and weights: W_e's elements [N][K] are read at
+ * w_off of expert e's block and its scales [N][moe_mx_scale_pitch(K)] at s_off.  f32 outputs, and those of
+ * few rows an expert, are f32 sums of exact products (the values expanded to bf16, which holds them).
+ * bf16 outputs of many rows come from the 8-bit MFMA, which adds eight consecutive products at once, each
+ * cut below 2^-13 of the largest: in the 2-norm about 3e-5 of the result, a sixtieth of bf16's rounding.
+ *   x, x_scales device, 8-bit rows of K ([R], or with src_of [ceil(R / top_k)])
+ *   other arguments as moe_grouped_gemm
+ * Errors: as moe_grouped_gemm; MOE_ERR_UNSUPPORTED for K not a multiple of 32 or N not one of 8, or
+ * pointers, w_off, s_off or expert_bytes not aligned to 16 bytes.
+ */
+int moe_grouped_gemm_mx(const uint8_t* x, const uint8_t* x_scales, const int32_t* src_of, int top_k,
+                        const int32_t* offsets, int R, int E, int K, int N, const moe_wbuf* w,
+                        int64_t w_off, int64_t s_off, moe_dtype y_dtype, void* y, int32_t* status,
+                        moe_stream_t stream);
+
+/*
+ * moe_dropout_add -- dropout and the residual's addition, with a mask that is never stored:
+ *   out[i] = residual[i] + (keep_i ? x[i] / (1 - p) : 0),  i < n.
+ * keep_i: Philox4x32-10 with rng[0] (the seed) as key and (i / 4, rng[1] (the step)) as counter gives
+ * four 32-bit words; i is kept where word i % 4 is at least floor(p * 2^32).  The mask depends on i, the
+ * seed and the step alone.  rng is read on the device when the call runs, so a captured graph draws a
+ * new mask on each replay if the program changes the step in between.
+ *   x        device [n] x_dtype
+ *   residual device [n] dtype; may be NULL (nothing is added)
+ *   p        in [0, 1)
+ *   rng      device u64[2]
+ *   out      device [n] dtype; may be x (of the same type) or the residual itself
+ * Any alignment of one element (rng: 8 bytes).  A dropped x counts for nothing, also where it is not finite.
+ * Errors: MOE_ERR_ARG for null pointers, n < 0, p outside [0, 1) or NaN, or a bad dtype.  n = 0 is a no-op.
+ */
+int moe_dropout_add(const void* x, moe_dtype x_dtype, const void* residual, int64_t n, double p,
+                    const uint64_t* rng, moe_dtype dtype, void* out, moe_stream_t stream);
+
+/*
+ * moe_dropout_add_backward -- its gradient with respect to x: dx[i] = keep_i ? dout[i] / (1 - p) : 0 with
+ * the same rng (the residual's gradient is dout itself).
+ *   dout device [n] dtype; dx device [n] x_dtype; dx may be dout itself when the types are the same
+ * Errors: as moe_dropout_add.
+ */
+int moe_dropout_add_backward(const void* dout, moe_dtype dtype, int64_t n, double p, const uint64_t* rng,
+                             moe_dtype x_dtype, void* dx, moe_stream_t stream);
+
+/*
  * Multi-layer pipeline helpers (the block between two MoE layers).  The
  * explainer's prefetch-schedule panel hides the fetch of layer l+1's remote
  * experts behind layer l's MoE block and layer l+1's attention block; a
