@@ -37,31 +37,56 @@ struct Tile {
 // Tile m of the list that cuts each expert's rows into tiles of TR, expert by expert, leaving out
 // experts without a slot in the merged buffer (a slot outside it is treated as absent, never
 // read; `report`: their status bit is set).  False past the last tile.  Wave-uniform.
-template <int TR>
+// LARGE_FIRST: tiles of more than TR / 2 rows come before the others, so that what the last CUs wait
+// for is a small one.
+template <int TR, bool LARGE_FIRST = false>
 __device__ __forceinline__ bool find_tile(const Experts& x, int m, bool report, Tile* t) {
   const int lane = threadIdx.x & (kWave - 1);
   const int per = (x.E + kWave - 1) / kWave;  // experts of a lane
   const int e0 = min(lane * per, x.E), e1 = min(e0 + per, x.E);
-  int n = 0, cnt = 0, lo = 0, slot = 0;
+  // of an expert's `cnt` rows: tiles of the first kind, and whether its last tile is of the second
+  const auto first_kind = [](int cnt) { return LARGE_FIRST ? (cnt + TR / 2 - 1) / TR : (cnt + TR - 1) / TR; };
+  const auto second_kind = [](int cnt) { return LARGE_FIRST && cnt % TR > 0 && cnt % TR <= TR / 2 ? 1 : 0; };
+  int n = 0, n2 = 0, cnt = 0, lo = 0, slot = 0;
   for (int e = e0; e < e1; ++e) {
     cnt = expert_rows(x, e, &lo);
     slot = x.slot_of[e];  // unconditional: it is on its way together with the offsets
-    if (slot >= 0 && slot < x.n_slots) n += (cnt + TR - 1) / TR;
-    else if (report && cnt > 0) status_or(x.status, MOE_STATUS_EXPERT_ABSENT);
+    if (slot >= 0 && slot < x.n_slots) {
+      n += first_kind(cnt);
+      n2 += second_kind(cnt);
+    } else if (report && cnt > 0) {
+      status_or(x.status, MOE_STATUS_EXPERT_ABSENT);
+    }
   }
-  const int end = wave_scan(n);  // tiles up to and with this lane's experts
+  int end = wave_scan(n);  // tiles up to and with this lane's experts
+  bool second = false;
+  if constexpr (LARGE_FIRST) {
+    const int all = __builtin_amdgcn_readlane(end, kWave - 1);
+    second = m >= all;
+    if (second) {
+      m -= all;
+      n = n2;
+      end = wave_scan(n);
+    }
+  }
   const uint64_t mine = __ballot(m >= end - n && m < end);
   if (mine == 0) return false;
-  int left = m - (end - n), row0 = lo + left * TR, rows = min(TR, cnt - left * TR);
-  if (per > 1) {
+  int left = m - (end - n);  // of this lane's tiles
+  int row0 = lo, rows = cnt;
+  const auto cut = [&](int i) {
+    row0 = lo + i * TR;
+    rows = min(TR, cnt - i * TR);
+  };
+  if (per == 1) {
+    cut(second ? cnt / TR : left);
+  } else {
     for (int e = e0; e < e1; ++e) {
       cnt = expert_rows(x, e, &lo);
       const int s = x.slot_of[e];
       if (s < 0 || s >= x.n_slots) continue;
-      const int tiles = (cnt + TR - 1) / TR;
+      const int tiles = second ? second_kind(cnt) : first_kind(cnt);
       if (left >= 0 && left < tiles) {
-        row0 = lo + left * TR;
-        rows = min(TR, cnt - left * TR);
+        cut(second ? cnt / TR : left);
         slot = s;
       }
       left -= tiles;
@@ -404,14 +429,14 @@ __device__ __forceinline__ void rows_tile(const Tile& t, int n0, const uint16_t*
 }
 
 // The same for tile (m, n) of the list; B of the tile's expert starts at b_off of its block.
-template <int TR, bool B_ROWS = false, typename O>
+template <int TR, bool B_ROWS = false, bool LARGE_FIRST = false, typename O>
 __device__ __forceinline__ void rows_product(const Experts& x, int m, int n, bool report,
                                              const uint16_t* A, int lda, const char* wbase,
                                              int64_t expert_bytes, int64_t b_off, int N, int K, O* C,
                                              lds_char* smem, Source src = {}) {
   const int n0 = n * tile_columns(TR, false);
   Tile t;
-  if (n0 >= N || !find_tile<TR>(x, m, report, &t)) return;
+  if (n0 >= N || !find_tile<TR, LARGE_FIRST>(x, m, report, &t)) return;
   const uint16_t* B = reinterpret_cast<const uint16_t*>(wbase + t.slot * expert_bytes + b_off);
   by_rows<TR>(t.rows, [&](auto mi) {
     rows_tile<TR, decltype(mi)::value, B_ROWS>(t, n0, A, lda, src, B, N, K, C, smem);

@@ -9,8 +9,19 @@
 //           to MFMA operands (no LDS), the depth split over the block's waves; bound by weight bytes.
 //   tile    256 x 256 (64 x 64) tiles through LDS (mfma_tile.h, mx_tile.h); bound by the MFMA pipes.
 #include "expert_tiles.h"
-#include "mx_tile.h"
+#include "row_tile.h"
 
+#ifndef NTW
+#define NTW false
+#endif
+#ifndef D1
+#define D1 4
+#define D2 3
+#define D4 2
+#endif
+#ifndef OCC
+#define OCC
+#endif
 namespace moe {
 namespace {
 
@@ -109,7 +120,7 @@ struct Operands {
 
 // Tiles of 16 MF rows by 64 columns.  D: chunks in flight per wave.
 template <bool MX, int MF, int D, typename O>
-__global__ __launch_bounds__(256) void stream_kernel(Experts ex, Source src, const char* __restrict__ x,
+__global__ __launch_bounds__(256 OCC) void stream_kernel(Experts ex, Source src, const char* __restrict__ x,
                                                      const uint8_t* __restrict__ xs, Weights w, int K, int N,
                                                      int col_blocks, O* __restrict__ y) {
   constexpr int NF = kStreamCols / 16;
@@ -122,7 +133,7 @@ __global__ __launch_bounds__(256) void stream_kernel(Experts ex, Source src, con
   const char* block = w.base + t.slot * w.expert_bytes;
   const bool gather = src.src_of;
   Stream<MX, MF, false> a;
-  Stream<MX, NF, true> b;
+  Stream<MX, NF, NTW> b;
   a.init(gather ? x : x + t.row0 * row_bytes, row_bytes, gather ? xs : xs + t.row0 * pitch, pitch,
          [&](int r) { return r >= t.rows ? -1 : gather ? src.at(t.row0 + r) : r; });
   b.init(block + w.off + n0 * row_bytes, row_bytes,
@@ -184,16 +195,6 @@ __global__ __launch_bounds__(256) void stream_kernel(Experts ex, Source src, con
 // tiles
 // ---------------------------------------------------------------------------
 
-template <int TR, typename O>
-TILE_KERNEL product_kernel(Experts ex, Source src, const uint16_t* __restrict__ x, Weights w, int K, int N,
-                           Order order, O* __restrict__ y) {
-  extern __shared__ __attribute__((aligned(1024))) char smem[];
-  int m, n;
-  place(order, blockIdx.x, &m, &n);
-  rows_product<TR, true>(ex, m, n, m == 0 && n == 0, x, K, w.base, w.expert_bytes, w.off, N, K, y, (lds_char*)smem,
-                         src);
-}
-
 template <int TR>
 __global__ __launch_bounds__(256) void product_f32_kernel(Experts ex, Source src, const float* __restrict__ x,
                                                           Weights w, int K, int N, int col_blocks,
@@ -203,41 +204,45 @@ __global__ __launch_bounds__(256) void product_f32_kernel(Experts ex, Source src
                              w.expert_bytes, w.off, N, K, y, lds, src);
 }
 
-template <int MI, typename O>
-__device__ __forceinline__ void mx_tile(const Tile& t, int n0, const Source& src, const uint8_t* x, const uint8_t* xs,
-                                        const uint8_t* B, const uint8_t* bs, int K, int N, O* y, lds_char* smem) {
+template <Kind KIND, int MI, typename O>
+__device__ __forceinline__ void row_tile(const Tile& t, int n0, const Source& src, const char* x, const uint8_t* xs,
+                                         const char* B, const uint8_t* bs, int K, int N, O* y, lds_char* smem) {
   using S = TileShape<256, MI, false>;
-  const int64_t pitch = mx_pitch(K);
+  const int bytes = K * value_bytes(KIND);
   const bool gather = src.src_of;
   const auto row = [&](int r) { return r >= t.rows ? -1 : gather ? src.at(t.row0 + r) : r; };
   const auto col = [&](int c) { return n0 + c < N ? c : -1; };
-  // pairs of 8-bit values as the 16-bit ones of a bf16 tile
-  Operand<false, S::ROWS> oa;
-  Operand<false, S::TN> ob;
-  oa.init(reinterpret_cast<const uint16_t*>(gather ? x : x + static_cast<int64_t>(t.row0) * K), K / 2, K / 2, row);
-  ob.init(reinterpret_cast<const uint16_t*>(B + static_cast<int64_t>(n0) * K), K / 2, K / 2, col);
+  RowOperand<S::ROWS> oa;
+  RowOperand<S::TN> ob;
+  oa.init(gather ? x : x + static_cast<int64_t>(t.row0) * bytes, bytes, row);
+  ob.init(B + static_cast<int64_t>(n0) * bytes, bytes, col);
   ScaleRows sa, sb;
-  sa.init(gather ? xs : xs + t.row0 * pitch, pitch, row);
-  sb.init(bs + n0 * pitch, pitch, col);
+  if constexpr (KIND != Kind::kBf16) {
+    const int64_t pitch = mx_pitch(K);
+    sa.init(gather ? xs : xs + t.row0 * pitch, pitch, row);
+    sb.init(bs + n0 * pitch, pitch, col);
+  }
   floatx16 acc[S::MW][S::NJ];
-  MxProduct<MI> p{oa, ob, sa, sb, acc};
-  p.run(K, smem);
+  RowProduct<KIND, MI> p{oa, ob, sa, sb, acc};
+  p.run(bytes, smem);
   store_tile<256, MI>(acc, smem, y + static_cast<int64_t>(t.row0) * N + n0, N, t.rows, N - n0);
 }
 
-template <typename O>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void mx_kernel(
-    Experts ex, Source src, const uint8_t* __restrict__ x, const uint8_t* __restrict__ xs, Weights w, int K, int N,
+template <Kind KIND, typename O>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void row_kernel(
+    Experts ex, Source src, const char* __restrict__ x, const uint8_t* __restrict__ xs, Weights w, int K, int N,
     Order order, O* __restrict__ y) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   int m, n;
   place(order, blockIdx.x, &m, &n);
   const int n0 = n * 256;
   Tile t;
-  if (n0 >= N || !find_tile<256>(ex, m, m == 0 && n == 0, &t)) return;
-  const uint8_t* block = reinterpret_cast<const uint8_t*>(w.base + t.slot * w.expert_bytes);
+  if (n0 >= N || !find_tile<256, true>(ex, m, m == 0 && n == 0, &t)) return;
+  const char* block = w.base + t.slot * w.expert_bytes;
   by_rows<256>(t.rows, [&](auto mi) {
-    mx_tile<decltype(mi)::value>(t, n0, src, x, xs, block + w.off, block + w.scales_off, K, N, y, (lds_char*)smem);
+    row_tile<KIND, decltype(mi)::value>(t, n0, src, x, xs, block + w.off,
+                                        reinterpret_cast<const uint8_t*>(block) + w.scales_off, K, N, y,
+                                        (lds_char*)smem);
   });
 }
 
@@ -263,7 +268,7 @@ TILE_KERNEL grads_kernel(Experts ex, const uint16_t* __restrict__ x, const uint1
   int64_t b = blockIdx.x;
   if (b < ranges.dx) {
     place(odx, static_cast<int>(b), &m, &n);
-    rows_product<TR>(ex, m, n, m == 0 && n == 0, dy, N, w.base, w.expert_bytes, w.off, K, N, dx, (lds_char*)smem);
+    rows_product<TR, false, true>(ex, m, n, m == 0 && n == 0, dy, N, w.base, w.expert_bytes, w.off, K, N, dx, (lds_char*)smem);
     return;
   }
   report_absent<TR>(ex, blockIdx.x == 0);
@@ -319,26 +324,29 @@ int launch_stream(const Call& c, const void* x, const uint8_t* xs, void* y) {
 template <bool MX, typename O>
 int run_stream(const Call& c, const void* x, const uint8_t* xs, void* y) {
   const int64_t per = c.ex.R / c.ex.E;
-  if (per <= 8) return launch_stream<MX, 1, 4, O>(c, x, xs, y);
-  if (per <= 24) return launch_stream<MX, 2, 3, O>(c, x, xs, y);
-  return launch_stream<MX, 4, 2, O>(c, x, xs, y);
+  if (per <= 8) return launch_stream<MX, 1, D1, O>(c, x, xs, y);
+  if (per <= 24) return launch_stream<MX, 2, D2, O>(c, x, xs, y);
+  return launch_stream<MX, 4, D4, O>(c, x, xs, y);
 }
 
 // Whether the stream kernel takes a product.
-bool few_rows(int R, int E) { return R <= 64 * static_cast<int64_t>(E); }
+#ifndef FEW
+#define FEW 64
+#endif
+bool few_rows(int R, int E) { return R <= FEW * static_cast<int64_t>(E); }
 
-template <int TR, typename O>
-int launch_product(const Call& c, const void* x, void* y) {
+template <Kind KIND, typename O>
+int run_rows(const Call& c, const void* x, const uint8_t* xs, void* y) {
   int64_t n;
-  const Order o = make_order(TR, max_tiles(c.ex.R, c.ex.E, TR), ceil_div(c.N, tile_columns(TR, false)), &n);
-  return launch_tiles(c.who, product_kernel<TR, O>, n, tile_lds(TR, false), c.s, c.ex, c.src,
-                      static_cast<const uint16_t*>(x), c.w, c.K, c.N, o, static_cast<O*>(y));
+  const Order o = make_order(256, max_tiles(c.ex.R, c.ex.E, 256), ceil_div(c.N, 256), &n);
+  return launch_tiles(c.who, row_kernel<KIND, O>, n, row_tile_lds(KIND), c.s, c.ex, c.src, static_cast<const char*>(x),
+                      xs, c.w, c.K, c.N, o, static_cast<O*>(y));
 }
 
 template <typename O>
 int run_bf16(const Call& c, const void* x, void* y) {
   if (few_rows(c.ex.R, c.ex.E)) return run_stream<false, O>(c, x, nullptr, y);
-  return launch_product<256, O>(c, x, y);
+  return run_rows<Kind::kBf16, O>(c, x, nullptr, y);
 }
 
 int run_f32(const Call& c, const void* x, void* y) {
@@ -349,15 +357,6 @@ int run_f32(const Call& c, const void* x, void* y) {
                      static_cast<const float*>(x), c.w, c.K, c.N, nb, static_cast<float*>(y));
   MOE_LAUNCH_CHECK(c.who);
   return MOE_OK;
-}
-
-template <typename O>
-int run_mx(const Call& c, const uint8_t* x, const uint8_t* xs, void* y) {
-  if (few_rows(c.ex.R, c.ex.E) || sizeof(O) == 4) return run_stream<true, O>(c, x, xs, y);
-  int64_t n;
-  const Order o = make_order(256, max_tiles(c.ex.R, c.ex.E, 256), ceil_div(c.N, 256), &n);
-  return launch_tiles(c.who, mx_kernel<O>, n, kMxTileLds, c.s, c.ex, c.src, x, xs, c.w, c.K, c.N, o,
-                      static_cast<O*>(y));
 }
 
 template <int TR>
@@ -477,7 +476,8 @@ extern "C" int moe_grouped_gemm_mx(const uint8_t* x, const uint8_t* x_scales, co
   hipStream_t s = as_stream(stream);
   const Call c{who, Experts{offsets, w->slot_of, R, E, w->n_slots, status}, Source{src_of, top_k, static_cast<int>(x_rows)},
                Weights{static_cast<const char*>(w->base), w->expert_bytes, w_off, s_off}, K, N, s};
-  rc = y_dtype == MOE_F32 ? run_mx<float>(c, x, x_scales, y) : run_mx<uint16_t>(c, x, x_scales, y);
+  rc = y_dtype == MOE_F32 ? run_rows<Kind::kMxExact, float>(c, x, x_scales, y)
+                          : run_rows<Kind::kMx, uint16_t>(c, x, x_scales, y);
   return debug_check(rc, who, s, status);
 }
 
