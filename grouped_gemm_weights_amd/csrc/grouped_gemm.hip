@@ -4,192 +4,24 @@
 //
 // The 8-bit form takes e4m3 rows and weights with a scale for each 32 values (mx.h).
 //
-// Two kinds of kernel:
-//   stream  few rows an expert: tiles of up to 64 rows x 64 columns whose weights go from HBM straight
-//           to MFMA operands (no LDS), the depth split over the block's waves; bound by weight bytes.
-//   tile    256 x 256 (64 x 64) tiles through LDS (mfma_tile.h, mx_tile.h); bound by the MFMA pipes.
+// The forward products of both types run on the tile loop of row_tile.h (256 x 256, 64 x 256 for few tiles,
+// 64 x 64 with the depth split over the waves for fewer), the gradients on that of mfma_tile.h, whose
+// operands run across the depth, and f32 on tiles of the fp32 MFMA (expert_tiles.h).  Blocks find their
+// tile from offsets by themselves.  Many rows are bound by the MFMA pipes, few by the weights' bytes.
+// Measured: 64 tokens x 8 on 64 experts of 7168 x 4096 in 8 bits 327 us (5.9 TB/s); 65536 rows of 32 such
+// experts 1.56 ms (2470 TFLOP/s).
 #include "expert_tiles.h"
 #include "row_tile.h"
 
-#ifndef NTW
-#define NTW false
-#endif
-#ifndef D1
-#define D1 4
-#define D2 3
-#define D4 2
-#endif
-#ifndef OCC
-#define OCC
-#endif
 namespace moe {
 namespace {
 
-// What a product reads its second operand from: the matrices [N][K] at `off` of each expert's block,
-// their scales (8 bits) at `scales_off`.
+// What a product reads its second operand from: the matrices [N][K] at `off` of each expert's block, their
+// scales (8 bits) at `scales_off`.
 struct Weights {
   const char* base;
   int64_t expert_bytes, off, scales_off;
 };
-
-// ---------------------------------------------------------------------------
-// stream
-// ---------------------------------------------------------------------------
-
-constexpr int kStreamCols = 64;
-constexpr int kChunk = 128;  // bytes of a row that a wave takes at a time
-
-// One operand: blocks of 16 rows, a lane row lane % 16 and, of each chunk, 16 bytes at 16 (lane / 16)
-// and 16 bytes 64 further on (what the MFMAs take from a lane).  The block's four waves take every
-// fourth chunk.  MX: and the chunk's word of four scales.
-template <bool MX, int BLOCKS, bool NT>
-struct Stream {
-  uint64_t base, scales;  // wave-uniform: where the chunk to load next starts
-  uint32_t voff[BLOCKS], soff[BLOCKS];
-
-  template <typename Src>
-  __device__ __forceinline__ void init(const char* p, int64_t row_bytes, const uint8_t* s, int64_t pitch, Src src) {
-    const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    base = reinterpret_cast<uint64_t>(p) + wave * kChunk;
-    scales = reinterpret_cast<uint64_t>(s) + wave * 4;
-#pragma unroll
-    for (int b = 0; b < BLOCKS; ++b) {
-      const int r = src(b * 16 + (lane & 15));
-      voff[b] = r < 0 ? kOutside : static_cast<uint32_t>(r * row_bytes + (lane >> 4) * 16);
-      soff[b] = r < 0 ? kOutside : static_cast<uint32_t>(r * pitch);
-    }
-  }
-  // left: bytes of a row from the chunk on; what is past them reads as zeros
-  __device__ __forceinline__ void load(int left, u32x4 (&v)[BLOCKS][2], uint32_t (&s)[BLOCKS]) {
-    const __amdgpu_buffer_rsrc_t r =
-        __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(base), 0, kOutside, 0x00020000);
-    const int k = (threadIdx.x & 48);
-#pragma unroll
-    for (int b = 0; b < BLOCKS; ++b) {
-      v[b][0] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, k < left ? voff[b] : kOutside, 0, NT ? 2 : 0));
-      v[b][1] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, k + 64 < left ? voff[b] + 64 : kOutside, 0, NT ? 2 : 0));
-    }
-    if constexpr (MX) {
-      const __amdgpu_buffer_rsrc_t q =
-          __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(scales), 0, kOutside, 0x00020000);
-#pragma unroll
-      for (int b = 0; b < BLOCKS; ++b) s[b] = __builtin_amdgcn_raw_buffer_load_b32(q, left > 0 ? soff[b] : kOutside, 0, 0);
-    }
-    base += 4 * kChunk;
-    scales += 16;
-  }
-};
-
-// Sixteen e4m3 values times 2^(byte - 127) as bf16, which holds them exactly.
-__device__ __forceinline__ void expand(const u32x4& v, uint32_t byte, bf16x8 (&out)[2]) {
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  const float scale = __uint_as_float(byte << 23);
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    bf16x2 p[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      p[i] = i % 2 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[2 * h + i / 2], scale, true)
-                   : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[2 * h + i / 2], scale, false);
-    out[h] = bf16x8{p[0][0], p[0][1], p[1][0], p[1][1], p[2][0], p[2][1], p[3][0], p[3][1]};
-  }
-}
-
-// A chunk of one block of 16 rows as MFMA operands, 8 bits expanded.  word: its four scales; a lane's
-// first 16 bytes are half of block 0 or 1, the others of block 2 or 3.
-template <bool MX>
-struct Operands {
-  static constexpr int N = MX ? 4 : 2;
-  bf16x8 v[N];
-  __device__ __forceinline__ void set(const u32x4 (&raw)[2], uint32_t word) {
-    if constexpr (MX) {
-      const uint32_t s = word >> (threadIdx.x >> 2 & 8);
-      bf16x8 h[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        expand(raw[i], s >> 16 * i & 0xff, h);
-        v[2 * i] = h[0];
-        v[2 * i + 1] = h[1];
-      }
-    } else {
-      v[0] = __builtin_bit_cast(bf16x8, raw[0]);
-      v[1] = __builtin_bit_cast(bf16x8, raw[1]);
-    }
-  }
-};
-
-// Tiles of 16 MF rows by 64 columns.  D: chunks in flight per wave.
-template <bool MX, int MF, int D, typename O>
-__global__ __launch_bounds__(256 OCC) void stream_kernel(Experts ex, Source src, const char* __restrict__ x,
-                                                     const uint8_t* __restrict__ xs, Weights w, int K, int N,
-                                                     int col_blocks, O* __restrict__ y) {
-  constexpr int NF = kStreamCols / 16;
-  __shared__ __attribute__((aligned(16))) floatx4 sums[4][MF * NF][kWave];
-  Tile t;
-  const int m = blockIdx.x / col_blocks, n0 = blockIdx.x % col_blocks * kStreamCols;
-  if (!find_tile<16 * MF>(ex, m, blockIdx.x == 0, &t)) return;
-  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int64_t row_bytes = static_cast<int64_t>(K) * (MX ? 1 : 2), pitch = MX ? mx_pitch(K) : 0;
-  const char* block = w.base + t.slot * w.expert_bytes;
-  const bool gather = src.src_of;
-  Stream<MX, MF, false> a;
-  Stream<MX, NF, NTW> b;
-  a.init(gather ? x : x + t.row0 * row_bytes, row_bytes, gather ? xs : xs + t.row0 * pitch, pitch,
-         [&](int r) { return r >= t.rows ? -1 : gather ? src.at(t.row0 + r) : r; });
-  b.init(block + w.off + n0 * row_bytes, row_bytes,
-         reinterpret_cast<const uint8_t*>(block) + w.scales_off + n0 * pitch, pitch,
-         [&](int c) { return n0 + c < N ? c : -1; });
-  floatx4 acc[MF][NF];
-#pragma unroll
-  for (int i = 0; i < MF; ++i)
-#pragma unroll
-    for (int j = 0; j < NF; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
-  u32x4 va[D][MF][2], vb[D][NF][2];
-  uint32_t sa[D][MF], sb[D][NF];
-  int left = static_cast<int>(row_bytes) - wave * kChunk;
-  auto load = [&](auto d) {
-    constexpr int I = decltype(d)::value;
-    b.load(left, vb[I], sb[I]);
-    a.load(left, va[I], sa[I]);
-    left -= 4 * kChunk;
-  };
-  each<0, D>(load);
-  // every wave makes the same number of steps; those past its depth add zeros
-  for (int at = 0; at < row_bytes; at += 4 * kChunk * D) {
-    each<0, D>([&](auto d) {
-      constexpr int I = decltype(d)::value;
-      Operands<MX> oa[MF], ob;
-#pragma unroll
-      for (int i = 0; i < MF; ++i) oa[i].set(va[I][i], sa[I][i]);
-      // the transposed block: a lane ends with four consecutive columns of one row
-#pragma unroll
-      for (int j = 0; j < NF; ++j) {
-        ob.set(vb[I][j], sb[I][j]);
-#pragma unroll
-        for (int h = 0; h < Operands<MX>::N; ++h)
-#pragma unroll
-          for (int i = 0; i < MF; ++i)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ob.v[h], oa[i].v[h], acc[i][j], 0, 0, 0);
-      }
-      load(d);
-    });
-  }
-#pragma unroll
-  for (int i = 0; i < MF; ++i)
-#pragma unroll
-    for (int j = 0; j < NF; ++j) sums[wave][i * NF + j][lane] = acc[i][j];
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < MF; ++i) {  // wave w joins column block w
-    const int f = i * NF + wave;
-    const floatx4 s = (sums[0][f][lane] + sums[1][f][lane]) + (sums[2][f][lane] + sums[3][f][lane]);
-    const int r = i * 16 + (lane & 15), c = n0 + wave * 16 + (lane >> 4) * 4;
-    if (r >= t.rows || c >= N) continue;
-    O* out = y + static_cast<int64_t>(t.row0 + r) * N + c;
-    if constexpr (sizeof(O) == 4) *reinterpret_cast<floatx4*>(out) = s;
-    else *reinterpret_cast<u32x2*>(out) = pack4(s[0], s[1], s[2], s[3]);
-  }
-}
 
 // ---------------------------------------------------------------------------
 // tiles
@@ -206,7 +38,8 @@ __global__ __launch_bounds__(256) void product_f32_kernel(Experts ex, Source src
 
 template <Kind KIND, int MI, typename O>
 __device__ __forceinline__ void row_tile(const Tile& t, int n0, const Source& src, const char* x, const uint8_t* xs,
-                                         const char* B, const uint8_t* bs, int K, int N, O* y, lds_char* smem) {
+                                         const char* B, const uint8_t* bs, int K, int N, int start, O* y,
+                                         lds_char* smem) {
   using S = TileShape<256, MI, false>;
   const int bytes = K * value_bytes(KIND);
   const bool gather = src.src_of;
@@ -214,13 +47,13 @@ __device__ __forceinline__ void row_tile(const Tile& t, int n0, const Source& sr
   const auto col = [&](int c) { return n0 + c < N ? c : -1; };
   RowOperand<S::ROWS> oa;
   RowOperand<S::TN> ob;
-  oa.init(gather ? x : x + static_cast<int64_t>(t.row0) * bytes, bytes, row);
-  ob.init(B + static_cast<int64_t>(n0) * bytes, bytes, col);
+  oa.init(gather ? x : x + static_cast<int64_t>(t.row0) * bytes, bytes, start, row);
+  ob.init(B + static_cast<int64_t>(n0) * bytes, bytes, start, col);
   ScaleRows sa, sb;
   if constexpr (KIND != Kind::kBf16) {
     const int64_t pitch = mx_pitch(K);
-    sa.init(gather ? xs : xs + t.row0 * pitch, pitch, row);
-    sb.init(bs + n0 * pitch, pitch, col);
+    sa.init(gather ? xs : xs + t.row0 * pitch, pitch, start / kMxBlock, row);
+    sb.init(bs + n0 * pitch, pitch, start / kMxBlock, col);
   }
   floatx16 acc[S::MW][S::NJ];
   RowProduct<KIND, MI> p{oa, ob, sa, sb, acc};
@@ -228,22 +61,58 @@ __device__ __forceinline__ void row_tile(const Tile& t, int n0, const Source& sr
   store_tile<256, MI>(acc, smem, y + static_cast<int64_t>(t.row0) * N + n0, N, t.rows, N - n0);
 }
 
-template <Kind KIND, typename O>
+// Tiles of TR rows (256 or 64) by 256 columns.  phases: how many 512-byte parts of a row the tiles of an XCD
+// take turns to start at (1: all at the row's start).
+template <Kind KIND, int TR, typename O>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void row_kernel(
     Experts ex, Source src, const char* __restrict__ x, const uint8_t* __restrict__ xs, Weights w, int K, int N,
-    Order order, O* __restrict__ y) {
+    Order order, int phases, O* __restrict__ y) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   int m, n;
   place(order, blockIdx.x, &m, &n);
   const int n0 = n * 256;
   Tile t;
-  if (n0 >= N || !find_tile<256, true>(ex, m, m == 0 && n == 0, &t)) return;
+  if (n0 >= N || !find_tile<TR, true>(ex, m, m == 0 && n == 0, &t)) return;
   const char* block = w.base + t.slot * w.expert_bytes;
-  by_rows<256>(t.rows, [&](auto mi) {
+  const int start = static_cast<int>(blockIdx.x / 8 % phases) * 512;
+  const auto run = [&](auto mi) {
     row_tile<KIND, decltype(mi)::value>(t, n0, src, x, xs, block + w.off,
-                                        reinterpret_cast<const uint8_t*>(block) + w.scales_off, K, N, y,
+                                        reinterpret_cast<const uint8_t*>(block) + w.scales_off, K, N, start, y,
                                         (lds_char*)smem);
-  });
+  };
+  if constexpr (TR == 256) by_rows<256>(t.rows, run);
+  else if (t.rows > 32) run(std::integral_constant<int, 2>{});
+  else run(std::integral_constant<int, 1>{});
+}
+
+// Tiles of 64 rows by 64 columns, the depth split over the waves.
+template <Kind KIND, typename O>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) void split_kernel(
+    Experts ex, Source src, const char* __restrict__ x, const uint8_t* __restrict__ xs, Weights w, int K, int N,
+    int col_blocks, O* __restrict__ y) {
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  const int m = blockIdx.x / col_blocks, n0 = blockIdx.x % col_blocks * 64;
+  Tile t;
+  if (!find_tile<64>(ex, m, blockIdx.x == 0, &t)) return;
+  const int bytes = K * value_bytes(KIND);
+  const int64_t pitch = KIND == Kind::kBf16 ? 0 : mx_pitch(K);
+  const char* block = w.base + t.slot * w.expert_bytes;
+  const bool gather = src.src_of;
+  const auto run = [&](auto mw) {
+    SplitProduct<KIND, decltype(mw)::value> p;
+    p.init(gather ? x : x + static_cast<int64_t>(t.row0) * bytes, block + w.off + static_cast<int64_t>(n0) * bytes,
+           gather ? xs : xs + t.row0 * pitch, reinterpret_cast<const uint8_t*>(block) + w.scales_off + n0 * pitch, bytes,
+           pitch, [&](int r) { return r >= t.rows ? -1 : gather ? src.at(t.row0 + r) : r; },
+           [&](int c) { return n0 + c < N ? c : -1; });
+    p.run(bytes, (lds_char*)smem, [&](int r, int c, floatx4 s) {
+      if (r >= t.rows || n0 + c >= N) return;
+      O* out = y + static_cast<int64_t>(t.row0 + r) * N + n0 + c;
+      if constexpr (sizeof(O) == 4) *reinterpret_cast<floatx4*>(out) = s;
+      else *reinterpret_cast<u32x2*>(out) = pack4(s[0], s[1], s[2], s[3]);
+    });
+  };
+  if (t.rows > 32) run(std::integral_constant<int, 2>{});
+  else run(std::integral_constant<int, 1>{});
 }
 
 // dX and dW in one launch: the blocks of one fill the CUs that the last of the other leave.
@@ -310,43 +179,43 @@ struct Call {
   hipStream_t s;
 };
 
-template <bool MX, int MF, int D, typename O>
-int launch_stream(const Call& c, const void* x, const uint8_t* xs, void* y) {
-  const int nb = ceil_div(c.N, kStreamCols);
-  const int64_t blocks = max_tiles(c.ex.R, c.ex.E, 16 * MF) * nb;
-  hipLaunchKernelGGL((stream_kernel<MX, MF, D, O>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, c.s, c.ex,
-                     c.src, static_cast<const char*>(x), xs, c.w, c.K, c.N, nb, static_cast<O*>(y));
-  MOE_LAUNCH_CHECK(c.who);
-  return MOE_OK;
-}
+// Whether an expert's weights are read about once: what bounds the product is then their bytes, and where
+// a row is a multiple of 2 KB all tiles at the same depth would ask few of the memory channels.  So
+// the tiles of an XCD start at different depths.  Measured, 8 rows each of 32 experts of 2048 columns,
+// the same start against different ones: bf16, depth 2048 65.8 / 48.9 us, 4096 129 / 93 us; 8 bits, 4096
+// 67 / 53 us.  With many rows tiles share panels in L2 and have to go together (2048 rows each of 8
+// experts of 4096 x 4096 427 / 470 us).
+bool few_rows(int R, int E) { return R <= 64 * static_cast<int64_t>(E); }
 
-// Tile height of the stream kernel by the rows that an expert has on average.
-template <bool MX, typename O>
-int run_stream(const Call& c, const void* x, const uint8_t* xs, void* y) {
-  const int64_t per = c.ex.R / c.ex.E;
-  if (per <= 8) return launch_stream<MX, 1, D1, O>(c, x, xs, y);
-  if (per <= 24) return launch_stream<MX, 2, D2, O>(c, x, xs, y);
-  return launch_stream<MX, 4, D4, O>(c, x, xs, y);
+template <Kind KIND, int TR, typename O>
+int launch_rows(const Call& c, const void* x, const uint8_t* xs, void* y) {
+  int64_t n;
+  const Order o = make_order(TR, max_tiles(c.ex.R, c.ex.E, TR), ceil_div(c.N, 256), &n);
+  const int bytes = c.K * value_bytes(KIND);
+  const int phases = few_rows(c.ex.R, c.ex.E) && bytes % 2048 == 0 ? bytes / 512 : 1;
+  return launch_tiles(c.who, row_kernel<KIND, TR, O>, n, row_tile_lds(KIND), c.s, c.ex, c.src,
+                      static_cast<const char*>(x), xs, c.w, c.K, c.N, o, phases, static_cast<O*>(y));
 }
-
-// Whether the stream kernel takes a product.
-#ifndef FEW
-#define FEW 64
-#endif
-bool few_rows(int R, int E) { return R <= FEW * static_cast<int64_t>(E); }
 
 template <Kind KIND, typename O>
-int run_rows(const Call& c, const void* x, const uint8_t* xs, void* y) {
-  int64_t n;
-  const Order o = make_order(256, max_tiles(c.ex.R, c.ex.E, 256), ceil_div(c.N, 256), &n);
-  return launch_tiles(c.who, row_kernel<KIND, O>, n, row_tile_lds(KIND), c.s, c.ex, c.src, static_cast<const char*>(x),
-                      xs, c.w, c.K, c.N, o, static_cast<O*>(y));
+int launch_split(const Call& c, const void* x, const uint8_t* xs, void* y) {
+  const int nb = ceil_div(c.N, 64);
+  return launch_tiles(c.who, split_kernel<KIND, O>, max_tiles(c.ex.R, c.ex.E, 64) * nb, SplitProduct<KIND, 2>::LDS, c.s,
+                      c.ex, c.src, static_cast<const char*>(x), xs, c.w, c.K, c.N, nb, static_cast<O*>(y));
 }
 
-template <typename O>
-int run_bf16(const Call& c, const void* x, void* y) {
-  if (few_rows(c.ex.R, c.ex.E)) return run_stream<false, O>(c, x, nullptr, y);
-  return run_rows<Kind::kBf16, O>(c, x, nullptr, y);
+// By how many tiles each kind would have (with one for every expert more than there can be):
+//   split  up to two a CU.  Measured, 4 experts, split against 64 x 256: bf16, 8 rows each of 4096 x 512
+//          9.9 / 34.8 us, 128 rows of 2048 x 2048 13.2 / 21.7 us, 256 rows (640 tiles) 21.4 / 22.0 us; 64 rows
+//          of 32 experts of 2112 x 2048 (2048 tiles) 72 / 54 us.
+//   64     up to one a CU.  Against 256 x 256: bf16, 1024 rows each of 4096 x 512 40 / 72 us, of 1024 x 768
+//          15 / 25 us; of 2048 x 2048 (544 tiles) 47 / 43 us.
+template <Kind KIND, typename O>
+int run_rows(const Call& c, const void* x, const uint8_t* xs, void* y) {
+  const int64_t small = max_tiles(c.ex.R, c.ex.E, 64);
+  if (small * ceil_div(c.N, 64) <= 2 * kCus) return launch_split<KIND, O>(c, x, xs, y);
+  if (small * ceil_div(c.N, 256) <= kCus) return launch_rows<KIND, 64, O>(c, x, xs, y);
+  return launch_rows<KIND, 256, O>(c, x, xs, y);
 }
 
 int run_f32(const Call& c, const void* x, void* y) {
@@ -451,7 +320,8 @@ extern "C" int moe_grouped_gemm(const void* x, const int32_t* src_of, int top_k,
   const Call c{who, Experts{offsets, w->slot_of, R, E, w->n_slots, status}, Source{src_of, top_k, static_cast<int>(x_rows)},
                Weights{static_cast<const char*>(w->base), w->expert_bytes, w_off, 0}, K, N, s};
   rc = dtype == MOE_F32 ? run_f32(c, x, y)
-                        : y_dtype == MOE_F32 ? run_bf16<float>(c, x, y) : run_bf16<uint16_t>(c, x, y);
+                        : y_dtype == MOE_F32 ? run_rows<Kind::kBf16, float>(c, x, nullptr, y)
+                                           : run_rows<Kind::kBf16, uint16_t>(c, x, nullptr, y);
   return debug_check(rc, who, s, status);
 }
 

@@ -80,28 +80,62 @@ __device__ __forceinline__ void expand(const i32x4& v, uint32_t byte, i32x4 (&ou
   }
 }
 
+__device__ __forceinline__ uint64_t uniform(const void* p) {
+  const uint64_t at = reinterpret_cast<uint64_t>(p);
+  return static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at))) |
+         static_cast<uint64_t>(static_cast<uint32_t>(
+             __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at >> 32)))) << 32;
+}
+
+// Four bytes per lane from buffer r + voff to LDS at `lds` + OFF + 4 lane.
+template <int OFF>
+__device__ __forceinline__ void copy_word_to_lds(u32x4 r, uint32_t voff, uint32_t lds) {
+  asm volatile(
+      "s_add_u32 m0, %0, %3\n\t"
+      "s_nop 0\n\t"
+      "buffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(voff), "s"(r), "n"(OFF)
+      : "memory", "scc");
+}
+
+// Where a product is in its depth: pieces of STEP bytes of a row, from `start` on and around its end.
+template <int STEP>
+struct Depth {
+  int bytes, at, todo;  // of a row; the piece to issue next; pieces still to be issued
+  __device__ __forceinline__ void init(int row, int start) {
+    bytes = row;
+    at = start;
+    todo = (row + STEP - 1) / STEP;
+  }
+  // Bytes of a row from the piece on: what lies past them is not there.
+  __device__ __forceinline__ int left() const { return todo > 0 ? bytes - at : 0; }
+  __device__ __forceinline__ void next() {
+    at = at + STEP >= bytes ? 0 : at + STEP;
+    --todo;
+  }
+};
+
 // How an operand's scales are copied: a lane a row.
 struct ScaleRows {
-  uint64_t base;   // wave-uniform: where the group to issue next starts
-  int left;        // bytes of a row from there on
+  uint64_t base;   // wave-uniform
+  Depth<16> depth;
   uint32_t voff;   // this lane's row, kOutside for none
 
   template <typename Src>
-  __device__ __forceinline__ void init(const uint8_t* p, int64_t pitch, Src src) {
-    const uint64_t at = reinterpret_cast<uint64_t>(p);
-    base = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at))) |
-           static_cast<uint64_t>(static_cast<uint32_t>(
-               __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at >> 32)))) << 32;
-    left = static_cast<int>(pitch);
+  __device__ __forceinline__ void init(const uint8_t* p, int64_t pitch, int start, Src src) {
+    base = uniform(p);
+    depth.init(static_cast<int>(pitch), start);
     const int r = src(threadIdx.x);
     voff = r < 0 ? kOutside : static_cast<uint32_t>(r * pitch);
   }
   template <int OFF>
   __device__ __forceinline__ void copy(uint32_t lds, bool live) {
-    const u32x4 r = {static_cast<uint32_t>(base), static_cast<uint32_t>(base >> 32), kOutside, 0x00020000u};
-    copy_to_lds<OFF>(r, live && left > 0 ? voff : kOutside, lds);
-    base += live ? 16 : 0;
-    left -= live ? 16 : 0;
+    const uint64_t at = base + depth.at;
+    const u32x4 r = {static_cast<uint32_t>(at), static_cast<uint32_t>(at >> 32), kOutside, 0x00020000u};
+    copy_to_lds<OFF>(r, live && depth.left() > 0 ? voff : kOutside, lds);
+    const Depth<16> now = depth;
+    depth.next();
+    depth.at = live ? depth.at : now.at;
+    depth.todo = live ? depth.todo : now.todo;
   }
 };
 
@@ -109,46 +143,31 @@ struct ScaleRows {
 template <int ROWS>
 struct RowOperand {
   static constexpr int N = ROWS / 32;  // copies per wave and stage, of 8 rows each
-  uint64_t base;     // wave-uniform: where the stage to issue next starts
-  int left;          // bytes of depth from there on
+  uint64_t base;     // wave-uniform
+  Depth<kRowBytes> depth;
   uint32_t voff[N];  // this lane's offset in each copy, kOutside for what does not exist
   int k_at;          // this lane's byte of a stage
 
   // Tile row r is at p + src(r) * bytes, src(r) < 0 for none.
   template <typename Src>
-  __device__ __forceinline__ void init(const char* p, int bytes, Src src) {
+  __device__ __forceinline__ void init(const char* p, int bytes, int start, Src src) {
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-    const uint64_t at = reinterpret_cast<uint64_t>(p);
-    base = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at))) |
-           static_cast<uint64_t>(static_cast<uint32_t>(
-               __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at >> 32)))) << 32;
-    left = bytes;
+    base = uniform(p);
+    depth.init(bytes, start);
     k_at = ((lane & 7) ^ ((wave & 1) * 4 + (lane >> 4))) * 16;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int r = src((i * 4 + wave) * 8 + (lane >> 3));
       voff[i] = r < 0 ? kOutside : static_cast<uint32_t>(static_cast<int64_t>(r) * bytes + k_at);
     }
-    bound();
   }
-  // The last stage may be short and the ones after it are empty: lanes past the depth copy zeros
-  // from there on.
-  __device__ __forceinline__ void bound() {
-    const bool past = k_at >= left;
-#pragma unroll
-    for (int i = 0; i < N; ++i) voff[i] = past ? kOutside : voff[i];
-  }
-  __device__ __forceinline__ void next_stage() {
-    base += kRowBytes;
-    left -= kRowBytes;
-    bound();
-  }
-  // Copy I of the stage at `base` to LDS offset OFF (the operand's stage buffer); lds is this wave's
-  // place: the tile's LDS + wave * 1024.
+  // Copy I of the next stage to LDS offset OFF (the operand's stage buffer); lds is this wave's place:
+  // the tile's LDS + wave * 1024.  Past the depth it copies zeros.
   template <int I, int OFF>
   __device__ __forceinline__ void copy(uint32_t lds) const {
-    const u32x4 r = {static_cast<uint32_t>(base), static_cast<uint32_t>(base >> 32), kOutside, 0x00020000u};
-    copy_to_lds<OFF + I * 4096>(r, voff[I], lds);
+    const uint64_t at = base + depth.at;
+    const u32x4 r = {static_cast<uint32_t>(at), static_cast<uint32_t>(at >> 32), kOutside, 0x00020000u};
+    copy_to_lds<OFF + I * 4096>(r, k_at < depth.left() ? voff[I] : kOutside, lds);
   }
 };
 
@@ -196,8 +215,8 @@ struct RowProduct {
     else B.template copy<C - NA, BUF * kRowStage + kRowOperand>(lds_c);
   }
   __device__ __forceinline__ void next_stage() {
-    A.next_stage();
-    B.next_stage();
+    A.depth.next();
+    B.depth.next();
   }
   // The next group's scales to `to` bytes from the first buffer; live: otherwise zeros, and it stays the next.
   __device__ __forceinline__ void copy_scales(uint32_t to, bool live) {
@@ -363,6 +382,187 @@ struct RowProduct {
       for (int j = 0; j < NJ; ++j) mfma_done(acc[i][j]);
     // the epilogue writes LDS: every wave's copies have landed and its reads are done
     wait_copies_and_sync<0>();
+  }
+};
+
+// A tile of 32 MW rows (MW = 1 or 2) by 64 columns for products that have too few of the tiles above to
+// fill the CUs: what bounds them is latency, so each of the four waves has the whole tile, every
+// fourth stage of its depth and two stages of its own in LDS, and waits for nobody until the four sums
+// are added in wave order.
+template <Kind KIND, int MW>
+struct SplitProduct {
+  static constexpr bool SCALES = KIND != Kind::kBf16;
+  static constexpr int NJ = 2, NA = MW * 4, NB = NJ * 4, NL = NA + NB + (SCALES ? 2 : 0);  // copies of a stage
+  static constexpr int STAGE = 2 * 64 * kRowBytes, SCALE_STAGE = 2 * 256;
+  static constexpr int WAVE = 2 * STAGE;                                  // LDS of a wave, 32 KB
+  static constexpr int LDS = 4 * WAVE + (SCALES ? 4 * 2 * SCALE_STAGE : 0);
+  uint64_t a, b, as, bs;       // wave-uniform: where a row's next stage of this wave starts, and its scales
+  int left;                    // bytes of a row from there on
+  uint32_t va[NA], vb[NB], vas, vbs;
+  int k_at;
+
+  // As for RowOperand; tile rows and columns below 64.
+  template <typename Row, typename Col>
+  __device__ __forceinline__ void init(const char* A, const char* B, const uint8_t* SA, const uint8_t* SB, int bytes,
+                                       int64_t pitch, Row row, Col col) {
+    const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    a = uniform(A) + wave * kRowBytes;
+    b = uniform(B) + wave * kRowBytes;
+    as = uniform(SA) + wave * 4;
+    bs = uniform(SB) + wave * 4;
+    left = bytes - wave * kRowBytes;
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      // copy i takes rows 8 i .. +7, chunks permuted by (row / 2) % 8
+      const int r = i * 8 + (lane >> 3);
+      if (i == 0) k_at = ((lane & 7) ^ (lane >> 4)) * 16;
+      const int k = k_at ^ (i & 1) * 64;
+      const int c = col(r);
+      vb[i] = c < 0 ? kOutside : static_cast<uint32_t>(static_cast<int64_t>(c) * bytes + k);
+      if (i < NA) {
+        const int s = row(r);
+        va[i % NA] = s < 0 ? kOutside : static_cast<uint32_t>(static_cast<int64_t>(s) * bytes + k);
+      }
+    }
+    if constexpr (SCALES) {
+      const int s = lane < MW * 32 ? row(lane) : -1, c = col(lane);
+      vas = s < 0 ? kOutside : static_cast<uint32_t>(s * pitch);
+      vbs = c < 0 ? kOutside : static_cast<uint32_t>(c * pitch);
+    }
+  }
+
+  static __device__ __forceinline__ u32x4 buffer(uint64_t at) {
+    return u32x4{static_cast<uint32_t>(at), static_cast<uint32_t>(at >> 32), kOutside, 0x00020000u};
+  }
+  // This wave's next stage to its buffer BUF; past the depth zeros.
+  template <int BUF>
+  __device__ __forceinline__ void copy(uint32_t lds, uint32_t lds_s) {
+    const bool even = k_at < left, odd = (k_at ^ 64) < left;  // the two orders of chunks
+    each<0, NB>([&](auto i) {
+      constexpr int I = decltype(i)::value;
+      const bool in = I % 2 ? odd : even;
+      if constexpr (I < NA) copy_to_lds<BUF * STAGE + I * 1024>(buffer(a), in ? va[I % NA] : kOutside, lds);
+      copy_to_lds<BUF * STAGE + 64 * kRowBytes + I * 1024>(buffer(b), in ? vb[I] : kOutside, lds);
+    });
+    if constexpr (SCALES) {
+      copy_word_to_lds<BUF * SCALE_STAGE>(buffer(as), left > 0 ? vas : kOutside, lds_s);
+      copy_word_to_lds<BUF * SCALE_STAGE + 256>(buffer(bs), left > 0 ? vbs : kOutside, lds_s);
+    }
+    a += 4 * kRowBytes;
+    b += 4 * kRowBytes;
+    as += 16;
+    bs += 16;
+    left -= 4 * kRowBytes;
+  }
+
+  template <int BUF>
+  __device__ __forceinline__ void stage(floatx16 (&acc)[MW][NJ], int mine, int mine_s) {
+    typedef const __attribute__((address_space(3))) i32x4 lds_i32x4;
+    typedef const __attribute__((address_space(3))) uint32_t lds_u32;
+    const int lane = threadIdx.x & (kWave - 1);
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(NL) : "memory");
+    i32x4 f[MW + NJ][4];
+    uint32_t sc[MW + NJ];
+#pragma unroll
+    for (int q = 0; q < MW + NJ; ++q) {
+      const int at = mine + BUF * STAGE + (q < MW ? q * 32 : 64 + (q - MW) * 32) * kRowBytes + (lane & 31) * kRowBytes;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        f[q][c] = *reinterpret_cast<lds_i32x4*>(
+            static_cast<uintptr_t>(at + ((2 * c + (lane >> 5)) ^ ((lane >> 1) & 7)) * 16));
+      if constexpr (SCALES)
+        sc[q] = *reinterpret_cast<lds_u32*>(static_cast<uintptr_t>(
+            mine_s + BUF * SCALE_STAGE + (q < MW ? q * 32 : 64 + (q - MW) * 32) * 4 + (lane & 31) * 4));
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    copy<BUF>(lds_d, lds_sc);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if constexpr (KIND == Kind::kMx) {
+#pragma unroll
+        for (int i = 0; i < MW; ++i)
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            const i32x8 x = __builtin_shufflevector(f[i][2 * h], f[i][2 * h + 1], 0, 1, 2, 3, 4, 5, 6, 7);
+            const i32x8 w = __builtin_shufflevector(f[MW + j][2 * h], f[MW + j][2 * h + 1], 0, 1, 2, 3, 4, 5, 6, 7);
+            const int own = (lane >> 5) * 8 + 16 * h;  // this lane's block's byte
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                w, x, acc[i][j], 0, 0, 0, static_cast<int>(sc[MW + j] >> own), 0, static_cast<int>(sc[i] >> own));
+          }
+      } else {
+        constexpr int N = KIND == Kind::kBf16 ? 1 : 2;  // MFMAs a chunk
+        i32x4 x[MW + NJ][2 * N];
+#pragma unroll
+        for (int q = 0; q < MW + NJ; ++q)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            if constexpr (N == 1) {
+              x[q][c] = f[q][2 * h + c];
+            } else {
+              i32x4 two[2];
+              expand(f[q][2 * h + c], sc[q] >> (16 * h + 8 * c) & 0xff, two);
+              x[q][2 * c % (2 * N)] = two[0];
+              x[q][(2 * c + 1) % (2 * N)] = two[1];
+            }
+          }
+#pragma unroll
+        for (int c = 0; c < 2 * N; ++c)
+#pragma unroll
+          for (int i = 0; i < MW; ++i)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, x[MW + j][c]),
+                                                                 __builtin_bit_cast(bf16x8, x[i][c]), acc[i][j], 0, 0, 0);
+      }
+    }
+  }
+
+  uint32_t lds_d, lds_sc;  // this wave's places
+
+  // bytes: of a row's depth.  put(row, column, sums): four consecutive columns of a row of the tile.
+  template <typename Put>
+  __device__ __forceinline__ void run(int bytes, lds_char* smem, Put put) {
+    const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    floatx16 acc[MW][NJ];
+#pragma unroll
+    for (int i = 0; i < MW; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+    const int lds = static_cast<int>(reinterpret_cast<uintptr_t>(smem));
+    lds_d = lds + wave * WAVE;
+    lds_sc = lds + 4 * WAVE + wave * 2 * SCALE_STAGE;
+    const int mine = static_cast<int>(lds_d), mine_s = static_cast<int>(lds_sc);
+    copy<0>(lds_d, lds_sc);
+    copy<1>(lds_d, lds_sc);
+    // every wave makes the same number of turns; stages past the depth add zeros
+    const int stages = (bytes + 4 * kRowBytes - 1) / (4 * kRowBytes);
+    for (int s = 0; s < stages; s += 2) {
+      stage<0>(acc, mine, mine_s);
+      stage<1>(acc, mine, mine_s);
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    typedef __attribute__((address_space(3))) floatx4 lds_floatx4;
+    lds_floatx4* sums = reinterpret_cast<lds_floatx4*>(smem);  // [wave][block][quarter][lane]: own buffers first
+#pragma unroll
+    for (int i = 0; i < MW; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          sums[wave * (WAVE / 16) + ((i * NJ + j) * 4 + v) * kWave + lane] =
+              floatx4{acc[i][j][v * 4], acc[i][j][v * 4 + 1], acc[i][j][v * 4 + 2], acc[i][j][v * 4 + 3]};
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < MW; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const lds_floatx4* p = sums + ((i * NJ + j) * 4 + wave) * kWave + lane;
+        const floatx4 s = (p[0] + p[WAVE / 16]) + (p[2 * (WAVE / 16)] + p[3 * (WAVE / 16)]);
+        put(i * 32 + (lane & 31), j * 32 + lane_col(wave), s);
+      }
   }
 };
 
