@@ -409,37 +409,32 @@ __device__ __forceinline__ void store_tile(
   }
 }
 
-// C[r][n] = sum_k A[r][k] B[k][n], or with B_ROWS sum_k A[r][k] B[n][k], for the rows of a tile and
-// columns n0 .. n0 + TN - 1.
-template <int TR, int MI, bool B_ROWS, typename O>
+// C[r][n] = sum_k A[r][k] B[k][n] for the rows of a tile and columns n0 .. n0 + TN - 1.
+template <int TR, int MI, typename O>
 __device__ __forceinline__ void rows_tile(const Tile& t, int n0, const uint16_t* A, int lda,
-                                          const Source& src, const uint16_t* B, int N, int K, O* C,
-                                          lds_char* smem) {
+                                          const uint16_t* B, int N, int K, O* C, lds_char* smem) {
   using S = TileShape<TR, MI, false>;
   Operand<false, S::ROWS> oa;
-  Operand<!B_ROWS, S::TN> ob;
-  const bool gather = src.src_of;
-  oa.init(gather ? A : A + static_cast<int64_t>(t.row0) * lda, lda, K,
-          [&](int r) { return r >= t.rows ? -1 : gather ? src.at(t.row0 + r) : r; });
-  ob.init(B_ROWS ? B + static_cast<int64_t>(n0) * K : B + n0, B_ROWS ? K : N, K,
-          [&](int c) { return n0 + c < N ? c : -1; });
+  Operand<true, S::TN> ob;
+  oa.init(A + static_cast<int64_t>(t.row0) * lda, lda, K, [&](int r) { return r < t.rows ? r : -1; });
+  ob.init(B + n0, N, K, [&](int c) { return n0 + c < N ? c : -1; });
   floatx16 acc[S::MW][S::NJ];
-  tile_product<TR, MI, false, false, !B_ROWS>(oa, ob, K, smem, acc);
+  tile_product<TR, MI, false, false, true>(oa, ob, K, smem, acc);
   store_tile<TR, MI>(acc, smem, C + static_cast<int64_t>(t.row0) * N + n0, N, t.rows, N - n0);
 }
 
 // The same for tile (m, n) of the list; B of the tile's expert starts at b_off of its block.
-template <int TR, bool B_ROWS = false, bool LARGE_FIRST = false, typename O>
+template <int TR, bool LARGE_FIRST = false, typename O>
 __device__ __forceinline__ void rows_product(const Experts& x, int m, int n, bool report,
                                              const uint16_t* A, int lda, const char* wbase,
                                              int64_t expert_bytes, int64_t b_off, int N, int K, O* C,
-                                             lds_char* smem, Source src = {}) {
+                                             lds_char* smem) {
   const int n0 = n * tile_columns(TR, false);
   Tile t;
   if (n0 >= N || !find_tile<TR, LARGE_FIRST>(x, m, report, &t)) return;
   const uint16_t* B = reinterpret_cast<const uint16_t*>(wbase + t.slot * expert_bytes + b_off);
   by_rows<TR>(t.rows, [&](auto mi) {
-    rows_tile<TR, decltype(mi)::value, B_ROWS>(t, n0, A, lda, src, B, N, K, C, smem);
+    rows_tile<TR, decltype(mi)::value>(t, n0, A, lda, B, N, K, C, smem);
   });
 }
 

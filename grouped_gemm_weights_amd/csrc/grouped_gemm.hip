@@ -137,7 +137,7 @@ TILE_KERNEL grads_kernel(Experts ex, const uint16_t* __restrict__ x, const uint1
   int64_t b = blockIdx.x;
   if (b < ranges.dx) {
     place(odx, static_cast<int>(b), &m, &n);
-    rows_product<TR, false, true>(ex, m, n, m == 0 && n == 0, dy, N, w.base, w.expert_bytes, w.off, K, N, dx, (lds_char*)smem);
+    rows_product<TR, true>(ex, m, n, m == 0 && n == 0, dy, N, w.base, w.expert_bytes, w.off, K, N, dx, (lds_char*)smem);
     return;
   }
   report_absent<TR>(ex, blockIdx.x == 0);

@@ -29,11 +29,23 @@ struct Outputs {
   float* rstd;
 };
 
+// How arrays of this size pass the caches.  Small ones take plain loads and stores: what one kernel writes
+// the next finds in the 256 MB that all XCDs share.  Larger ones leave by non-temporal stores, and from
+// 96 MB on come by such loads too, as in the backward pass, which reads three.  Measured (loads / stores,
+// n: non-temporal): bf16, 16384 rows of 7168 n/n 192 us, -/n 201; of 2048 n/n 46.5, -/n 42.4, -/- 49.7; f32,
+// 4099 rows of 1001 n/n 17.2, -/n 15.7, -/- 13.1; backward passes of these two n/n 51.8 and 24.8, -/- after
+// a forward pass that leaves the sum behind 48 and 19.3, after one that does not 61 and 19.
+enum Cache { kNear, kPast, kFar };
+Cache cache(int64_t T, int H, int size) {
+  const int64_t bytes = T * H * size;
+  return bytes <= (int64_t{32} << 20) ? kNear : bytes < (int64_t{96} << 20) ? kPast : kFar;
+}
+
 // `waves` waves per row, each lane NV vectors of 8 elements: H <= waves * 64 * NV * 8.  Rows of one
 // wave go four to a block, each wave on its own.  A block (wave) takes every `step`-th row.  KEEP:
 // gamma stays in registers from row to row and the next row's loads are issued before this row's sum.
-// TAIL: H is not a multiple of 8.  RES: with a residual.
-template <typename T, int NV, bool KEEP, bool TAIL, bool RES>
+// TAIL: H is not a multiple of 8.  RES: with a residual.  CACHE: as cache() says.
+template <typename T, int NV, bool KEEP, bool TAIL, bool RES, int CACHE>
 __global__ __launch_bounds__(1024) void rms_kernel(const T* x, const T* res, const float* __restrict__ gamma,
                                                    int rows, int H, int waves, float eps, Outputs<T> out) {
   __shared__ __attribute__((aligned(16))) float part[2][kMaxWaves];
@@ -51,8 +63,8 @@ __global__ __launch_bounds__(1024) void rms_kernel(const T* x, const T* res, con
     const int64_t at = n ? row * H : 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      load_raw<true, TAIL>(x + at, tid + i * lanes, n, raw[i]);
-      if constexpr (RES) load_raw<true, TAIL>(res + at, tid + i * lanes, n, raw_res[i]);
+      load_raw<CACHE == kFar, TAIL>(x + at, tid + i * lanes, n, raw[i]);
+      if constexpr (RES) load_raw<CACHE == kFar, TAIL>(res + at, tid + i * lanes, n, raw_res[i]);
     }
   };
   fetch();
@@ -71,7 +83,7 @@ __global__ __launch_bounds__(1024) void rms_kernel(const T* x, const T* res, con
         unpack<TAIL>(raw_res[i], tid + i * lanes, H, b);
 #pragma unroll
         for (int j = 0; j < kVec; ++j) v[i][j] = stored(v[i][j] + b[j], x);
-        if (out.sum) store8<true, TAIL>(out.sum + at_row * H, tid + i * lanes, H, v[i]);
+        if (out.sum) store8<CACHE != kNear, TAIL>(out.sum + at_row * H, tid + i * lanes, H, v[i]);
       }
 #pragma unroll
       for (int j = 0; j < kVec; ++j) s = fmaf(v[i][j], v[i][j], s);
@@ -86,7 +98,7 @@ __global__ __launch_bounds__(1024) void rms_kernel(const T* x, const T* res, con
       if (!KEEP) load8<false, TAIL>(gamma, at, H, g[i]);
 #pragma unroll
       for (int j = 0; j < kVec; ++j) v[i][j] = v[i][j] * r * g[i][j];
-      if (out.y) store8<true, TAIL>(out.y + at_row * H, at, H, v[i]);
+      if (out.y) store8<CACHE != kNear, TAIL>(out.y + at_row * H, at, H, v[i]);
       if (!TAIL && out.q)
         mx_store(v[i], static_cast<int64_t>(at) * kVec, H, out.q + at_row * H, out.scales + at_row * mx_pitch(H));
     }
@@ -143,8 +155,8 @@ __global__ __launch_bounds__(1024) void rms_long_kernel(const T* x, const T* res
 // columns, so the sums over its rows for dgamma stay in registers; the block's teams are joined in LDS
 // in team order and leave as one partial row of H floats (partial != nullptr).  Every team makes the
 // same number of turns, so all waves meet at the barriers.  AHEAD: the next row's loads are issued
-// before this row's sum and gamma stays in registers.
-template <typename T, int NV, bool AHEAD, bool TAIL>
+// before this row's sum and gamma stays in registers.  FAR: non-temporal loads and stores.
+template <typename T, int NV, bool AHEAD, bool TAIL, bool FAR>
 __global__ __launch_bounds__(1024) void rms_backward_kernel(
     const T* __restrict__ dy, const T* dsum, const T* __restrict__ x, const float* __restrict__ gamma,
     const float* __restrict__ rstd, int rows, int H, int waves, int groups, T* dx,
@@ -175,9 +187,9 @@ __global__ __launch_bounds__(1024) void rms_backward_kernel(
     r_n = n ? rstd[r] : 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      load_raw<true, TAIL>(x + at, tid + i * lanes, n, xn[i]);
-      load_raw<true, TAIL>(dy + at, tid + i * lanes, n, dn[i]);
-      load_raw<true, TAIL>(dsum + at, tid + i * lanes, dsum ? n : 0, sn[i]);
+      load_raw<FAR, TAIL>(x + at, tid + i * lanes, n, xn[i]);
+      load_raw<FAR, TAIL>(dy + at, tid + i * lanes, n, dn[i]);
+      load_raw<FAR, TAIL>(dsum + at, tid + i * lanes, dsum ? n : 0, sn[i]);
     }
   };
   int64_t first = static_cast<int64_t>(blockIdx.x) * groups, row = first + group;
@@ -218,7 +230,7 @@ __global__ __launch_bounds__(1024) void rms_backward_kernel(
     for (int i = 0; i < NV; ++i) {
 #pragma unroll
       for (int j = 0; j < kVec; ++j) a[i][j] = fmaf(r, a[i][j] - xh[i][j] * s, d[i][j]);
-      store8<true, TAIL>(dx + row * H, tid + i * lanes, H, a[i]);
+      store8<FAR, TAIL>(dx + row * H, tid + i * lanes, H, a[i]);
     }
   }
   if (!partial) return;
@@ -336,7 +348,7 @@ int partials(int T, int H) {
   return H <= kMaxBackwardH ? backward_shape(T, H).blocks : std::min(T, kCus);
 }
 
-template <typename E, int NV, bool RES>
+template <typename E, int NV, bool RES, int CACHE>
 int launch_rms(const E* x, const E* res, const float* gamma, int T, int H, float eps, const Outputs<E>& out,
                hipStream_t s) {
   const int waves = ceil_div(H, NV * kWave * kVec), rows = waves == 1 ? 4 : 1;
@@ -348,8 +360,8 @@ int launch_rms(const E* x, const E* res, const float* gamma, int T, int H, float
   if (too_many(blocks, waves * rows * kWave))
     return fail(MOE_ERR_UNSUPPORTED, "moe_rms_norm: T=%d too large at H=%d", T, H);
   auto kernel = H % kVec == 0
-                    ? (keep ? rms_kernel<E, NV, NV <= 2, false, RES> : rms_kernel<E, NV, false, false, RES>)
-                    : (keep ? rms_kernel<E, NV, NV <= 2, true, RES> : rms_kernel<E, NV, false, true, RES>);
+                    ? (keep ? rms_kernel<E, NV, NV <= 2, false, RES, CACHE> : rms_kernel<E, NV, false, false, RES, CACHE>)
+                    : (keep ? rms_kernel<E, NV, NV <= 2, true, RES, CACHE> : rms_kernel<E, NV, false, true, RES, CACHE>);
   hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(blocks)), dim3(waves * rows * kWave), 0, s, x, res,
                      gamma, T, H, waves, eps, out);
   MOE_LAUNCH_CHECK("moe_rms_norm: launch");
@@ -361,9 +373,10 @@ int rms(const void* xv, const void* rv, const float* gamma, int T, int H, float 
         hipStream_t s) {
   const E* x = static_cast<const E*>(xv);
   const E* res = static_cast<const E*>(rv);
-#define RMS(NV)                                                             \
-  return res ? launch_rms<E, NV, true>(x, res, gamma, T, H, eps, out, s)    \
-             : launch_rms<E, NV, false>(x, res, gamma, T, H, eps, out, s)
+  const Cache how = cache(T, H, sizeof(E));
+#define RMS_OF(NV, RES) \
+  (how == kNear ? launch_rms<E, NV, RES, kNear> : how == kPast ? launch_rms<E, NV, RES, kPast> : launch_rms<E, NV, RES, kFar>)
+#define RMS(NV) return (res ? RMS_OF(NV, true) : RMS_OF(NV, false))(x, res, gamma, T, H, eps, out, s)
   // Few rows, which leave CUs idle: a vector a lane, so that a row's loads spread over more waves.
   // Many rows: two, so that fewer waves wait for one another.
   const int per = kWave * kVec;
@@ -371,6 +384,7 @@ int rms(const void* xv, const void* rv, const float* gamma, int T, int H, float 
   if (H <= kMaxWaves * 2 * per) RMS(2);
   if (H <= kMaxH) RMS(4);
 #undef RMS
+#undef RMS_OF
   hipLaunchKernelGGL(rms_long_kernel<E>, dim3(T), dim3(1024), 0, s, x, res, gamma, H, eps, out);
   MOE_LAUNCH_CHECK("moe_rms_norm: launch");
   return MOE_OK;
@@ -385,9 +399,12 @@ int rms_backward(const void* dyv, const void* dsv, const void* xv, const float* 
   E* dx = static_cast<E*>(dxv);
   if (H <= kMaxBackwardH) {
     const BackwardShape b = backward_shape(T, H);
-    auto kernel = H % kVec == 0
-                      ? (b.nv == 1 ? rms_backward_kernel<E, 1, true, false> : rms_backward_kernel<E, 2, false, false>)
-                      : (b.nv == 1 ? rms_backward_kernel<E, 1, true, true> : rms_backward_kernel<E, 2, false, true>);
+    const bool far = cache(T, H, sizeof(E)) != kNear;
+#define BACKWARD(NV, AHEAD, TAIL) \
+  (far ? rms_backward_kernel<E, NV, AHEAD, TAIL, true> : rms_backward_kernel<E, NV, AHEAD, TAIL, false>)
+    auto kernel = H % kVec == 0 ? (b.nv == 1 ? BACKWARD(1, true, false) : BACKWARD(2, false, false))
+                                : (b.nv == 1 ? BACKWARD(1, true, true) : BACKWARD(2, false, true));
+#undef BACKWARD
     const size_t lds = b.groups > 1 && partial ? b.groups * static_cast<size_t>(H) * sizeof(float) : 0;
     hipLaunchKernelGGL(kernel, dim3(b.blocks), dim3(b.groups * b.waves * kWave), lds, s, dy, dsum, x, gamma,
                        rstd, T, H, b.waves, b.groups, dx, partial);
