@@ -2,7 +2,8 @@
 // halves, silu(gate) up.
 //
 // Bound by HBM.  A wave takes 512 columns of a row at a time: eight values a lane, one 16-byte load of
-// bf16 (two with SwiGLU), eight bytes and, for every 16 lanes, a word of four scales out.
+// bf16 (two with SwiGLU), eight bytes and, for every 16 lanes, a word of four scales out.  Measured, bf16:
+// SwiGLU of 65536 rows of 2 x 2048 107 us (6.3 TB/s), 4096 x 7168 weights 16 us (5.6 TB/s).
 #include "mx.h"
 #include "rows.h"
 
@@ -21,7 +22,8 @@ __global__ __launch_bounds__(256) void quantize_kernel(const T* __restrict__ x, 
                                                        uint32_t units, uint8_t* __restrict__ q,
                                                        uint8_t* __restrict__ scales) {
   const int lane = threadIdx.x & (kWave - 1);
-  const uint32_t all = gridDim.x * 4, n = rows * units;  // the host keeps their sum below 2^32
+  // n is below 2^26 where a wave takes more than one: no sum here passes 32 bits
+  const uint32_t all = gridDim.x * 4, n = rows * units;
   const int64_t pitch = mx_pitch(cols);
   for (uint32_t u = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave); u < n; u += all) {
     const int64_t row = u / units;
@@ -42,7 +44,11 @@ __global__ __launch_bounds__(256) void quantize_kernel(const T* __restrict__ x, 
 template <typename T>
 void launch(const void* x, int rows, int cols, bool swiglu, uint8_t* q, uint8_t* scales, hipStream_t s) {
   const int units = ceil_div(cols, kMxUnit);
-  const int64_t blocks = std::min<int64_t>(ceil_div64(static_cast<int64_t>(rows) * units, 4), kCus * 64);
+  // A unit a wave, or, where that is at most 64 blocks a CU, 16 of them that take turns.  Measured, turns
+  // against none: bf16 4096 x 7168 16.0 / 17.5 us, SwiGLU of 8192 x 1408 10.2 / 11.6 us; of 65536 x 2048 117 /
+  // 107 us.
+  const int64_t all = ceil_div64(static_cast<int64_t>(rows) * units, 4);
+  const int64_t blocks = all <= kCus * 64 ? std::min<int64_t>(all, kCus * 16) : all;
   hipLaunchKernelGGL((swiglu ? quantize_kernel<T, true> : quantize_kernel<T, false>),
                      dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, static_cast<const T*>(x),
                      static_cast<uint32_t>(rows), cols, static_cast<uint32_t>(units), q, scales);
@@ -66,7 +72,7 @@ extern "C" int moe_mx_quantize(const void* x, int rows, int cols, moe_dtype dtyp
     return fail(MOE_ERR_ARG, "%s: bad sizes rows=%d cols=%d, dtype or swiglu", who, rows, cols);
   if (cols % kMxBlock != 0 || cols > kMaxRow)
     return fail(MOE_ERR_UNSUPPORTED, "%s: cols=%d is not a multiple of %d, or above %d", who, cols, kMxBlock, kMaxRow);
-  if (static_cast<int64_t>(rows) * ceil_div(cols, kMxUnit) > UINT32_MAX - kCus * 256)
+  if (too_many(ceil_div64(static_cast<int64_t>(rows) * ceil_div(cols, kMxUnit), 4), 256))
     return fail(MOE_ERR_UNSUPPORTED, "%s: rows=%d too many at cols=%d", who, rows, cols);
   if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(scales)) % 16 != 0)
     return fail(MOE_ERR_UNSUPPORTED, "%s: q or scales is not aligned to 16 bytes", who);

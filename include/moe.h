@@ -524,8 +524,8 @@ int moe_mx_scale_pitch(int cols, size_t* bytes);
  *   x       device [rows][cols] dtype ([rows][2 cols] with swiglu); any alignment of one element
  *   q, scales device, aligned to 16 bytes
  * Errors: MOE_ERR_ARG for null pointers, bad sizes or swiglu not 0 or 1; MOE_ERR_UNSUPPORTED for cols not
- * a multiple of 32 or above 2^26, an unaligned output, or about 2^32 units of 512 columns.  rows = 0 is
- * a no-op.
+ * a multiple of 32 or above 2^26, an unaligned output, or a launch past 2^32 threads (a wave takes 512
+ * columns of a row: 2^26 of them).  rows = 0 is a no-op.
  */
 int moe_mx_quantize(const void* x, int rows, int cols, moe_dtype dtype, int swiglu, uint8_t* q,
                     uint8_t* scales, moe_stream_t stream);

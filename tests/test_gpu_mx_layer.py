@@ -1,0 +1,129 @@
+"""The 8-bit block (``mx_layer.MxMoELayer``) on the GPU: each step against ``oracle.block`` in float64 on what
+the step before stored, its graph, and its refusals.  Tolerances as in test_gpu_grouped_gemm."""
+import numpy as np
+import pytest
+
+from moe_cases import O, log, synth
+from oracle import block as K8
+from test_gpu_backward import HALF, U, check, gpu, host
+from test_gpu_grouped_gemm import largest_of_eight
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+
+def layer(T, H, I, E, k, dtype, seed):
+    from grouped_gemm_weights_amd.mx_layer import MxMoELayer
+    cfg = synth.MoEConfig("mx", T=T, H=H, I=I, E=E, k=k, dtype=dtype, n_local=E, seed=seed)
+    L = MxMoELayer(cfg)
+    rng = np.random.default_rng(seed)
+    for e in range(E):
+        w = rng.standard_normal(3 * H * I) * H ** -0.5
+        w[2 * H * I:] *= (H / I) ** 0.5
+        L.load_expert(e, gpu(w, dtype))
+    return cfg, L, rng
+
+
+def inputs(L, rng, dtype):
+    cfg = L.cfg
+    L.x.copy_(gpu(rng.standard_normal((cfg.T, cfg.H)), dtype))
+    L.residual.copy_(gpu(0.5 * rng.standard_normal((cfg.T, cfg.H)), dtype))
+    L.gamma.copy_(gpu(1 + 0.2 * rng.standard_normal(cfg.H)))
+    L.logits.copy_(gpu(rng.standard_normal((cfg.T, cfg.E))))
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("T,H,I,E,k,dtype", [(1, 64, 32, 4, 2, "bf16"), (64, 544, 288, 9, 3, "bf16"),
+                                             (700, 256, 192, 4, 2, "bf16"), (40, 96, 160, 5, 2, "f32"),
+                                             (0, 64, 32, 4, 2, "bf16")])
+def test_step(T, H, I, E, k, dtype):
+    log(f"case mx layer T={T} H={H} I={I} E={E} k={k} {dtype}")
+    cfg, L, rng = layer(T, H, I, E, k, dtype, 3 + T)
+    inputs(L, rng, dtype)
+    L.norm()
+    L.forward()
+    assert L.read_status() == 0
+    half = HALF[dtype]
+    n = lambda t: t.cpu().numpy()
+    total = (host(L.x).astype(np.float32) + host(L.residual).astype(np.float32))
+    assert torch.equal(L.sum.cpu(), torch.from_numpy(total).to(L.sum.dtype))
+    xn, _ = K8.rms_norm(host(L.sum), host(L.gamma), L.eps)
+    check("xn", L.xn, xn, (half + 80 * U) * np.abs(xn))
+    idx, w = O.route(n(L.logits), k) if T else (n(L.topk_idx), n(L.topk_w))
+    assert (np.asarray(idx) == n(L.topk_idx)).all()
+    off, src = n(L.offsets), n(L.src_of)
+    b = n(L.blocks)
+
+    def matrix(e, at, scales, rows, cols):
+        p = K8.pitch(cols)
+        return K8.decode(b[e, at:at + rows * cols].reshape(rows, cols), b[e, scales:scales + rows * p].reshape(rows, p))
+
+    wu = np.stack([matrix(e, 0, L.up_scales_off, 2 * I, H) for e in range(E)])
+    wd = np.stack([matrix(e, L.down_off, L.down_scales_off, H, I) for e in range(E)])
+    q = K8.decode(n(L.q), n(L.scales))[src // k]
+    ref, tol = K8.grouped_gemm(q, off, wu), H * U * K8.grouped_gemm(np.abs(q), off, np.abs(wu))
+    if dtype == "bf16":
+        for e in range(E):
+            rows = slice(int(off[e]), int(off[e + 1]))
+            tol[rows] += 7 * 2.0 ** -13 * largest_of_eight(q[rows], wu[e])
+    check("gate and up", L.gate_up, ref, half * (np.abs(ref) + tol) + tol)
+    h = K8.decode(n(L.h), n(L.h_scales))
+    v = K8.swiglu(host(L.gate_up))
+    assert np.linalg.norm(h - v) <= 2.0 ** -4 * np.linalg.norm(v)
+    check("down", L.y_perm, K8.grouped_gemm(h, off, wd), I * U * K8.grouped_gemm(np.abs(h), off, np.abs(wd)))
+    y = O.combine(host(L.y_perm), n(L.row_of), host(L.topk_w), k)
+    size = O.combine(np.abs(host(L.y_perm)), n(L.row_of), host(L.topk_w), k)
+    check("y", L.y, y, (k + 1) * U * size)
+    out = host(L.sum) + host(L.y)
+    check("out", L.out, out, half * np.abs(out) + 2 * U * (np.abs(out) + np.abs(host(L.y))))
+
+
+def test_graph_replay():
+    """forward captured, replayed on new rows and logits with eager work in between: the eager bits."""
+    cfg, L, rng = layer(50, 96, 64, 6, 2, "bf16", 8)
+    inputs(L, rng, "bf16")
+    L.norm()
+    L.forward()
+    g = L.capture()
+    for turn in range(4):
+        inputs(L, rng, "bf16")
+        L.norm()
+        L.y.fill_(float("nan"))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(L.compute_stream):
+            g.replay()
+        L.compute_stream.synchronize()
+        got = L.y.clone(), L.out.clone()
+        L.forward()
+        assert L.read_status() == 0
+        assert torch.equal(got[0], L.y) and torch.equal(got[1], L.out), turn
+        torch.randn(1 << 20, device="cuda").sum().item()
+
+
+def test_experts_pulled_from_a_pool():
+    """Blocks in another order in a pool, pulled by the routed prefetch into the layer's buffer."""
+    from grouped_gemm_weights_amd import binding as B
+    cfg, L, rng = layer(30, 96, 64, 6, 2, "bf16", 9)
+    inputs(L, rng, "bf16")
+    L.norm()
+    L.forward()
+    L.compute_stream.synchronize()
+    y = L.y.clone()
+    pool = L.blocks.clone()
+    L.blocks.fill_(0x7F)
+    torch.cuda.synchronize()
+    B.moe_prefetch_routed(B.pool(pool, L.expert_bytes, 0, cfg.E), L.counts, L.wbuf, L.compute_stream)
+    L.forward()
+    assert L.read_status() == 0
+    assert torch.equal(L.y, y)
+
+
+def test_refusals():
+    from grouped_gemm_weights_amd.mx_layer import MxMoELayer
+    with pytest.raises(ValueError):
+        MxMoELayer(synth.MoEConfig("mx", T=2, H=40, I=32, E=2, k=1, dtype="bf16", n_local=2, seed=0))
+    cfg, L, _ = layer(2, 64, 32, 2, 1, "bf16", 1)
+    block = torch.zeros(3 * 64 * 32, dtype=torch.bfloat16, device="cuda")
+    for e, bad in ((2, block), (-1, block), (0, block[:-1]), (0, block.float()), (0, block.cpu())):
+        with pytest.raises(ValueError):
+            L.load_expert(e, bad)
