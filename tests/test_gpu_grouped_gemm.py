@@ -509,3 +509,90 @@ def test_block_in_8_bits(T, top_k):
     off_by = np.linalg.norm(host(out) - full) / np.linalg.norm(full)
     log(f"  8 bits against bf16 weights in float64: {off_by:.3f}")
     assert off_by < 0.15
+
+
+# ----------------------------------------------------------------------------
+# many experts, rows of 2 KB, large sizes
+# ----------------------------------------------------------------------------
+
+def spread(E, seed, top):
+    """Rows of E experts: most a few, some none, some up to `top`."""
+    rng = np.random.default_rng(seed)
+    n = rng.integers(0, 4, E)
+    n[rng.integers(0, E, 3)] = rng.integers(1, top, 3)
+    return tuple(int(v) for v in n)
+
+
+@pytest.mark.parametrize("dtype", ["mx", "bf16", "f32"])
+@pytest.mark.parametrize("E,K,N,top", [(130, 64, 264, 300), (1000, 32, 72, 600), (1024, 32, 8, 70), (65, 96, 520, 900)])
+def test_many_experts(E, K, N, top, dtype):
+    """More experts than a wave has lanes: each lane looks after several in the list of tiles."""
+    counts = spread(E, E + K, top)
+    log(f"case {dtype} E={E} rows={sum(counts)} K={K} N={N}")
+    c = Case(counts, K, N, dtype, 71, gather=2)
+    c.call()
+    torch.cuda.synchronize()
+    assert int(c.status.item()) == 0
+    c.check()
+    if dtype != "mx":
+        c = Case(counts, K, N, dtype, 72)
+        dy, dx, dw, _ = backward(c, 4)
+        check_backward(c, dy, dx, dw)
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("E,N", [(70, 264), (20, 1032)])
+@pytest.mark.parametrize("K,dtype", [(2048, "mx"), (4096, "mx"), (1024, "bf16"), (2048, "bf16")])
+def test_tiles_that_start_at_different_depths(K, dtype, E, N, out):
+    """Few rows an expert and rows of a multiple of 2 KB: tiles begin inside the depth and go around it."""
+    if K * E > 50000:
+        E = E // 2 + 30
+    counts = spread(E, K, 80)
+    log(f"case {dtype} E={E} rows={sum(counts)} K={K} N={N} {out}")
+    c = Case(counts, K, N, dtype, 73, gather=3, out=out)
+    c.call()
+    torch.cuda.synchronize()
+    c.check()
+
+
+@pytest.mark.parametrize("dtype,out", [("mx", "bf16"), ("mx", "f32"), ("bf16", "bf16")])
+def test_outputs_past_2_31_elements(dtype, out):
+    """The last expert's rows lie past 2^31 elements of y."""
+    B = B_()
+    K, N, R = 32, 4104, 530_000
+    last = 40
+    log(f"case {dtype} -> {out}: {R * N / 2 ** 31:.2f} * 2^31 outputs")
+    c = Case((3, last), K, N, dtype, 74, out=out)          # the values to check against
+    offsets = i32([0, 3, R - last, R])
+    slots = i32([c.slots[0], c.slots[0], c.slots[1]])
+    buf = B.wbuf(c.wt, c.block, 2, 3, slots)
+    x = torch.zeros((R, K), dtype=c.xt.dtype, device="cuda")
+    x[:3], x[-last:] = c.xt[:3], c.xt[3:]
+    y = torch.empty((R, N), dtype=c.y.dtype, device="cuda")
+    if dtype == "mx":
+        xs = torch.zeros((R, 16), dtype=torch.uint8, device="cuda")
+        xs[:3], xs[-last:] = c.xs[:3], c.xs[3:]
+        B.moe_grouped_gemm_mx(x, xs, None, 0, offsets, R, 3, K, N, buf, c.w_off, c.s_off, code(out), y)
+    else:
+        B.moe_grouped_gemm(x, None, 0, offsets, R, 3, K, N, code(dtype), buf, c.w_off, code(out), y)
+    torch.cuda.synchronize()
+    c.y[:3], c.y[3:] = y[:3], y[-last:]
+    c.check()
+    assert not y[R // 2].any() and not y[R - last - 1].any()
+
+
+def test_gradients_past_2_31_elements():
+    B = B_()
+    K, N, R, last = 7168, 8, 300_100, 33
+    c = Case((5, last), K, N, "bf16", 75)
+    rng = np.random.default_rng(5)
+    dy = host(gpu(0.2 * rng.standard_normal((5 + last, N)), "bf16"))
+    x, dyt = (torch.zeros((R, n), dtype=torch.bfloat16, device="cuda") for n in (K, N))
+    x[:5], x[-last:] = c.xt[:5], c.xt[5:]
+    dyt[:5], dyt[-last:] = gpu(dy[:5], "bf16"), gpu(dy[5:], "bf16")
+    dx, dw = torch.empty_like(x), blank(tuple(c.wt.shape), "bf16")
+    offsets, slots = i32([0, R - last, R]), i32(c.slots)
+    B.moe_grouped_gemm_backward(x, dyt, offsets, R, 2, K, N, B.MOE_BF16, B.wbuf(c.wt, c.block, 2, 2, slots), c.w_off,
+                                dx, dw)
+    torch.cuda.synchronize()
+    check_backward(c, dy, torch.cat([dx[:5], dx[-last:]]), dw)      # rows of zeros add nothing to the first expert's
