@@ -330,7 +330,8 @@ constexpr int kMaxH = kMaxWaves * kWave * 4 * kVec;          // 32768: the longe
 constexpr int kMaxBackwardH = kMaxWaves * kWave * 2 * kVec;  // 16384: the longest of the backward kernel
 
 // Waves per row, rows at once per block and blocks of the backward pass: as many waves as the row has
-// 512 columns, as many rows as 16 waves hold, and a block a CU (more would mean more partial rows).
+// 512 columns, as many rows as 16 waves hold, and a block a CU (more would mean more partial rows).  Two
+// turns of one block are shorter than the launch that would add two blocks' sums.
 struct BackwardShape {
   int nv, waves, groups, blocks;
 };
@@ -340,7 +341,7 @@ BackwardShape backward_shape(int T, int H) {
   b.nv = H <= kMaxBackwardH / 2 ? 1 : 2;
   b.waves = ceil_div(H, b.nv * kWave * kVec);
   b.groups = std::max(1, kMaxWaves / b.waves);
-  b.blocks = static_cast<int>(std::min<int64_t>(kCus, ceil_div64(T, b.groups)));
+  b.blocks = T <= 2 * b.groups ? std::min(T, 1) : static_cast<int>(std::min<int64_t>(kCus, ceil_div64(T, b.groups)));
   return b;
 }
 
@@ -477,16 +478,17 @@ extern "C" int moe_rms_norm_backward(const void* dy, const void* dsum, const voi
     return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", who, ws_bytes, need);
   if (T == 0 && !dgamma) return MOE_OK;
   hipStream_t s = as_stream(stream);
-  float* partial = dgamma ? static_cast<float*>(ws) : nullptr;
+  const int n = partials(T, H);
+  float* partial = n == 1 ? dgamma : dgamma ? static_cast<float*>(ws) : nullptr;  // one row of sums is dgamma
   if (T > 0) {
     const int rc = dtype == MOE_F32 ? rms_backward<float>(dy, dsum, x, gamma, rstd, T, H, dx, partial, s)
                                     : rms_backward<uint16_t>(dy, dsum, x, gamma, rstd, T, H, dx, partial, s);
     if (rc) return rc;
   }
-  if (dgamma) {
+  if (dgamma && n != 1) {
     // no rows: zero sums
-    hipLaunchKernelGGL(rms_sum_kernel, dim3(ceil_div(H, kWave)), dim3(kMaxWaves * kWave), 0, s, partial,
-                       partials(T, H), H, dgamma);
+    hipLaunchKernelGGL(rms_sum_kernel, dim3(ceil_div(H, kWave)), dim3(kMaxWaves * kWave), 0, s, partial, n, H,
+                       dgamma);
     MOE_LAUNCH_CHECK("moe_rms_norm_backward: sum launch");
   }
   return debug_check(MOE_OK, who, s, nullptr);

@@ -405,3 +405,25 @@ def test_norm_and_quantize_graph_replay():
         for name in ("sum", "y", "rstd", "dx", "dg", "q", "s", "q2", "s2"):
             assert torch.equal(a[name].view(torch.uint8), b[name].view(torch.uint8)), (turn, name)
         torch.randn(1 << 20, device="cuda").sum().item()
+
+
+@pytest.mark.parametrize("T,H,dtype", [(1, 64, "f32"), (2, 8192, "bf16"), (3, 8192, "bf16"), (32, 500, "bf16"),
+                                       (33, 500, "f32"), (31, 512, "f32"), (4, 4096, "f32"), (5, 4096, "bf16")])
+def test_rms_norm_backward_of_few_rows(T, H, dtype):
+    """One block's sums are dgamma itself; from one row more on they are added from the workspace."""
+    B = B_()
+    s, _, dy, dsum, gamma = norm_inputs(T, H, dtype, 60 + T + H)
+    rstd = host(gpu(K.rms_norm(s, gamma, 1e-5)[1]))
+    need = B.moe_rms_norm_backward_workspace_size(T, H)
+    dx, dg = blank((T, H), dtype), blank((H,))
+    B.moe_rms_norm_backward(gpu(dy, dtype), gpu(dsum, dtype), gpu(s, dtype), gpu(gamma), gpu(rstd), T, H, code(dtype),
+                            dx, dg, scratch(need), need)
+    torch.cuda.synchronize()
+    rdx, rdg = K.rms_norm_backward(dy, dsum, s, gamma, rstd)
+    xh = np.abs(s * rstd[:, None])
+    check("dgamma", dg, rdg, (DEPTH + 4) * U * (np.abs(dy) * xh).sum(0))
+    a, r = np.abs(dy * gamma), rstd[:, None]
+    f32 = r * (4 * U * a + (DEPTH + 8) * U * xh * (a * xh).mean(1, keepdims=True)) + 2 * U * np.abs(rdx)
+    check("dx", dx, rdx, HALF[dtype] * (np.abs(rdx) + f32) + f32)
+    behind = torch.as_strided(dg, (32,), (1,), dg.storage_offset() + H)
+    assert torch.isnan(behind).all()
