@@ -61,8 +61,12 @@ __device__ __forceinline__ void row_tile(const Tile& t, int n0, const Source& sr
   store_tile<256, MI>(acc, smem, y + static_cast<int64_t>(t.row0) * N + n0, N, t.rows, N - n0);
 }
 
-// Tiles of TR rows (256 or 64) by 256 columns.  phases: how many 512-byte parts of a row the tiles of an XCD
-// take turns to start at (1: all at the row's start).
+// Tiles of TR rows (256 or 64) by 256 columns.  phases: how many 512-byte parts of a row the units of tiles
+// take turns to start at (1: all at the row's start).  Where a row is a multiple of 2 KB, all tiles at one
+// depth would ask few of the memory channels; the tiles of a unit go together, since they read the same
+// rows.  Measured at 32 experts of 2048 columns, the same start against these: 8 rows each, bf16, depth
+// 2048 65.8 / 48.3 us, 4096 129 / 101 us; 128 rows each, bf16, 2048 70 / 56 us, 4096 131 / 102 us, 8 bits,
+// 4096 74 / 60 us; 2048 rows each of 8 experts of 4096 x 4096 428 / 427 us.
 template <Kind KIND, int TR, typename O>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void row_kernel(
     Experts ex, Source src, const char* __restrict__ x, const uint8_t* __restrict__ xs, Weights w, int K, int N,
@@ -74,7 +78,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
   Tile t;
   if (n0 >= N || !find_tile<TR, true>(ex, m, m == 0 && n == 0, &t)) return;
   const char* block = w.base + t.slot * w.expert_bytes;
-  const int start = static_cast<int>(blockIdx.x / 8 % phases) * 512;
+  const int start = static_cast<int>((blockIdx.x / 8 / (order.gm * order.gn) * 8 + blockIdx.x % 8) % phases) * 512;
   const auto run = [&](auto mi) {
     row_tile<KIND, decltype(mi)::value>(t, n0, src, x, xs, block + w.off,
                                         reinterpret_cast<const uint8_t*>(block) + w.scales_off, K, N, start, y,
@@ -179,20 +183,25 @@ struct Call {
   hipStream_t s;
 };
 
-// Whether an expert's weights are read about once: what bounds the product is then their bytes, and where
-// a row is a multiple of 2 KB all tiles at the same depth would ask few of the memory channels.  So
-// the tiles of an XCD start at different depths.  Measured, 8 rows each of 32 experts of 2048 columns,
-// the same start against different ones: bf16, depth 2048 65.8 / 48.9 us, 4096 129 / 93 us; 8 bits, 4096
-// 67 / 53 us.  With many rows tiles share panels in L2 and have to go together (2048 rows each of 8
-// experts of 4096 x 4096 427 / 470 us).
-bool few_rows(int R, int E) { return R <= 64 * static_cast<int64_t>(E); }
+// The tallest unit of 4, 2 or 1 by up to 8 tiles (columns cut evenly) that leaves every XCD four, else single
+// tiles: tiles of one row panel that run together on an XCD read it once into its L2.  Measured, 256 rows
+// each of 32 experts of 2112 x 2048, 1 x 8 against single tiles, which read x again for each column tile:
+// bf16 73 / 88 us, 8 bits 45 / 60 us; 8 bits of 4224 x 2048 76 / 108 us.
+Order row_order(int64_t mt, int64_t nt, int64_t* blocks) {
+  Order o{4, static_cast<int>(ceil_div64(nt, ceil_div64(nt, 8))), 0};
+  while (o.gm > 1 && ceil_div64(mt, o.gm) * ceil_div64(nt, o.gn) < 32) o.gm /= 2;
+  if (ceil_div64(mt, o.gm) * ceil_div64(nt, o.gn) < 32) o.gm = o.gn = 1;
+  o.n_gn = static_cast<int>(ceil_div64(nt, o.gn));
+  *blocks = ceil_div64(ceil_div64(mt, o.gm) * o.n_gn, 8) * 8 * o.gm * o.gn;
+  return o;
+}
 
 template <Kind KIND, int TR, typename O>
 int launch_rows(const Call& c, const void* x, const uint8_t* xs, void* y) {
   int64_t n;
-  const Order o = make_order(TR, max_tiles(c.ex.R, c.ex.E, TR), ceil_div(c.N, 256), &n);
+  const Order o = row_order(max_tiles(c.ex.R, c.ex.E, TR), ceil_div(c.N, 256), &n);
   const int bytes = c.K * value_bytes(KIND);
-  const int phases = few_rows(c.ex.R, c.ex.E) && bytes % 2048 == 0 ? bytes / 512 : 1;
+  const int phases = bytes % 2048 == 0 ? bytes / 512 : 1;
   return launch_tiles(c.who, row_kernel<KIND, TR, O>, n, row_tile_lds(KIND), c.s, c.ex, c.src,
                       static_cast<const char*>(x), xs, c.w, c.K, c.N, o, phases, static_cast<O*>(y));
 }
