@@ -70,7 +70,8 @@ __device__ __forceinline__ void mfma_done(floatx16& acc) {
   asm volatile("s_nop 15\n\ts_nop 15" : "+a"(acc));
 }
 
-// Sixteen e4m3 values times 2^(byte - 127) as bf16, which holds them exactly: two MFMA operands.
+// Sixteen e4m3 values times 2^(byte - 127) as bf16, which holds them exactly (from byte 3 on: an element has
+// steps of 2^-9, and bf16's subnormals steps of 2^-133): two MFMA operands.
 __device__ __forceinline__ void expand(const i32x4& v, uint32_t byte, i32x4 (&out)[2]) {
   const float scale = __uint_as_float(byte << 23);
 #pragma unroll

@@ -596,3 +596,26 @@ def test_gradients_past_2_31_elements():
                                 dx, dw)
     torch.cuda.synchronize()
     check_backward(c, dy, torch.cat([dx[:5], dx[-last:]]), dw)      # rows of zeros add nothing to the first expert's
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("low,high", [(0, 239), (3, 239), (228, 8), (40, 200)])
+@pytest.mark.parametrize("counts", [(5, 9), (200, 77), (700, 1300)])
+def test_mx_scales_at_the_ends(counts, low, high, out):
+    """x's smallest scale byte is ``low`` and the weights' largest ``high``: scales of 2^-127 to 2^117, values in
+    bf16's subnormals.  (2^-124 on with f32 outputs: below it not every element is a bf16 number.)"""
+    low = max(low, 3) if out == "f32" else low
+    c = Case(counts, 544, 2056 if sum(counts) > 1000 else 72, "mx", 76, out=out)
+    K, N, n = c.K, c.N, c.K // 32
+    xs, ws = host(c.xs), host(c.wt[:, c.s_off:c.s_off + N * 32]).reshape(len(counts), N, 32)
+    by_x, by_w = low - int(xs[:, :n].min()), high - int(ws[:, :, :n].max())
+    xs[:, :n] += by_x
+    ws[:, :, :n] += by_w
+    assert xs.min() >= 0 and ws.min() >= 0 and xs.max() < 248 and ws.max() < 248
+    c.xs.copy_(torch.from_numpy(xs.astype(np.uint8)))
+    c.wt[:, c.s_off:c.s_off + N * 32] = torch.from_numpy(ws.reshape(len(counts), -1).astype(np.uint8)).cuda()
+    c.x, c.w = c.x * 2.0 ** by_x, c.w * 2.0 ** by_w
+    c.rows = c.x
+    c.call()
+    torch.cuda.synchronize()
+    c.check()
