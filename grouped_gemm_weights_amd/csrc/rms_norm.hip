@@ -6,7 +6,9 @@
 //   backward  xh = s r,  a = dy gamma,  dx = dsum + r (a - xh mean(a xh)),  dgamma = sum_t dy xh
 //
 // Both are bound by HBM: a row is read once and held in registers as fp32; its one statistic is an
-// fp32 sum over it.  y is quantised from fp32, not from its rounding to bf16.
+// fp32 sum over it.  y is quantised from fp32, not from its rounding to bf16.  Measured: bf16, 16384 x 7168
+// with the residual, sum, y and 8-bit rows 191 us (5.6 TB/s); 64 x 7168 4.6 us on the GPU, 2-3 of them the
+// launch; f32, 4099 x 1001 forward 15, backward 17 + 4 us.
 #include <algorithm>
 
 #include "mx.h"
@@ -34,7 +36,9 @@ struct Outputs {
 // 96 MB on come by such loads too, as in the backward pass, which reads three.  Measured (loads / stores,
 // n: non-temporal): bf16, 16384 rows of 7168 n/n 192 us, -/n 201; of 2048 n/n 46.5, -/n 42.4, -/- 49.7; f32,
 // 4099 rows of 1001 n/n 17.2, -/n 15.7, -/- 13.1; backward passes of these two n/n 51.8 and 24.8, -/- after
-// a forward pass that leaves the sum behind 48 and 19.3, after one that does not 61 and 19.
+// a forward pass that leaves the sum behind 48 and 19.3, after one that does not 61 and 19.  Where other
+// work has passed the cache in between (f32, both passes in turn on 345 MB) -/-, n/- and n/n take 39.5,
+// 40.2 and 42.2 us.
 enum Cache { kNear, kPast, kFar };
 Cache cache(int64_t T, int H, int size) {
   const int64_t bytes = T * H * size;
