@@ -427,3 +427,18 @@ def test_rms_norm_backward_of_few_rows(T, H, dtype):
     check("dx", dx, rdx, HALF[dtype] * (np.abs(rdx) + f32) + f32)
     behind = torch.as_strided(dg, (32,), (1,), dg.storage_offset() + H)
     assert torch.isnan(behind).all()
+
+
+def test_dropout_past_2_34_elements():
+    """In place, where a thread takes more than one turn and an element's index / 4 passes 32 bits."""
+    B = B_()
+    n, p, seed, step = 2 ** 34 + 5003, 0.25, 9, 4
+    if torch.cuda.mem_get_info()[0] < 2 * n + 2 ** 33:
+        pytest.skip("34 GB of device memory are not free")
+    x = torch.ones(n, dtype=torch.bfloat16, device="cuda")
+    B.moe_dropout_add(x, B.MOE_BF16, None, n, p, rng_state(seed, step), B.MOE_BF16, x)
+    torch.cuda.synchronize()
+    one = float(host(gpu(np.array([1 / (1 - p)]), "bf16"))[0])
+    for first in (0, 2 ** 33 - 1000, 2 ** 34 - 2000, n - 3000):
+        got = host(x[first:first + 3000])
+        assert np.array_equal(got, np.where(K.keep(got.size, p, seed, step, first=first), one, 0))

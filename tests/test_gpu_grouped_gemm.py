@@ -619,3 +619,27 @@ def test_mx_scales_at_the_ends(counts, low, high, out):
     c.call()
     torch.cuda.synchronize()
     c.check()
+
+
+@pytest.mark.parametrize("K,dtype,out", [(2048, "mx", "bf16"), (2048, "mx", "f32"), (1024, "bf16", "bf16"),
+                                         (2048, "bf16", "f32")])
+@pytest.mark.parametrize("counts,N", [((2300, 1, 0, 1500, 700), 2056), ((600, 900, 256), 3336), ((8000,), 520)])
+def test_units_of_many_rows_start_at_different_depths(K, dtype, out, counts, N):
+    """Rows of a multiple of 2 KB in units of 1, 2 and 4 tiles by several."""
+    log(f"case {dtype} rows={counts} K={K} N={N} {out}")
+    c = Case(counts, K, N, dtype, 77, out=out)
+    c.call()
+    torch.cuda.synchronize()
+    c.check()
+
+
+@pytest.mark.parametrize("counts", [(3, 0, 30), (200, 77)])
+@pytest.mark.parametrize("K,N,dtype", [(2 ** 20, 8, "mx"), (2 ** 20, 8, "bf16"), (2 ** 20, 3, "f32"),
+                                       (32, 2 ** 20, "mx"), (8, 2 ** 20, "bf16"), (3, 2 ** 20, "f32")])
+def test_the_longest_sides(counts, K, N, dtype):
+    log(f"case {dtype} rows={counts} K={K} N={N}")
+    counts = counts if K > N or counts[1] == 0 else (70, 20)
+    c = Case(counts, K, N, dtype, 78, out="f32")
+    c.call()
+    torch.cuda.synchronize()
+    c.check()
