@@ -163,7 +163,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) voi
   else run(std::integral_constant<int, 1>{});
 }
 
-// dX and dW in one launch: the blocks of one fill the CUs that the last of the other leave.
+// dX and dW in one launch where their tiles are alike: the blocks of one fill the CUs that the last of the other leave.
 struct GradRanges {
   int64_t dx;  // blocks of dX
   int per;     // blocks of an expert's dW
@@ -286,7 +286,7 @@ int launch_grads(const Call& c, const void* x, const void* dy, void* dx, void* d
   GradRanges r{0, 1};
   Order odx{}, odw{};
   int64_t n, blocks = 0;
-  if (dx && c.ex.R > 0) {
+  if (dx) {
     odx = make_order(TR, max_tiles(c.ex.R, c.ex.E, TR), ceil_div(c.K, tile_columns(TR, false)), &n);
     blocks = r.dx = n;
   }
@@ -420,17 +420,30 @@ extern "C" int moe_grouped_gemm_backward(const void* x, const void* dy, const in
   hipStream_t s = as_stream(stream);
   const Call c{who, Experts{offsets, w->slot_of, R, E, w->n_slots, status}, Source{},
                Weights{static_cast<const char*>(w->base), w->expert_bytes, w_off, 0}, K, N, s};
+  if (R == 0) dx = nullptr;
   if (dtype == MOE_F32) {
     const int64_t nk = ceil_div(K, 64);
     const bool small_dx = small_tiles_f32(max_tiles(R, E, 64) * nk);
     const bool small_dw = small_tiles_f32(E * nk * ceil_div(N, 64));
     auto launch = small_dx ? (small_dw ? launch_grads_f32<32, 32> : launch_grads_f32<32, 64>)
                            : (small_dw ? launch_grads_f32<64, 32> : launch_grads_f32<64, 64>);
-    rc = launch(c, x, dy, R > 0 ? dx : nullptr, dw);
+    rc = launch(c, x, dy, dx, dw);
   } else {
-    // large tiles when dX has one for every CU, else small ones, of which there are 16 times as many
-    rc = max_tiles(R, E, 256) * ceil_div(K, 256) >= kCus ? launch_grads<256>(c, x, dy, dx, dw)
-                                                         : launch_grads<64>(c, x, dy, dx, dw);
+    // Large tiles for dX when it has one for every CU; for dW when it has one for every other CU, or every
+    // fourth beside large tiles of dX.  Where the two differ they are launches of their own.  Measured
+    // (both gradients and the forward product), dW in dX's size against its own: 32 rows each of 8 experts
+    // of 2048 x 2048 (512 tiles) 61 / 51 us, 1373 rows each of 12 of 88 x 3024 (144) 138 / 130 us, 12 rows
+    // each of 23 of 88 x 1168 (115) 13.8 / 20.6 us; beside large dX 4096 rows each of 8 of 512 x 1024 (64)
+    // 167 / 200 us, 65536 rows of 512 x 512 (4) 1091 / 338 us.
+    const bool large_dx = max_tiles(R, E, 256) * ceil_div(K, 256) >= kCus;
+    const bool large_dw =
+        static_cast<int64_t>(E) * ceil_div(N, 256) * ceil_div(K, 256) >= (dx && large_dx ? kCus / 4 : kCus / 2);
+    if (dx && dw && large_dx != large_dw) {
+      rc = large_dx ? launch_grads<256>(c, x, dy, dx, nullptr) : launch_grads<64>(c, x, dy, dx, nullptr);
+      if (rc) return rc;
+      dx = nullptr;
+    }
+    rc = (dx ? large_dx : large_dw) ? launch_grads<256>(c, x, dy, dx, dw) : launch_grads<64>(c, x, dy, dx, dw);
   }
   return debug_check(rc, who, s, status);
 }

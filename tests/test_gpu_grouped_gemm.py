@@ -643,3 +643,14 @@ def test_the_longest_sides(counts, K, N, dtype):
     c.call()
     torch.cuda.synchronize()
     c.check()
+
+
+@pytest.mark.parametrize("want", [("dx", "dw"), ("dw",), ("dx",)])
+@pytest.mark.parametrize("counts,K,N", [((33_000,), 264, 256), ((1, 0, 20, 7, 3, 12, 40, 5), 1096, 1032),
+                                        ((4000, 0, 5500, 2100), 1544, 520)])
+def test_gradients_whose_tiles_differ(counts, K, N, want):
+    """dX of large tiles and dW of small ones, the other way round, and one of the two alone."""
+    log(f"case rows={counts} K={K} N={N} {want}")
+    c = Case(counts, K, N, "bf16", 79)
+    dy, dx, dw, _ = backward(c, 4, want)
+    check_backward(c, dy, dx, dw)
