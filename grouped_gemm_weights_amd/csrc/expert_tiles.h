@@ -44,8 +44,11 @@ __device__ __forceinline__ bool find_tile(const Experts& x, int m, bool report, 
   const int lane = threadIdx.x & (kWave - 1);
   const int per = (x.E + kWave - 1) / kWave;  // experts of a lane
   const int e0 = min(lane * per, x.E), e1 = min(e0 + per, x.E);
-  // of an expert's `cnt` rows: tiles of the first kind, and whether its last tile is of the second
-  const auto first_kind = [](int cnt) { return LARGE_FIRST ? (cnt + TR / 2 - 1) / TR : (cnt + TR - 1) / TR; };
+  // of an expert's `cnt` rows: tiles of the first kind (up to 2^31 - 1 rows, so the sum is unsigned), and
+  // whether its last tile is of the second
+  const auto first_kind = [](int cnt) {
+    return static_cast<int>((static_cast<uint32_t>(cnt) + (LARGE_FIRST ? TR / 2 : TR) - 1) / TR);
+  };
   const auto second_kind = [](int cnt) { return LARGE_FIRST && cnt % TR > 0 && cnt % TR <= TR / 2 ? 1 : 0; };
   int n = 0, n2 = 0, cnt = 0, lo = 0, slot = 0;
   for (int e = e0; e < e1; ++e) {
@@ -258,7 +261,7 @@ __device__ __forceinline__ void tile_product_f32(const float* __restrict__ A, in
   });
   __syncthreads();
   each<0, NP>([&](auto t) { read(std::integral_constant<int, 0>{}, t, lds); });
-  int stages = (K + T::K - 1) / T::K;
+  int stages = static_cast<int>((static_cast<uint32_t>(K) + T::K - 1) / T::K);
   for (; stages >= 2; stages -= 2) each<0, 2>(stage);
   if (stages > 0) stage(std::integral_constant<int, 0>{});
   const floatx16 sum = even + odd;

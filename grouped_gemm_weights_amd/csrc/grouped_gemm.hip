@@ -240,77 +240,115 @@ Order row_order(int64_t mt, int64_t nt, int64_t* blocks) {
   return o;
 }
 
-template <Kind KIND, int TR, typename O>
-int launch_rows(const Call& c, const void* x, const uint8_t* xs, void* y) {
-  int64_t n;
-  const Order o = row_order(max_tiles(c.ex.R, c.ex.E, TR), ceil_div(c.N, 256), &n);
-  const int bytes = c.K * value_bytes(KIND);
-  const int phases = bytes % 2048 == 0 ? bytes / 512 : 1;
-  return launch_tiles(c.who, row_kernel<KIND, TR, O>, n, row_tile_lds(KIND), c.s, c.ex, c.src,
-                      static_cast<const char*>(x), xs, c.w, c.K, c.N, o, phases, static_cast<O*>(y));
-}
-
-template <Kind KIND, typename O>
-int launch_split(const Call& c, const void* x, const uint8_t* xs, void* y) {
-  const int nb = ceil_div(c.N, 64);
-  return launch_tiles(c.who, split_kernel<KIND, O>, max_tiles(c.ex.R, c.ex.E, 64) * nb, SplitProduct<KIND, 2>::LDS, c.s,
-                      c.ex, c.src, static_cast<const char*>(x), xs, c.w, c.K, c.N, nb, static_cast<O*>(y));
-}
-
-// By how many tiles each kind would have (with one for every expert more than there can be):
+// What a forward product launches, by how many tiles each kind would have (with one for every expert more
+// than there can be):
 //   split  up to two a CU.  Measured, 4 experts, split against 64 x 256: bf16, 8 rows each of 4096 x 512
 //          9.9 / 34.8 us, 128 rows of 2048 x 2048 13.2 / 21.7 us, 256 rows (640 tiles) 21.4 / 22.0 us; 64 rows
 //          of 32 experts of 2112 x 2048 (2048 tiles) 72 / 54 us.
 //   64     up to one a CU.  Against 256 x 256: bf16, 1024 rows each of 4096 x 512 40 / 72 us, of 1024 x 768
 //          15 / 25 us; of 2048 x 2048 (544 tiles) 47 / 43 us.
-template <Kind KIND, typename O>
-int run_rows(const Call& c, const void* x, const uint8_t* xs, void* y) {
-  const int64_t small = max_tiles(c.ex.R, c.ex.E, 64);
-  if (small * ceil_div(c.N, 64) <= 2 * kCus) return launch_split<KIND, O>(c, x, xs, y);
-  if (small * ceil_div(c.N, 256) <= kCus) return launch_rows<KIND, 64, O>(c, x, xs, y);
-  return launch_rows<KIND, 256, O>(c, x, xs, y);
+struct RowPlan {
+  enum Tiles { kSplit, k64, k256 } tiles;
+  Order order;  // of all but split tiles
+  int64_t blocks;
+};
+
+RowPlan plan_rows(int R, int E, int N) {
+  const int64_t small = max_tiles(R, E, 64);
+  RowPlan p{RowPlan::kSplit, Order{}, small * ceil_div(N, 64)};
+  if (p.blocks <= 2 * kCus) return p;
+  p.tiles = small * ceil_div(N, 256) <= kCus ? RowPlan::k64 : RowPlan::k256;
+  p.order = row_order(p.tiles == RowPlan::k64 ? small : max_tiles(R, E, 256), ceil_div(N, 256), &p.blocks);
+  return p;
 }
 
-int run_f32(const Call& c, const void* x, void* y) {
-  const bool small = small_tiles_f32(max_tiles(c.ex.R, c.ex.E, 64) * ceil_div(c.N, 64));
-  const int tr = small ? 32 : 64, nb = ceil_div(c.N, tr);
-  hipLaunchKernelGGL(small ? product_f32_kernel<32> : product_f32_kernel<64>,
-                     dim3(static_cast<unsigned>(max_tiles(c.ex.R, c.ex.E, tr) * nb)), dim3(256), 0, c.s, c.ex, c.src,
-                     static_cast<const float*>(x), c.w, c.K, c.N, nb, static_cast<float*>(y));
+template <Kind KIND, int TR, typename O>
+int launch_rows(const Call& c, const RowPlan& p, const void* x, const uint8_t* xs, void* y) {
+  const int bytes = c.K * value_bytes(KIND);
+  const int phases = bytes % 2048 == 0 ? bytes / 512 : 1;
+  return launch_tiles(c.who, row_kernel<KIND, TR, O>, p.blocks, row_tile_lds(KIND), c.s, c.ex, c.src,
+                      static_cast<const char*>(x), xs, c.w, c.K, c.N, p.order, phases, static_cast<O*>(y));
+}
+
+template <Kind KIND, typename O>
+int run_rows(const Call& c, const RowPlan& p, const void* x, const uint8_t* xs, void* y) {
+  if (p.tiles == RowPlan::k256) return launch_rows<KIND, 256, O>(c, p, x, xs, y);
+  if (p.tiles == RowPlan::k64) return launch_rows<KIND, 64, O>(c, p, x, xs, y);
+  return launch_tiles(c.who, split_kernel<KIND, O>, p.blocks, SplitProduct<KIND, 2>::LDS, c.s, c.ex, c.src,
+                      static_cast<const char*>(x), xs, c.w, c.K, c.N, ceil_div(c.N, 64), static_cast<O*>(y));
+}
+
+// The same in f32: tiles of 64 x 64 or 32 x 32.
+struct F32Plan {
+  int tr;
+  int64_t blocks;
+};
+
+F32Plan plan_f32(int R, int E, int N) {
+  const int64_t large = max_tiles(R, E, 64) * ceil_div(N, 64);
+  if (small_tiles_f32(large)) return {32, max_tiles(R, E, 32) * ceil_div(N, 32)};
+  return {64, large};
+}
+
+int run_f32(const Call& c, const F32Plan& p, const void* x, void* y) {
+  hipLaunchKernelGGL(p.tr == 32 ? product_f32_kernel<32> : product_f32_kernel<64>, dim3(static_cast<unsigned>(p.blocks)),
+                     dim3(256), 0, c.s, c.ex, c.src, static_cast<const float*>(x), c.w, c.K, c.N, ceil_div(c.N, p.tr),
+                     static_cast<float*>(y));
   MOE_LAUNCH_CHECK(c.who);
   return MOE_OK;
 }
 
-template <int TR>
-int launch_grads(const Call& c, const void* x, const void* dy, void* dx, void* dw) {
-  GradRanges r{0, 1};
-  Order odx{}, odw{};
-  int64_t n, blocks = 0;
+// A launch of the gradients: dX, dW or both.
+struct GradPlan {
+  int dx, dw;  // tile sizes, 0 for what it leaves out (bf16: the same one where it has both)
+  GradRanges r;
+  Order odx, odw;  // bf16
+  int64_t blocks;
+};
+
+GradPlan plan_grads(int R, int E, int K, int N, int dx, int dw) {
+  GradPlan p{dx, dw, GradRanges{0, 1}, Order{}, Order{}, 0};
+  int64_t n;
   if (dx) {
-    odx = make_order(TR, max_tiles(c.ex.R, c.ex.E, TR), ceil_div(c.K, tile_columns(TR, false)), &n);
-    blocks = r.dx = n;
+    p.odx = make_order(dx, max_tiles(R, E, dx), ceil_div(K, dx), &n);
+    p.blocks = p.r.dx = n;
   }
   if (dw) {
-    odw = make_order(TR, ceil_div(c.N, TR), ceil_div(c.K, tile_columns(TR, false)), &n);
-    r.per = static_cast<int>(n);
-    blocks += c.ex.E * n;
+    p.odw = make_order(dw, ceil_div(N, dw), ceil_div(K, dw), &n);
+    p.r.per = static_cast<int>(n);
+    p.blocks += E * n;
   }
-  if (blocks == 0) return MOE_OK;
-  return launch_tiles(c.who, grads_kernel<TR>, blocks, tile_lds(TR, false), c.s, c.ex, static_cast<const uint16_t*>(x),
-                      static_cast<const uint16_t*>(dy), c.w, c.K, c.N, r, odx, odw, static_cast<uint16_t*>(dx),
+  return p;
+}
+
+GradPlan plan_grads_f32(int R, int E, int K, int N, bool dx, bool dw) {
+  const int64_t nk = ceil_div(K, 64);
+  const int tx = small_tiles_f32(max_tiles(R, E, 64) * nk) ? 32 : 64, tw = small_tiles_f32(E * nk * ceil_div(N, 64)) ? 32 : 64;
+  GradPlan p{tx, tw, GradRanges{0, 1}, Order{}, Order{}, 0};
+  p.r.dx = dx ? max_tiles(R, E, tx) * ceil_div(K, tx) : 0;
+  p.r.per = ceil_div(N, tw) * ceil_div(K, tw);
+  p.blocks = p.r.dx + (dw ? static_cast<int64_t>(E) * p.r.per : 0);
+  return p;
+}
+
+template <int TR>
+int launch_grads(const Call& c, const GradPlan& p, const void* x, const void* dy, void* dx, void* dw) {
+  return launch_tiles(c.who, grads_kernel<TR>, p.blocks, tile_lds(TR, false), c.s, c.ex, static_cast<const uint16_t*>(x),
+                      static_cast<const uint16_t*>(dy), c.w, c.K, c.N, p.r, p.odx, p.odw, static_cast<uint16_t*>(dx),
                       static_cast<char*>(dw));
 }
 
-template <int DX, int DW>
-int launch_grads_f32(const Call& c, const void* x, const void* dy, void* dx, void* dw) {
-  GradRanges r;
-  r.dx = dx ? max_tiles(c.ex.R, c.ex.E, DX) * ceil_div(c.K, DX) : 0;
-  r.per = ceil_div(c.N, DW) * ceil_div(c.K, DW);
-  const int64_t blocks = r.dx + (dw ? static_cast<int64_t>(c.ex.E) * r.per : 0);
-  if (blocks == 0) return MOE_OK;
-  hipLaunchKernelGGL((grads_f32_kernel<DX, DW>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, c.s, c.ex,
-                     static_cast<const float*>(x), static_cast<const float*>(dy), c.w, c.K, c.N, r,
-                     static_cast<float*>(dx), static_cast<char*>(dw));
+int run_grads(const Call& c, const GradPlan& p, const void* x, const void* dy, void* dx, void* dw) {
+  if (p.blocks == 0) return MOE_OK;
+  return std::max(p.dx, p.dw) == 256 ? launch_grads<256>(c, p, x, dy, dx, dw) : launch_grads<64>(c, p, x, dy, dx, dw);
+}
+
+int run_grads_f32(const Call& c, const GradPlan& p, const void* x, const void* dy, void* dx, void* dw) {
+  if (p.blocks == 0) return MOE_OK;
+  auto kernel = p.dx == 32 ? (p.dw == 32 ? grads_f32_kernel<32, 32> : grads_f32_kernel<32, 64>)
+                           : (p.dw == 32 ? grads_f32_kernel<64, 32> : grads_f32_kernel<64, 64>);
+  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(p.blocks)), dim3(256), 0, c.s, c.ex, static_cast<const float*>(x),
+                     static_cast<const float*>(dy), c.w, c.K, c.N, p.r, static_cast<float*>(dx), static_cast<char*>(dw));
   MOE_LAUNCH_CHECK(c.who);
   return MOE_OK;
 }
@@ -335,10 +373,13 @@ int check(const char* who, int R, int E, int K, int N, int unit, int bytes, cons
                 static_cast<long long>(w->expert_bytes), w->n_experts);
   if (x_rows * K * bytes >= (int64_t{1} << 31))
     return fail(MOE_ERR_UNSUPPORTED, "%s: a gathered x of 2^31 bytes or more", who);
-  // the largest launch: small tiles of the rows and of every expert's weight gradient
-  const int64_t side = std::max(ceil_div(K, 32), ceil_div(N, 32));
-  if (too_many((max_tiles(R, E, 16) + 8) * side + static_cast<int64_t>(E) * ceil_div(K, 32) * ceil_div(N, 32) + 24, 256))
-    return fail(MOE_ERR_UNSUPPORTED, "%s: R=%d rows of K=%d, N=%d are more than a launch takes", who, R, K, N);
+  return MOE_OK;
+}
+
+int check_blocks(const char* who, int64_t blocks) {
+  if (too_many(blocks, 256))
+    return fail(MOE_ERR_UNSUPPORTED, "%s: %lld workgroups are more than a launch takes", who,
+                static_cast<long long>(blocks));
   return MOE_OK;
 }
 
@@ -364,6 +405,10 @@ extern "C" int moe_grouped_gemm(const void* x, const int32_t* src_of, int top_k,
   if (rc) return rc;
   if (dtype == MOE_F32 && y_dtype != MOE_F32)
     return fail(MOE_ERR_UNSUPPORTED, "%s: f32 products have f32 outputs", who);
+  const F32Plan f32 = plan_f32(R, E, N);
+  const RowPlan rows = plan_rows(R, E, N);
+  rc = check_blocks(who, dtype == MOE_F32 ? f32.blocks : rows.blocks);
+  if (rc) return rc;
   rc = check_aligned(who, bits(x) | bits(w->base) | bits(y) | static_cast<uintptr_t>(w->expert_bytes | w_off),
                      dtype == MOE_F32 ? 4 : 16);
   if (rc) return rc;
@@ -372,9 +417,9 @@ extern "C" int moe_grouped_gemm(const void* x, const int32_t* src_of, int top_k,
   hipStream_t s = as_stream(stream);
   const Call c{who, Experts{offsets, w->slot_of, R, E, w->n_slots, status}, Source{src_of, top_k, static_cast<int>(x_rows)},
                Weights{static_cast<const char*>(w->base), w->expert_bytes, w_off, 0}, K, N, s};
-  rc = dtype == MOE_F32 ? run_f32(c, x, y)
-                        : y_dtype == MOE_F32 ? run_rows<Kind::kBf16, float>(c, x, nullptr, y)
-                                           : run_rows<Kind::kBf16, uint16_t>(c, x, nullptr, y);
+  rc = dtype == MOE_F32 ? run_f32(c, f32, x, y)
+                        : y_dtype == MOE_F32 ? run_rows<Kind::kBf16, float>(c, rows, x, nullptr, y)
+                                           : run_rows<Kind::kBf16, uint16_t>(c, rows, x, nullptr, y);
   return debug_check(rc, who, s, status);
 }
 
@@ -391,6 +436,9 @@ extern "C" int moe_grouped_gemm_mx(const uint8_t* x, const uint8_t* x_scales, co
   if (s_off < 0 || w->expert_bytes < scales || s_off > w->expert_bytes - scales)
     return fail(MOE_ERR_ARG, "%s: %lld bytes of scales at %lld do not lie in the merged buffer's %lld-byte blocks", who,
                 static_cast<long long>(scales), static_cast<long long>(s_off), static_cast<long long>(w->expert_bytes));
+  const RowPlan rows = plan_rows(R, E, N);
+  rc = check_blocks(who, rows.blocks);
+  if (rc) return rc;
   rc = check_aligned(who, bits(x) | bits(x_scales) | bits(w->base) | bits(y) |
                               static_cast<uintptr_t>(w->expert_bytes | w_off | s_off), 16);
   if (rc) return rc;
@@ -399,8 +447,8 @@ extern "C" int moe_grouped_gemm_mx(const uint8_t* x, const uint8_t* x_scales, co
   hipStream_t s = as_stream(stream);
   const Call c{who, Experts{offsets, w->slot_of, R, E, w->n_slots, status}, Source{src_of, top_k, static_cast<int>(x_rows)},
                Weights{static_cast<const char*>(w->base), w->expert_bytes, w_off, s_off}, K, N, s};
-  rc = y_dtype == MOE_F32 ? run_rows<Kind::kMxExact, float>(c, x, x_scales, y)
-                          : run_rows<Kind::kMx, uint16_t>(c, x, x_scales, y);
+  rc = y_dtype == MOE_F32 ? run_rows<Kind::kMxExact, float>(c, rows, x, x_scales, y)
+                          : run_rows<Kind::kMx, uint16_t>(c, rows, x, x_scales, y);
   return debug_check(rc, who, s, status);
 }
 
@@ -413,21 +461,10 @@ extern "C" int moe_grouped_gemm_backward(const void* x, const void* dy, const in
   int rc = check(who, R, E, K, N, dtype == MOE_F32 ? 1 : 8, elem_size(dtype), w, w_off, offsets, 0);
   if (rc) return rc;
   if (!dx && !dw) return fail(MOE_ERR_ARG, "%s: null pointer", who);
-  rc = check_aligned(who, bits(x) | bits(dy) | bits(w->base) | bits(dx) | bits(dw) |
-                              static_cast<uintptr_t>(w->expert_bytes | w_off), dtype == MOE_F32 ? 4 : 16);
-  if (rc) return rc;
-  if (R > 0 && (!x || !dy)) return fail(MOE_ERR_ARG, "%s: null pointer", who);
-  hipStream_t s = as_stream(stream);
-  const Call c{who, Experts{offsets, w->slot_of, R, E, w->n_slots, status}, Source{},
-               Weights{static_cast<const char*>(w->base), w->expert_bytes, w_off, 0}, K, N, s};
-  if (R == 0) dx = nullptr;
+  const bool has_dx = dx && R > 0, has_dw = dw;
+  GradPlan first, second{};
   if (dtype == MOE_F32) {
-    const int64_t nk = ceil_div(K, 64);
-    const bool small_dx = small_tiles_f32(max_tiles(R, E, 64) * nk);
-    const bool small_dw = small_tiles_f32(E * nk * ceil_div(N, 64));
-    auto launch = small_dx ? (small_dw ? launch_grads_f32<32, 32> : launch_grads_f32<32, 64>)
-                           : (small_dw ? launch_grads_f32<64, 32> : launch_grads_f32<64, 64>);
-    rc = launch(c, x, dy, dx, dw);
+    first = plan_grads_f32(R, E, K, N, has_dx, has_dw);
   } else {
     // Large tiles for dX when it has one for every CU; for dW when it has one for every other CU, or every
     // fourth beside large tiles of dX.  Where the two differ they are launches of their own.  Measured
@@ -435,15 +472,27 @@ extern "C" int moe_grouped_gemm_backward(const void* x, const void* dy, const in
     // of 2048 x 2048 (512 tiles) 61 / 51 us, 1373 rows each of 12 of 88 x 3024 (144) 138 / 130 us, 12 rows
     // each of 23 of 88 x 1168 (115) 13.8 / 20.6 us; beside large dX 4096 rows each of 8 of 512 x 1024 (64)
     // 167 / 200 us, 65536 rows of 512 x 512 (4) 1091 / 338 us.
-    const bool large_dx = max_tiles(R, E, 256) * ceil_div(K, 256) >= kCus;
-    const bool large_dw =
-        static_cast<int64_t>(E) * ceil_div(N, 256) * ceil_div(K, 256) >= (dx && large_dx ? kCus / 4 : kCus / 2);
-    if (dx && dw && large_dx != large_dw) {
-      rc = large_dx ? launch_grads<256>(c, x, dy, dx, nullptr) : launch_grads<64>(c, x, dy, dx, nullptr);
-      if (rc) return rc;
-      dx = nullptr;
-    }
-    rc = (dx ? large_dx : large_dw) ? launch_grads<256>(c, x, dy, dx, dw) : launch_grads<64>(c, x, dy, dx, dw);
+    const bool large_dx = has_dx && max_tiles(R, E, 256) * ceil_div(K, 256) >= kCus;
+    const bool large_dw = static_cast<int64_t>(E) * ceil_div(N, 256) * ceil_div(K, 256) >= (large_dx ? kCus / 4 : kCus / 2);
+    const int tx = has_dx ? (large_dx ? 256 : 64) : 0, tw = has_dw ? (large_dw ? 256 : 64) : 0;
+    const bool apart = tx && tw && tx != tw;
+    first = plan_grads(R, E, K, N, tx, apart ? 0 : tw);
+    if (apart) second = plan_grads(R, E, K, N, 0, tw);
+  }
+  rc = check_blocks(who, std::max(first.blocks, second.blocks));
+  if (rc) return rc;
+  rc = check_aligned(who, bits(x) | bits(dy) | bits(w->base) | bits(dx) | bits(dw) |
+                              static_cast<uintptr_t>(w->expert_bytes | w_off), dtype == MOE_F32 ? 4 : 16);
+  if (rc) return rc;
+  if (R > 0 && (!x || !dy)) return fail(MOE_ERR_ARG, "%s: null pointer", who);
+  hipStream_t s = as_stream(stream);
+  const Call c{who, Experts{offsets, w->slot_of, R, E, w->n_slots, status}, Source{},
+               Weights{static_cast<const char*>(w->base), w->expert_bytes, w_off, 0}, K, N, s};
+  if (dtype == MOE_F32) {
+    rc = run_grads_f32(c, first, x, dy, dx, dw);
+  } else {
+    rc = run_grads(c, first, x, dy, dx, dw);
+    if (!rc) rc = run_grads(c, second, x, dy, dx, dw);
   }
   return debug_check(rc, who, s, status);
 }

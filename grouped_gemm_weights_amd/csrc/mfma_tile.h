@@ -309,7 +309,7 @@ struct TileProduct {
 #pragma unroll
     for (int t = 0; t < NRD; ++t) read(pa, pb, t, 0, 0);
     __builtin_amdgcn_sched_barrier(0);
-    int stages = (K + kStageK - 1) / kStageK;
+    int stages = static_cast<int>((static_cast<uint32_t>(K) + kStageK - 1) / kStageK);
     for (; stages >= STAGES; stages -= STAGES) {
       stage<0>();
       stage<1>();
