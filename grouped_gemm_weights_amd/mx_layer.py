@@ -29,6 +29,9 @@ class MxMoELayer:
     Set ``x`` and ``residual`` ([T, H] in the layer's dtype), ``gamma`` (f32 [H]) and, after ``norm``,
     ``logits`` (f32 [T, E]); ``forward`` leaves the block's output in ``y`` (f32) and the new stream
     in ``out``.
+
+    Experts are filled by ``load_expert``, by a pull into ``wbuf``, or by the caller in ``blocks``.  One
+    that never was holds NaN, and so does the output of every token that is routed to it.
     """
 
     def __init__(self, cfg: MoEConfig, device="cuda", compute_stream=None, eps: float = 1e-6):
@@ -60,7 +63,8 @@ class MxMoELayer:
         self.up_scales_off = self.down_off + H * I
         self.down_scales_off = self.up_scales_off + 2 * I * B.moe_mx_scale_pitch(H)
         self.expert_bytes = self.down_scales_off + H * B.moe_mx_scale_pitch(I)
-        self.blocks = u8(E, self.expert_bytes)
+        # 0x7f is e4m3's NaN, with the scale 2^0: an expert that nobody filled does not pass for weights
+        self.blocks = u8(E, self.expert_bytes).fill_(0x7F)
         self.slot_of = torch.arange(E, dtype=torch.int32, device=d)
         self.wbuf = B.wbuf(self.blocks, self.expert_bytes, E, E, self.slot_of)
         self.compute_stream = compute_stream or torch.cuda.Stream(device=d)

@@ -127,3 +127,30 @@ def test_refusals():
     for e, bad in ((2, block), (-1, block), (0, block[:-1]), (0, block.float()), (0, block.cpu())):
         with pytest.raises(ValueError):
             L.load_expert(e, bad)
+
+
+def test_experts_that_nobody_loaded():
+    """Their tokens come out NaN, all others as with every expert loaded; a pull into their slots mends them."""
+    from grouped_gemm_weights_amd import binding as B
+    from grouped_gemm_weights_amd.mx_layer import MxMoELayer
+    T, H, I, E, k, missing = 60, 96, 64, 6, 2, (1, 4)
+    cfg, full, rng = layer(T, H, I, E, k, "bf16", 10)
+    inputs(full, rng, "bf16")
+    part = MxMoELayer(cfg)
+    part.blocks[[e for e in range(E) if e not in missing]] = full.blocks[[e for e in range(E) if e not in missing]]
+    for name in ("x", "residual", "gamma", "logits"):
+        getattr(part, name).copy_(getattr(full, name))
+    torch.cuda.synchronize()
+    for L in (full, part):
+        L.norm()
+        L.forward()
+        assert L.read_status() == 0
+    idx = full.topk_idx.cpu().numpy()
+    hit = torch.from_numpy(np.isin(idx, missing).any(1)).cuda()
+    assert 0 < int(hit.sum()) < T
+    assert torch.isfinite(full.y).all() and torch.isnan(part.y[hit]).all() and torch.isnan(part.out[hit]).all()
+    assert torch.equal(part.y[~hit], full.y[~hit]) and torch.equal(part.out[~hit], full.out[~hit])
+    B.moe_prefetch_routed(B.pool(full.blocks, full.expert_bytes, 0, E), part.counts, part.wbuf, part.compute_stream)
+    part.forward()
+    assert part.read_status() == 0
+    assert torch.equal(part.y, full.y) and torch.equal(part.out, full.out)
