@@ -364,9 +364,12 @@ int launch_rms(const E* x, const E* res, const float* gamma, int T, int H, float
   const int64_t blocks = keep ? most : all;
   if (too_many(blocks, waves * rows * kWave))
     return fail(MOE_ERR_UNSUPPORTED, "moe_rms_norm: T=%d too large at H=%d", T, H);
+  // Up to 2 * most blocks hold at most 512 * 16 waves of 512 NV elements: with NV <= 2 that is 32 MB, so
+  // larger arrays are all KEEP
+  constexpr bool always = NV <= 2 && CACHE != kNear, never = NV > 2;
   auto kernel = H % kVec == 0
-                    ? (keep ? rms_kernel<E, NV, NV <= 2, false, RES, CACHE> : rms_kernel<E, NV, false, false, RES, CACHE>)
-                    : (keep ? rms_kernel<E, NV, NV <= 2, true, RES, CACHE> : rms_kernel<E, NV, false, true, RES, CACHE>);
+                    ? (keep ? rms_kernel<E, NV, !never, false, RES, CACHE> : rms_kernel<E, NV, always, false, RES, CACHE>)
+                    : (keep ? rms_kernel<E, NV, !never, true, RES, CACHE> : rms_kernel<E, NV, always, true, RES, CACHE>);
   hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(blocks)), dim3(waves * rows * kWave), 0, s, x, res,
                      gamma, T, H, waves, eps, out);
   MOE_LAUNCH_CHECK("moe_rms_norm: launch");
