@@ -38,7 +38,10 @@ struct Tile {
 // experts without a slot in the merged buffer (a slot outside it is treated as absent, never
 // read; `report`: their status bit is set).  False past the last tile.  Wave-uniform.
 // LARGE_FIRST: tiles of more than TR / 2 rows come before the others, so that what the last CUs wait
-// for is a small one.
+// for is a small one.  Measured, expert by expert / large first: bf16, 4096 tokens x 6 on 64 skewed experts
+// of 1408 x 2048 179 / 172 us, with the gradients 580 / 569; 2048 x 6 on 64 of 2048 x 1408 132 / 131; with less
+// skew it costs up to 4 %: 1024 x 8 on 32 of 4096 x 2048 180 / 186, 8 bits, 8192 x 8 on 32 of 7168 x 4096
+// 1543 / 1567.
 template <int TR, bool LARGE_FIRST = false>
 __device__ __forceinline__ bool find_tile(const Experts& x, int m, bool report, Tile* t) {
   const int lane = threadIdx.x & (kWave - 1);

@@ -110,7 +110,8 @@ __device__ __forceinline__ void row_tile(const Tile& t, int n0, const Source& sr
 // depth would ask few of the memory channels; the tiles of a unit go together, since they read the same
 // rows.  Measured at 32 experts of 2048 columns, the same start against these: 8 rows each, bf16, depth
 // 2048 65.8 / 48.3 us, 4096 129 / 101 us; 128 rows each, bf16, 2048 70 / 56 us, 4096 131 / 102 us, 8 bits,
-// 4096 74 / 60 us; 2048 rows each of 8 experts of 4096 x 4096 428 / 427 us.
+// 4096 74 / 60 us; 2048 rows each of 8 experts of 4096 x 4096 428 / 427 us.  (A start of its own for every
+// tile took 57 and 93 us at 8 rows, and 470 at 2048.)
 template <Kind KIND, int TR, typename O>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void row_kernel(
     Experts ex, Source src, const char* __restrict__ x, const uint8_t* __restrict__ xs, Weights w, int K, int N,
@@ -471,7 +472,7 @@ extern "C" int moe_grouped_gemm_backward(const void* x, const void* dy, const in
     // (both gradients and the forward product), dW in dX's size against its own: 32 rows each of 8 experts
     // of 2048 x 2048 (512 tiles) 61 / 51 us, 1373 rows each of 12 of 88 x 3024 (144) 138 / 130 us, 12 rows
     // each of 23 of 88 x 1168 (115) 13.8 / 20.6 us; beside large dX 4096 rows each of 8 of 512 x 1024 (64)
-    // 167 / 200 us, 65536 rows of 512 x 512 (4) 1091 / 338 us.
+    // 167 / 200 us, 65536 rows of 512 x 512 (4) 1091 / 332 us.
     const bool large_dx = has_dx && max_tiles(R, E, 256) * ceil_div(K, 256) >= kCus;
     const bool large_dw = static_cast<int64_t>(E) * ceil_div(N, 256) * ceil_div(K, 256) >= (large_dx ? kCus / 4 : kCus / 2);
     const int tx = has_dx ? (large_dx ? 256 : 64) : 0, tw = has_dw ? (large_dw ? 256 : 64) : 0;

@@ -1,6 +1,7 @@
 // A bf16 product of one workgroup: C[m][n] = sum_k A(m, k) B(k, n) into fp32 accumulators, for
 // operands whose rows run along the depth ("row" operands) or across it ("column" operands, read
-// transposed).  Used by the grouped SwiGLU's gradient, whose products need both.
+// transposed).  Used by the gradients of the grouped SwiGLU and of the products by expert, which need both;
+// row_tile.h builds its loop for row operands on the shapes, copies and epilogues here.
 //
 // Two tile sizes, four waves each:
 //   256 x 256  one wave per SIMD with a 128 x 128 quarter in 256 accumulators (4 x 4 MFMAs of

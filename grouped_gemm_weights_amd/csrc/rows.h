@@ -1,6 +1,6 @@
-// Row access shared by the bandwidth-bound kernels (layer norm, combine and permute
-// gradients): eight consecutive elements of a row per lane, converted to fp32, at whatever
-// alignment the row has.
+// Row access shared by the bandwidth-bound kernels (layer norm, RMS norm, rows to 8 bits, dropout,
+// combine and permute gradients): eight consecutive elements of a row per lane, converted to fp32, at
+// whatever alignment the row has; scans and sums over a wave and a block.
 #pragma once
 
 #include "common.h"

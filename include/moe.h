@@ -508,10 +508,11 @@ int moe_clear_unmapped(const moe_wbuf* w, void* dw, moe_stream_t stream);
  *   moe_mx_quantize      with swiglu -> q and scales [R][I]
  *   moe_grouped_gemm_mx  down -> y_perm f32
  *   moe_combine
- * Statistics and sums are f32, outputs are rounded once, no call uses atomics on its outputs and the
- * same inputs give the same bits.  Every call only enqueues and may be captured into a HIP graph;
- * captured calls that may run at the same time need workspaces of their own.  Unless a call says
- * otherwise, outputs must not overlap inputs.  Sizes whose launch would pass 2^32 threads are
+ * Statistics and sums are f32 (of moe_grouped_gemm_mx with bf16 outputs see there), outputs are rounded
+ * once, no call uses atomics on its outputs and the same inputs give the same bits.  Every call only
+ * enqueues and may be captured into a HIP graph; captured calls that may run at the same time need
+ * workspaces of their own.  Unless a call says otherwise, outputs must not overlap inputs.  Sizes whose
+ * launch would pass 2^32 threads are
  * MOE_ERR_UNSUPPORTED.
  */
 
@@ -611,7 +612,10 @@ int moe_grouped_gemm_backward(const void* x, const void* dy, const int32_t* offs
  * of exact products: the values are expanded to bf16, which holds them (with scales below 2^-124 to the
  * nearest of its subnormals; values from 2^128 on are infinite).  bf16 outputs come from the 8-bit MFMA,
  * twice as fast at many rows, which adds eight consecutive products at once, each cut below 2^-13 of the
- * largest: in the 2-norm about 3e-5 of the result, a sixtieth of what bf16's rounding makes.
+ * largest: in the 2-norm about 3e-5 of the result, a sixtieth of what bf16's rounding makes.  The cut is at
+ * most 7 * 2^-13 of the sum over those eights of their largest |product|, whatever the products add up to:
+ * an output whose products cancel can be off by more than its own rounding.  Of random values 1.2 % come
+ * out as the neighbour of the nearest bf16 number.  Where that matters, take f32 outputs.
  *   x, x_scales device, 8-bit rows of K ([R], or with src_of [ceil(R / top_k)])
  *   other arguments as moe_grouped_gemm
  * Errors: as moe_grouped_gemm; MOE_ERR_UNSUPPORTED for K not a multiple of 32 or N not one of 8, or

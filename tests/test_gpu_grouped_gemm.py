@@ -133,7 +133,8 @@ class Case:
             check(f"y of expert {e} ({ref.shape[0]} rows)", self.y[rows], ref, HALF[self.out] * (np.abs(ref) + f32) + f32)
 
 
-# rows by expert: decode tiles of 16, 32 and 64 rows, and every mode of the 256-row tile
+# rows by expert: tiles of 1 to 64 rows.  These products are small enough for the 64 x 64 tiles whose depth
+# is split over the waves; test_gpu_grouped_gemm_tiles has those of 64 x 256 and of 256 x 256
 FEW = [(1,), (3, 0, 5), (1, 2, 0, 16, 17), (15, 33, 16, 20), (64, 40, 33, 65, 0, 1)]
 MANY = [(300,), (33, 0, 400, 1), (64, 65, 255, 257), (191, 193, 128, 129, 31), (512, 5, 96, 160)]
 SHAPES_MX = [(32, 8), (64, 72), (96, 264), (416, 136), (544, 520), (1024, 256), (1120, 24)]
