@@ -72,7 +72,8 @@ class MxMoELayer:
 
     def load_expert(self, e: int, block: torch.Tensor) -> None:
         """Compute stream: expert e's weights to 8 bits, from its block [3 * H * I] (Wg | Wu | Wd) in the
-        layer's dtype on the device, written on torch's current stream."""
+        layer's dtype on the device, written on torch's current stream, which may write the next one to the
+        same place after this call."""
         cfg, cs = self.cfg, self.compute_stream
         if not 0 <= e < cfg.E:
             raise ValueError(f"expert {e} outside [0, {cfg.E})")
@@ -80,12 +81,14 @@ class MxMoELayer:
                 block.device != self.x.device:
             raise ValueError(f"an expert's block is {3 * cfg.H * cfg.I} contiguous {self.x.dtype} values on "
                              f"{self.x.device}")
-        cs.wait_stream(torch.cuda.current_stream(self.dev))
+        current = torch.cuda.current_stream(self.dev)
+        cs.wait_stream(current)
         block.record_stream(cs)
         at, src = self.blocks[e].data_ptr(), block.data_ptr()
         B.moe_mx_quantize(src, 2 * cfg.I, cfg.H, self.dt, 0, at, at + self.up_scales_off, cs)
         B.moe_mx_quantize(src + 2 * cfg.I * cfg.H * block.element_size(), cfg.H, cfg.I, self.dt, 0,
                           at + self.down_off, at + self.down_scales_off, cs)
+        current.wait_stream(cs)
 
     def norm(self) -> None:
         """Compute stream: ``sum`` = x + residual, ``xn`` its norm, and the same in 8 bits."""

@@ -154,3 +154,29 @@ def test_experts_that_nobody_loaded():
     part.forward()
     assert part.read_status() == 0
     assert torch.equal(part.y, full.y) and torch.equal(part.out, full.out)
+
+
+def test_experts_loaded_through_one_buffer():
+    """The caller's next write to the block waits until the compute stream, busy with other work, has read it."""
+    from grouped_gemm_weights_amd.mx_layer import MxMoELayer
+    H, I, E = 256, 192, 5
+    cfg = synth.MoEConfig("mx", T=8, H=H, I=I, E=E, k=2, dtype="bf16", n_local=E, seed=11)
+    one, each = MxMoELayer(cfg), MxMoELayer(cfg)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(11)
+    weights = [torch.randn(3 * H * I, generator=g, device="cuda").to(torch.bfloat16) for _ in range(E)]
+    busy, out = torch.randn(4096, 4096, device="cuda"), torch.empty(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    for e in range(E):
+        each.load_expert(e, weights[e])
+        torch.cuda.synchronize()
+    block = torch.empty(3 * H * I, dtype=torch.bfloat16, device="cuda")
+    for e in range(E):
+        with torch.cuda.stream(one.compute_stream):
+            for _ in range(3):
+                torch.mm(busy, busy, out=out)
+        block.copy_(weights[e])
+        one.load_expert(e, block)
+    block.fill_(float("nan"))
+    torch.cuda.synchronize()
+    assert torch.equal(one.blocks, each.blocks)
