@@ -494,7 +494,8 @@ int moe_clear_unmapped(const moe_wbuf* w, void* dw, moe_stream_t stream);
  * The block in 8 bits, products by expert, and what stands around the block.
  *
  * 8-bit rows ("mx") are the OCP microscaling format MXFP8 with e4m3 elements: 32 consecutive values
- * of a row share a scale 2^s, kept as the byte s + 127, and are held as e4m3(v / 2^s).  A matrix of
+ * of a row share a scale 2^s, kept as the byte s + 127 (255: the block is NaN), and are held as
+ * e4m3(v / 2^s).  A matrix of
  * rows x cols is
  *   q       uint8 [rows][cols], cols a multiple of 32
  *   scales  uint8 [rows][pitch], pitch = moe_mx_scale_pitch(cols) = 16 * ceil(cols / 512): the bytes

@@ -1,5 +1,5 @@
 """8-bit products whose scales are the smallest there are, bytes 0 to 3 (2^-127 to 2^-124), in rows or in
-weights, against float64.
+weights, against float64; and what the largest bytes give.
 
 With f32 outputs the values are expanded to bf16, whose subnormals have steps of 2^-133: with scale byte b an
 element, a multiple of 2^(b - 136), is off by at most half a step where b < 3, and exact from 3 on.
@@ -46,3 +46,27 @@ def test_product(counts, N, low, side, out):
         if out == "bf16":
             f32 = f32 + 7 * 2.0 ** -13 * largest_of_eight(x, w)
         near(f"y of expert {e}", y[at], ref, HALF[out] * (ref.abs() + f32) + f32)
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("counts,N", [((5, 40), 72), ((300, 77, 200), 2056)])
+def test_the_largest_bytes(counts, N, out):
+    """254 is 2^127 and 255 NaN, also of a block of zeros, for its row alone."""
+    off, K = [0], 64
+    for c in counts:
+        off.append(off[-1] + c)
+    o = Operands("mx", off[-1], K, N, len(counts), 1)
+    o.x.fill_(0x38)                                                     # ones
+    o.xs[:, :2] = 127
+    o.w[:, :N * K] = 0x38
+    for e in range(len(counts)):
+        o.w[e, N * K:].view(N, -1)[:, :2] = 127
+    o.x[1, 1:32], o.xs[1, 0] = 0, 254                                   # 2^127 once
+    o.xs[2, 1] = 255
+    o.x[3, :32], o.xs[3, 0] = 0, 255
+    y = torch.zeros(off[-1], N, dtype=TORCH[out], device="cuda")
+    o.product(i32(off), o.buffer(range(len(counts))), out, y)
+    assert bool((y[1].double() == 2.0 ** 127).all())
+    assert torch.isnan(y[2]).all() and torch.isnan(y[3]).all()
+    rest = [r for r in range(off[-1]) if r not in (1, 2, 3)]
+    assert bool((y[rest] == 64).all())
